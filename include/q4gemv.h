@@ -488,6 +488,140 @@ Q4_API q4_status q4_0_gemm_prefill_batch_plan(const q4_gemv_desc* descs, int cou
  * q4_0_gemm_prefill call uses, so the results are the same bit for bit). */
 Q4_API q4_status q4_0_gemm_prefill_batch(const q4_prefill_plan* plan, void* stream);
 
+/*
+ * The operators between a layer's q/k/v products and its o product: rotary
+ * positions, the paged key/value cache and attention over it.
+ *
+ * Element types of their tensors. */
+#define Q4_TYPE_F16 0  /* IEEE binary16 */
+#define Q4_TYPE_BF16 1 /* bfloat16 */
+#define Q4_TYPE_F32 2  /* IEEE binary32 */
+
+/* Which two elements of a head a rotary angle turns (r = rotated elements). */
+#define Q4_ROPE_HALF 0        /* i and i + r/2 */
+#define Q4_ROPE_INTERLEAVED 1 /* 2i and 2i + 1 */
+
+/* Heads of a list of tokens: element d of head h of token t at
+ * data[t * token_stride + h * head_stride + d] (strides in elements, >= 0), for
+ * instance a part of the packed output of the q/k/v products. */
+typedef struct q4_heads {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+    int type; /* Q4_TYPE_* */
+} q4_heads;
+
+/* A paged key/value cache: element d of kv head h in slot s of page p at
+ * k[p * k_page_stride + h * k_head_stride + s * k_slot_stride + d], v alike
+ * (strides in elements).  Which pages a sequence holds is in its row of
+ * q4_kv_batch's block table. */
+typedef struct q4_kv_cache {
+    void* k;
+    void* v;
+    int64_t k_page_stride, k_head_stride, k_slot_stride;
+    int64_t v_page_stride, v_head_stride, v_slot_stride;
+    int64_t pages;  /* pages of the cache, >= 1 */
+    int page_size;  /* tokens of a page: a multiple of 8, 8 .. 65536 */
+    int kv_heads;   /* >= 1 */
+    int head_dim;   /* elements of a head, keys' and values' */
+    int type;       /* Q4_TYPE_F16 or Q4_TYPE_BF16 */
+} q4_kv_cache;
+
+/* The sequences of one call.  Sequence b's new tokens are the rows
+ * query_start[b] .. query_start[b + 1) of the call's token tensors; they are
+ * the last of its context_len[b] tokens, so new token i (of n) has position
+ * context_len[b] - n + i.  Position p lives in slot p % page_size of the page
+ * block_table[b * table_stride + p / page_size].  All three arrays are int32 in
+ * DEVICE memory (so a captured graph sees the lengths of each replay):
+ * query_start has seqs + 1 entries and does not fall, context_len has seqs.
+ * Rows outside [query_start[0], query_start[seqs]) are left as they are.
+ * A position below 0, beyond the table, or in a page whose index is outside
+ * [0, pages) (say -1 for a page given back) has no place: it is not written
+ * and no query sees it. */
+typedef struct q4_kv_batch {
+    const int32_t* block_table;
+    int64_t table_stride; /* int32 entries from one sequence's row to the next */
+    int table_pages;      /* entries of a row, >= 1 */
+    int seqs;             /* >= 1 */
+    const int32_t* query_start;
+    const int32_t* context_len;
+    int max_query;   /* most new tokens of a sequence, 0 if not known: chooses */
+    int max_context; /* longest context, 0 if not known: the kernel, not the result */
+} q4_kv_batch;
+
+/*
+ * Rotary positions: pair i of each head turns by the angle
+ * positions[t] * inv_freq[i],
+ *   (a, b) -> mscale * (a cos - b sin, a sin + b cos),
+ * and elements from rot_dim on are copied.
+ *   x, out    : tokens x heads x head_dim; out (written) may be x itself (the
+ *               same data, strides and type) but not overlap it otherwise
+ *   positions : tokens int32 (negative ones turn back, which is also the
+ *               gradient), 4-byte aligned
+ *   inv_freq  : rot_dim / 2 binary64 values, 8-byte aligned: the frequencies,
+ *               with any scaling for long contexts in them
+ *   tokens >= 1, heads >= 1, 2 <= rot_dim <= head_dim <= 1024, rot_dim even
+ * Angles are reduced in binary64, so far positions keep their precision; the
+ * rotation is in binary32 and each element is rounded once.  Any strides and
+ * alignments of the elements' own size; 16-byte aligned heads with
+ * rot_dim % 16 == 0 (half) or rot_dim % 8 == 0 (interleaved) and head_dim % 8
+ * == 0 take the fast path.
+ */
+Q4_API q4_status q4_rope(const q4_heads* x, const q4_heads* out, const int32_t* positions, const double* inv_freq,
+                         int64_t tokens, int heads, int head_dim, int rot_dim, int layout, float mscale,
+                         void* stream);
+
+/*
+ * Append the new tokens' keys and values to the cache, the keys (and the
+ * queries, if given) rotated on the way as in q4_rope by the angle of each
+ * token's position.
+ *   k, v      : tokens x kv_heads x head_dim
+ *   q, q_out  : NULL, or tokens x q_heads x head_dim; q_out (of the cache's
+ *               type, written) may be q itself
+ *   positions : NULL (the positions in the cache), or tokens int32 that give
+ *               the angles instead
+ *   inv_freq  : NULL with rot_dim == 0 (no rotation), else as in q4_rope
+ * Each element is rounded once to the cache's type.  Slots that no new token
+ * has are left as they are; a slot that two tokens share holds one of them.
+ */
+Q4_API q4_status q4_kv_append(const q4_kv_cache* cache, const q4_kv_batch* batch, const q4_heads* k,
+                              const q4_heads* v, const q4_heads* q, const q4_heads* q_out, int q_heads,
+                              int64_t tokens, const int32_t* positions, const double* inv_freq, int rot_dim,
+                              int layout, float mscale, void* stream);
+
+/* Bytes of device workspace q4_attention_paged needs (0, with the error text
+ * set, if the arguments are not valid). */
+Q4_API size_t q4_attention_paged_workspace_bytes(const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads,
+                                                 int64_t tokens);
+
+/*
+ * out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j  over the cached keys j
+ * of t's sequence with j <= position(t) and, with window > 0, j > position(t)
+ * - window; query head h reads kv head h / (q_heads / kv_heads).  The new
+ * tokens' keys and values are in the cache already (q4_kv_append).  One new
+ * token a sequence is a decode step, a few are the verify of a draft, many a
+ * prompt or a chunk of it.
+ *   q, out : tokens x q_heads x head_dim of the cache's type, 16-byte aligned,
+ *            strides multiples of 8; out is written and overlaps nothing else
+ *   lse    : NULL, or tokens x q_heads binary32 (written): the natural log of
+ *            the sum of exp(scale * q . k_j)
+ *   scale  : finite, > 0;  window >= 0 (0: no window)
+ *   workspace : q4_attention_paged_workspace_bytes(...) bytes of device memory,
+ *            16-byte aligned; its contents on entry do not matter.  Calls that
+ *            may overlap in time need one each.
+ *   head_dim 64, 96, 128 or 256; q_heads a multiple of kv_heads; the cache
+ *   16-byte aligned with strides that are multiples of 8.
+ * A row that sees no key is 0 (lse -infinity).  Slots beyond a context, pages
+ * without a place and keys a row does not see leave it unaffected whatever they
+ * hold.  Scores, softmax statistics and sums are binary32; the probabilities
+ * are rounded to the cache's type for the product with the values, and their
+ * sum is taken over the rounded ones; the output is rounded once.
+ * Deterministic for the same arguments, lengths and device.
+ */
+Q4_API q4_status q4_attention_paged(const q4_kv_cache* cache, const q4_kv_batch* batch, const q4_heads* q,
+                                    const q4_heads* out, float* lse, int q_heads, int64_t tokens, float scale,
+                                    int64_t window, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

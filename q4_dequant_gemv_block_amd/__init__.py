@@ -14,6 +14,7 @@ weight = (code - 8) * scale); activations are float16; outputs float32.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -44,7 +45,16 @@ EXPORTS = (
     "q4_0_gemm_smallm_batch_plan_bytes", "q4_0_gemm_smallm_batch_plan", "q4_0_gemm_smallm_batch",
     "q4_0_gemm_prefill_batch_plan_bytes", "q4_0_gemm_prefill_batch_plan", "q4_0_gemm_prefill_batch",
     "q4_0_gemv_batch", "q4_0_gemv_batch_handoff",
+    "q4_rope", "q4_kv_append", "q4_attention_paged_workspace_bytes", "q4_attention_paged",
 )
+
+Q4_TYPE_F16 = 0
+Q4_TYPE_BF16 = 1
+Q4_TYPE_F32 = 2
+Q4_ROPE_HALF = 0
+Q4_ROPE_INTERLEAVED = 1
+_TYPES = {torch.float16: Q4_TYPE_F16, torch.bfloat16: Q4_TYPE_BF16, torch.float32: Q4_TYPE_F32}
+_LAYOUTS = {"half": Q4_ROPE_HALF, "interleaved": Q4_ROPE_INTERLEAVED}
 
 
 class Q4Error(RuntimeError):
@@ -67,6 +77,25 @@ class Q8Plan(ctypes.Structure):
     _fields_ = [("device", ctypes.c_void_p), ("count", ctypes.c_int), ("n_slab", ctypes.c_int),
                 ("grid_slab", ctypes.c_int), ("nchunks_slab", ctypes.c_int), ("max_k", ctypes.c_int),
                 ("grid", ctypes.c_int), ("offset_other", ctypes.c_size_t)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("type", ctypes.c_int)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64), ("k_slot_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64), ("v_slot_stride", ctypes.c_int64),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("type", ctypes.c_int)]
+
+
+class BatchDesc(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_pages", ctypes.c_int),
+                ("seqs", ctypes.c_int), ("query_start", ctypes.c_void_p), ("context_len", ctypes.c_void_p),
+                ("max_query", ctypes.c_int), ("max_context", ctypes.c_int)]
 
 
 _lib = None
@@ -135,6 +164,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                  ctypes.POINTER(PrefillPlan), vp]
     lib.q4_0_gemm_prefill_batch.restype = st
     lib.q4_0_gemm_prefill_batch.argtypes = [ctypes.POINTER(PrefillPlan), vp]
+    # descriptors by address (byref): no pointer type to convert to on each call
+    i32, f32 = ctypes.c_int, ctypes.c_float
+    lib.q4_rope.restype = st
+    lib.q4_rope.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, i32, f32, vp]
+    lib.q4_kv_append.restype = st
+    lib.q4_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, vp, vp, i32, i32, f32, vp]
+    lib.q4_attention_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.q4_attention_paged_workspace_bytes.argtypes = [vp, vp, i32, i64]
+    lib.q4_attention_paged.restype = st
+    lib.q4_attention_paged.argtypes = [vp, vp, vp, vp, vp, i32, i64, f32, i64, vp, ctypes.c_size_t, vp]
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -555,7 +594,278 @@ class PrefillBatch:
         _check(load_library().q4_0_gemm_prefill_batch(ctypes.byref(self.plan), _stream(stream)))
 
 
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_length: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device="cuda") -> tuple[torch.Tensor, float]:
+    """(inv_freq float64 [rot_dim / 2], mscale) for q4_rope and q4_kv_append, made once for a model.
+
+    inv_freq[i] = base^(-2 i / rot_dim), scaled for contexts `factor` times as long as the trained ones:
+      None      as it is;
+      "linear"  positions divided by the factor;
+      "ntk"     the base times factor^(rot_dim / (rot_dim - 2)), so that the slowest pair turns as with
+                "linear" and the fastest as without;
+      "yarn"    pairs that make beta_fast turns or more over `original_length` positions as without,
+                those with beta_slow or fewer as with "linear", a ramp over the pair's index between,
+                and mscale = 0.1 ln(factor) + 1 (on queries and keys alike).
+    All of it in 64 bits on the host."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2")
+    if not base > 1.0 or not math.isfinite(base) or not factor >= 1.0 or not math.isfinite(factor):
+        raise ValueError("base must be above 1 and factor at least 1")
+    half, mscale = rot_dim // 2, 1.0
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim of at least 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-2.0 * i / rot_dim) for i in range(half)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        if not original_length or original_length < 1:
+            raise ValueError("yarn scaling needs original_length")
+        if not beta_fast > beta_slow > 0:
+            raise ValueError("beta_fast must be above beta_slow, and both above 0")
+
+        def index(turns):  # the (fractional) pair that makes so many turns over the original length
+            return rot_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        low, high = max(math.floor(index(beta_fast)), 0), min(math.ceil(index(beta_slow)), rot_dim - 1)
+        span = max(high - low, 1e-3)
+        ramp = [min(max((i - low) / span, 0.0), 1.0) for i in range(half)]
+        freq = [f * (1.0 - r) + f / factor * r for f, r in zip(freq, ramp)]
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+    return torch.tensor(freq, dtype=torch.float64, device=device), mscale
+
+
+def _heads(t: torch.Tensor, name: str, device=None) -> Heads:
+    """Tokens x heads x head_dim with the elements of a head side by side; other strides are free."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
+        raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be on a GPU" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    if t.dim() != 3:
+        raise ValueError("%s must be [tokens, heads, head_dim]" % name)
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] != 1:
+        raise ValueError("the elements of a head of %s must be side by side" % name)
+    return Heads(t.data_ptr(), st, sh, kind)
+
+
+def _vector(t: torch.Tensor, dtype, name: str, n: int, device) -> int:
+    p = _ptr(t, dtype, name)
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError("%s must be %s [%d]" % (name, dtype, n))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    return p
+
+
+def _layout(layout: str) -> int:
+    if layout not in _LAYOUTS:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    return _LAYOUTS[layout]
+
+
+def _on(device, stream):
+    """The context in which a call allocates and launches: the tensors' device and the given stream (so that what is
+    allocated here belongs to the stream that uses it), or None where they are the current ones already."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return None
+
+
+def q4_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layout: str = "half",
+            mscale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """x [T, H, D] (float16, bfloat16 or float32; the heads may lie apart, as in a part of packed projections)
+    with the leading 2 * len(inv_freq) elements of each head turned by the angles positions[t] * inv_freq[i]
+    (int32 [T], float64 [r / 2]; rope_frequencies makes them), the others as they are.  Pairs are elements i and
+    i + r/2 ("half") or 2i and 2i + 1 ("interleaved"), results times mscale.  out: like x in shape, of any of the
+    types, and may be x itself.  Turning by -positions undoes it and is its gradient."""
+    on = _on(x.device, stream) if x.is_cuda else None
+    if on is not None:
+        with on:
+            return q4_rope(x, positions, inv_freq, layout, mscale, out)
+    hx = _heads(x, "x")
+    t, h, d = x.shape
+    if out is None:
+        out = torch.empty((t, h, d), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    ho = _heads(out, "out", x.device)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be float64 [rot_dim / 2]")
+    r = inv_freq.shape[0]
+    _check(load_library().q4_rope(ctypes.byref(hx), ctypes.byref(ho), _vector(positions, torch.int32, "positions", t, x.device),
+                                  _vector(inv_freq, torch.float64, "inv_freq", r, x.device), t, h, d, 2 * r,
+                                  _layout(layout), mscale, _stream()))
+    return out
+
+
+class KVCache:
+    """A paged key/value cache: k and v [pages, kv_heads, page_size, head_dim], float16 or bfloat16, the elements of
+    a head side by side and the other strides free (a transposed view of [pages, page_size, kv_heads, head_dim] will
+    do).  page_size is a multiple of 8.  The handle holds the tensors, not their contents."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("%s must be a torch.Tensor" % name)
+            if t.dtype not in (torch.float16, torch.bfloat16):
+                raise TypeError("%s must be float16 or bfloat16, got %s" % (name, t.dtype))
+            if t.device.type != "cuda":
+                raise ValueError("%s must be on a GPU" % name)
+            if t.dim() != 4:
+                raise ValueError("%s must be [pages, kv_heads, page_size, head_dim]" % name)
+            if t.stride(3) != 1 and t.shape[3] != 1:
+                raise ValueError("the elements of a head of %s must be side by side" % name)
+        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must have one shape, type and device")
+        self.k, self.v = k, v
+        self.device, self.dtype = k.device, k.dtype
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.desc = CacheDesc(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
+                              v.stride(0), v.stride(1), v.stride(2), self.pages, self.page_size, self.kv_heads,
+                              self.head_dim, _TYPES[k.dtype])
+        self._ref = ctypes.byref(self.desc)
+
+
+class KVBatch:
+    """The sequences of a call: block_table [B, P] (the pages a sequence holds, in order), query_start [B + 1] (rows
+    of its new tokens in the token tensors) and context_lens [B] (its length with them), int32 on the GPU, where the
+    kernels read them: they may change between calls and between replays of a captured graph.  max_query_len and
+    max_context_len, if known, help to choose a kernel; results do not depend on them."""
+
+    def __init__(self, block_table: torch.Tensor, query_start: torch.Tensor, context_lens: torch.Tensor,
+                 max_query_len: int | None = None, max_context_len: int | None = None):
+        if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32:
+            raise TypeError("block_table must be an int32 tensor")
+        if block_table.device.type != "cuda":
+            raise ValueError("block_table must be on a GPU")
+        if block_table.dim() != 2 or (block_table.stride(1) != 1 and block_table.shape[1] != 1):
+            raise ValueError("block_table must be [sequences, pages] with consecutive entries")
+        b = block_table.shape[0]
+        self.device = block_table.device
+        self._keep = (block_table, query_start, context_lens)
+        self.desc = BatchDesc(block_table.data_ptr(), block_table.stride(0), block_table.shape[1], b,
+                              _vector(query_start, torch.int32, "query_start", b + 1, self.device),
+                              _vector(context_lens, torch.int32, "context_lens", b, self.device),
+                              int(max_query_len or 0), int(max_context_len or 0))
+        self._ref = ctypes.byref(self.desc)
+
+
+def _same_device(cache: KVCache, batch: KVBatch):
+    if batch.device != cache.device:
+        raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
+
+
+def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
+                 inv_freq: torch.Tensor | None = None, layout: str = "half", mscale: float = 1.0,
+                 positions: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None):
+    """Write the new tokens' keys and values (k, v [T, kv_heads, D], any of the three types) into the cache, the keys
+    turned on the way as by q4_rope (inv_freq None: not turned) by their positions in the sequence, or by
+    `positions` (int32 [T]).  With q [T, q_heads, D] also returns q turned, in the cache's type, in q_out if given."""
+    on = _on(cache.device, stream)
+    if on is not None:
+        with on:
+            return q4_kv_append(cache, batch, k, v, q, inv_freq, layout, mscale, positions, q_out)
+    _same_device(cache, batch)
+    dev = cache.device
+    hk, hv = _heads(k, "k", dev), _heads(v, "v", dev)
+    t = k.shape[0]
+    want = (t, cache.kv_heads, cache.head_dim)
+    if tuple(k.shape) != want or tuple(v.shape) != want:
+        raise ValueError("k and v must be [T, %d, %d]" % want[1:])
+    rq = ro = None
+    heads = 0
+    if q is not None:
+        hq = _heads(q, "q", dev)
+        heads = q.shape[1]
+        if q.shape[0] != t or q.shape[2] != cache.head_dim:
+            raise ValueError("q must be [T=%d, heads, %d]" % (t, cache.head_dim))
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=cache.dtype, device=dev)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        ho = _heads(q_out, "q_out", dev)
+        rq, ro = ctypes.byref(hq), ctypes.byref(ho)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    r = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be float64 [rot_dim / 2]")
+        r = inv_freq.shape[0]
+    _check(load_library().q4_kv_append(
+        cache._ref, batch._ref, ctypes.byref(hk), ctypes.byref(hv), rq, ro, heads, t,
+        None if positions is None else _vector(positions, torch.int32, "positions", t, dev),
+        _vector(inv_freq, torch.float64, "inv_freq", r, dev) if r else None, 2 * r, _layout(layout), mscale, _stream()))
+    return q_out
+
+
+def attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, tokens: int) -> int:
+    """Bytes of the workspace q4_attention_paged needs for these sizes."""
+    with torch.cuda.device(cache.device):  # the work is cut for this device
+        n = int(load_library().q4_attention_paged_workspace_bytes(cache._ref, batch._ref, q_heads, tokens))
+    if n == 0 and last_error():
+        raise Q4Error(Q4_ERR_INVALID_ARG, last_error())
+    return n
+
+
+def q4_attention_paged(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | None = None, window: int = 0,
+                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """softmax(scale q K^T) V of the new tokens' queries q [T, q_heads, D] (the cache's type) over the cached keys of
+    their sequences up to their own positions, the last `window` of them if window > 0; query head h reads kv head
+    h / (q_heads / kv_heads).  scale: 1 / sqrt(D) if None.  Append the new tokens first (q4_kv_append).  out like q;
+    lse (float32 [T, q_heads], optional) receives the log of the sum of exponentials; workspace (uint8) at least
+    attention_workspace_bytes.  Rows that see nothing are 0."""
+    on = _on(cache.device, stream)
+    if on is not None:
+        with on:
+            return q4_attention_paged(cache, batch, q, scale, window, out, lse, workspace)
+    _same_device(cache, batch)
+    dev = cache.device
+    hq = _heads(q, "q", dev)
+    t, h, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError("q must be [T, heads, %d]" % cache.head_dim)
+    if out is None:
+        out = torch.empty((t, h, d), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ho = _heads(out, "out", dev)
+    lp = None
+    if lse is not None:
+        if tuple(lse.shape) != (t, h) or lse.device != dev:
+            raise ValueError("lse must be float32 [T, heads] on %s" % dev)
+        lp = _ptr(lse, torch.float32, "lse")
+    lib = load_library()
+    if workspace is None:
+        need = lib.q4_attention_paged_workspace_bytes(cache._ref, batch._ref, h, t)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on %s" % dev)
+    wp, wb = (None, 0) if workspace is None else (_ptr(workspace, torch.uint8, "workspace"), workspace.numel())
+    _check(lib.q4_attention_paged(cache._ref, batch._ref, ctypes.byref(hq), ctypes.byref(ho), lp, h, t,
+                                  scale if scale is not None else d ** -0.5, window, wp, wb, _stream()))
+    return out
+
+
 # Short names.
 gemv = q4_0_gemv
 gemm_smallm = q4_0_gemm_smallm
 gemm_prefill = q4_0_gemm_prefill
+rope = q4_rope
+kv_append = q4_kv_append
+attention_paged = q4_attention_paged

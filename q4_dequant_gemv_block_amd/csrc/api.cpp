@@ -2,6 +2,7 @@
 // kernel launchers.  Every check runs on the host before anything is enqueued.
 #include "q4gemv.h"
 #include "q4_launch.h"
+#include "q4_status.h"
 
 #include <hip/hip_runtime.h>
 
@@ -80,6 +81,15 @@ q4_status check_tensors(const char* fn, const void* w, const void* x, const void
 bool fast_path(const void* w, int64_t k) { return k % 64 == 0 && k <= q4::kFastMaxK && aligned(w, 4); }
 
 }  // namespace
+
+namespace q4 {
+
+q4_status set_status(q4_status code, const char* text) {
+    std::snprintf(g_err, sizeof g_err, "%s", text);
+    return code;
+}
+
+}  // namespace q4
 
 extern "C" {
 

@@ -1,0 +1,672 @@
+// Attention of a chunk of new tokens over a paged key/value cache (gfx950).
+//
+// For every new token t and query head h:  out = sum_j p_j v_j / sum_j p_j with
+// p_j = exp(scale q.k_j - m) over the keys j the token sees.
+//
+// Items.  The query heads of a kv head read the same keys, so the rows (token,
+// head of the group) of one sequence and kv head are packed into items of 16 NR
+// rows (16 or 32); an item's keys are cut into units, and the units of all items, in
+// order, are dealt to the workgroups in equal contiguous ranges (ragged
+// contexts balance by themselves; the lengths are read on the device).  A range
+// that covers an item's keys whole writes its rows; one that holds a part of
+// them writes the part's sums, maxima and unnormalised outputs in 32 bits, and
+// a second launch joins the parts.
+//
+// A wave takes 32 keys at a time from HBM straight into registers, with no LDS
+// and no data movement between lanes:
+//   S^T = K Q^T on v_mfma_f32_16x16x32: two tiles of 16 keys.  Tile a holds the
+//     keys 8 (m / 4) + 4 a + m % 4 in its rows m, so that the lane that gets
+//     rows 4 q .. 4 q + 3 of both tiles has the 8 consecutive keys 8 q .. 8 q + 7
+//     of one query row - which is the B operand P^T of the second product.
+//   O^T = V^T P^T: lane (q, i) reads D/16 consecutive elements of keys 8 q .. 8 q
+//     + 7 (16 lanes read a whole row of V), and transposes its 8 x D/16 block by
+//     byte permutes into D/16 A operands; row i of operand j is element
+//     D/16 i + j.  The accumulators of lane (q, n) are then the consecutive
+//     elements D/4 q .. of query row n.
+// The running maximum is raised only when a score exceeds it by 2^8 (the
+// probabilities stay below 2^8, far inside both types), so most steps neither
+// reduce over lanes nor rescale.  Row sums are of the rounded probabilities, so
+// a rounding does not shift a row's weight.
+#include "kv_device.h"
+#include "q4gemv.h"
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+namespace q4 {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = kWaves * 64;
+constexpr int kStep = 32;         // keys of one step of a wave
+constexpr float kRaise = 8.0f;    // log2 by which a score may exceed the running maximum
+constexpr float kNone = -__builtin_inff();
+
+template <typename T>
+struct Mma;
+template <>
+struct Mma<F16> {
+    typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f4 mma(u4 a, u4 b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+};
+template <>
+struct Mma<BF16> {
+    typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f4 mma(u4 a, u4 b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+};
+
+// Two floats rounded to T in one dword (first in the low half), and back.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    typedef typename T::elem e2 __attribute__((ext_vector_type(2)));
+    const e2 v = {(typename T::elem)a, (typename T::elem)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+template <typename T>
+__device__ __forceinline__ float unpack_sum(uint32_t v) {
+    typedef typename T::elem e2 __attribute__((ext_vector_type(2)));
+    const e2 x = __builtin_bit_cast(e2, v);
+    return (float)x[0] + (float)x[1];
+}
+
+// The halves of a dword that hold NaN or an infinity, as a mask.
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite(uint32_t v) {
+    constexpr uint32_t e = std::is_same<T, F16>::value ? 0x7C00u : 0x7F80u;
+    return ((v & e) == e ? 0xFFFFu : 0u) | ((v & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
+}
+template <typename T>
+__device__ __forceinline__ float half_of(uint32_t v, int high) {
+    const uint16_t h = (uint16_t)(high ? v >> 16 : v);
+    return (float)__builtin_bit_cast(typename T::elem, h);
+}
+
+// Orders a wave's own LDS accesses (which the hardware runs in order).
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// What one sequence asks for.
+struct Seq {
+    int b, row0, n, ctx;  // first row, new tokens, context
+    int tiles, units;     // items of a kv head, units of an item
+};
+
+struct Cut {
+    int rows, unit, group, window, kv_heads, capacity;
+    int64_t tokens;
+    uint32_t total;  // units of all sequences
+};
+
+// n new tokens with the given context: items of a kv head and units of an item
+// (the most that any of its items has; a unit that lies behind an item's last
+// visible key holds no work).
+__device__ __forceinline__ void cut_sequence(const Cut& c, const BatchArg& batch, int b, Seq* s) {
+    const int first = batch.query_start[b], last = batch.query_start[b + 1];
+    s->b = b;
+    s->row0 = first;
+    s->ctx = batch.context_len[b];
+    s->n = first < 0 || last > c.tokens || last < first ? 0 : last - first;
+    const int keys = max(0, min(s->ctx, c.capacity));
+    int span = keys;
+    if (c.window) {
+        const int64_t most = (int64_t)c.window + (c.rows - 1) / c.group + 1 + kStep;
+        span = (int)min((int64_t)keys, most);
+    }
+    s->tiles = (int)(((int64_t)s->n * c.group + c.rows - 1) / c.rows);
+    s->units = s->n ? max(1, (span + c.unit - 1) / c.unit) : 0;
+}
+
+__device__ __forceinline__ uint32_t seq_units(const Cut& c, const BatchArg& batch, int b) {
+    if (b >= batch.seqs) return 0;
+    Seq s;
+    cut_sequence(c, batch, b, &s);
+    return (uint32_t)c.kv_heads * s.tiles * s.units;
+}
+
+__device__ __forceinline__ uint32_t wave_sum_u32(uint32_t v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += (uint32_t)__shfl_xor((int)v, o);
+    return v;
+}
+
+// The sequence that holds unit `at`, and the first unit of that sequence; by
+// whole waves, 64 sequences at a time.
+__device__ __forceinline__ int find_unit(const Cut& c, const BatchArg& batch, uint32_t at, uint32_t* begin) {
+    const int lane = threadIdx.x & 63;
+    uint32_t base = 0;
+    for (int b0 = 0; b0 < batch.seqs; b0 += 64) {
+        const uint32_t u = seq_units(c, batch, b0 + lane);
+        uint32_t incl = u;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t t = (uint32_t)__shfl_up((int)incl, o);
+            if (lane >= o) incl += t;
+        }
+        const uint64_t past = __ballot(base + incl > at);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            *begin = base + (uint32_t)__shfl((int)(incl - u), l);
+            return b0 + l;
+        }
+        base += (uint32_t)__shfl((int)incl, 63);
+    }
+    *begin = base;
+    return -1;
+}
+
+__device__ __forceinline__ uint32_t all_units(const Cut& c, const BatchArg& batch) {
+    uint32_t sum = 0;
+    for (int b0 = 0; b0 < batch.seqs; b0 += 64) sum += seq_units(c, batch, b0 + (int)(threadIdx.x & 63));
+    return wave_sum_u32(sum);
+}
+
+// First unit of workgroup w's range.
+__device__ __forceinline__ uint32_t range_begin(uint32_t total, uint32_t w, uint32_t grid) {
+    return (uint32_t)((uint64_t)total * w / grid);
+}
+
+// Parts in the workspace: every workgroup has at most two, one that begins its
+// range (slot 0) and one whose item begins inside it and ends behind it (slot 1).
+template <int D>
+struct Parts {
+    float* o;   // [2 grid][rows][D]
+    f2* ml;     // [2 grid][rows]: maximum (log2), sum
+    int rows;
+    __device__ Parts(void* ws, int grid, int rows_) : rows(rows_) {
+        o = static_cast<float*>(ws);
+        ml = reinterpret_cast<f2*>(o + (int64_t)2 * grid * rows_ * D);
+    }
+};
+
+// 32 keys of one wave in registers.
+template <int D>
+struct Keys {
+    u4 k[2][D / 32];           // tile a: A operand of k-step s
+    uint32_t v[8][D / 32];     // key 8 q + t: elements D/16 i ..
+};
+
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, Cut cut) {
+    constexpr int ROWS = 16 * NR;
+    constexpr int PER = D / 16;      // elements of V a lane holds of a key
+    constexpr int KS = D / 32;       // k-steps of the first product
+    constexpr int LD = D + 4;
+    // [wave][ROWS][LD] outputs, [wave][ROWS] maxima, the same of sums, [wave][ROWS][kStep] weights
+    extern __shared__ float sh[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int q = lane >> 4, n16 = lane & 15;
+    cut.total = all_units(cut, a.batch);
+    const uint32_t grid = min(gridDim.x, cut.total);  // no range is empty
+    if (blockIdx.x >= grid) return;
+    uint32_t lo = range_begin(cut.total, blockIdx.x, grid);
+    const uint32_t hi = range_begin(cut.total, blockIdx.x + 1, grid);
+    const Parts<D> parts(a.workspace, (int)gridDim.x, ROWS);
+    uint32_t begin;
+    Seq seq;
+    seq.b = __builtin_amdgcn_readfirstlane(find_unit(cut, a.batch, lo, &begin));
+    if (seq.b < 0) return;
+    begin = (uint32_t)__builtin_amdgcn_readfirstlane((int)begin);
+    cut_sequence(cut, a.batch, seq.b, &seq);
+
+    while (lo < hi) {
+        // the item and its units [u0, u1) of this range
+        while (lo - begin >= (uint32_t)cut.kv_heads * seq.tiles * seq.units) {
+            begin += (uint32_t)cut.kv_heads * seq.tiles * seq.units;
+            if (seq.b + 1 >= a.batch.seqs) return;
+            cut_sequence(cut, a.batch, seq.b + 1, &seq);
+        }
+        const uint32_t item = (lo - begin) / seq.units;
+        const int u0 = (int)((lo - begin) - item * seq.units);
+        const int u1 = (int)min((uint32_t)seq.units, u0 + (hi - lo));
+        lo += u1 - u0;
+        const int head = (int)(item / seq.tiles), tile = (int)(item - (uint32_t)head * seq.tiles);
+        const int row0 = tile * ROWS;
+        const int rows = min(ROWS, seq.n * a.group - row0);
+        const int past = seq.ctx - seq.n;  // position of the first new token
+        const int p_first = past + row0 / a.group, p_last = past + (row0 + rows - 1) / a.group;
+        const int keys = max(0, min(min(seq.ctx, cut.capacity), p_last + 1));
+        const int start = a.window ? max(0, p_first - a.window + 1) / kStep * kStep : 0;
+        const int k_lo = start + u0 * cut.unit;
+        const int k_hi = (int)min((int64_t)keys, (int64_t)start + (int64_t)u1 * cut.unit);
+
+        // queries: B operands, rows n16 of each 16-row tile
+        u4 qf[NR][KS];
+        int pos[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int row = row0 + 16 * r + n16;
+            const int rc = min(row, row0 + rows - 1);
+            const int i = rc / a.group, h = head * a.group + rc - i * a.group;
+            pos[r] = row < row0 + rows ? past + i : -1;
+            const char* src = a.q.data + ((int64_t)(seq.row0 + i) * a.q.token_stride + (int64_t)h * a.q.head_stride + 8 * q) * 2;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) qf[r][s] = *reinterpret_cast<const u4*>(src + 64 * s);
+        }
+        f4 acc[NR][PER];
+        float m[NR], l[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            m[r] = kNone;
+            l[r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) acc[r][j] = f4{0, 0, 0, 0};
+        }
+        const int32_t* table = a.batch.table + seq.b * a.batch.table_stride;
+        const char* kbase = a.cache.k + (int64_t)head * a.cache.k_head * 2 + 16 * q;
+        const char* vbase = a.cache.v + (int64_t)head * a.cache.v_head * 2 + n16 * PER * 2;
+
+        // pages of the two groups of 8 keys this lane reads in the step at key t
+        auto pages = [&](int t, int* pk, int* pv) {
+            *pk = page_of(a.cache, a.batch, table, t + 8 * (n16 >> 2));
+            *pv = page_of(a.cache, a.batch, table, t + 8 * q);
+        };
+        auto load_k = [&](int t, int page, Keys<D>& x) {
+            const uint32_t p = (uint32_t)(t + 8 * (n16 >> 2));
+            const uint32_t slot = p - a.cache.page_size.div(p) * a.cache.page_size.d + (n16 & 3);
+            const char* src = kbase + ((int64_t)max(page, 0) * a.cache.k_page + (int64_t)slot * a.cache.k_slot) * 2;
+#pragma unroll
+            for (int t4 = 0; t4 < 2; ++t4)
+#pragma unroll
+                for (int s = 0; s < KS; ++s) x.k[t4][s] = *(g_u4*)(src + t4 * 8 * a.cache.k_slot + 64 * s);
+        };
+        auto load_v = [&](int t, int page, Keys<D>& x) {
+            const uint32_t p = (uint32_t)(t + 8 * q);
+            const uint32_t slot = p - a.cache.page_size.div(p) * a.cache.page_size.d;
+            const char* src = vbase + ((int64_t)max(page, 0) * a.cache.v_page + (int64_t)slot * a.cache.v_slot) * 2;
+#pragma unroll
+            for (int t8 = 0; t8 < 8; ++t8) {
+                typedef uint32_t raw __attribute__((ext_vector_type(PER / 2), aligned(4)));
+                const raw r = *(__attribute__((address_space(1))) const raw*)(src + t8 * 2 * a.cache.v_slot);
+#pragma unroll
+                for (int j = 0; j < PER / 2; ++j) x.v[t8][j] = r[j];
+            }
+        };
+
+        Keys<D> x;
+        int t = k_lo + wave * kStep;
+        int pk, pv, pk_next, pv_next;
+        if (t < k_hi) {
+            pages(t, &pk, &pv);
+            load_k(t, pk, x);
+            load_v(t, pv, x);
+            pages(t + kWaves * kStep, &pk_next, &pv_next);
+        }
+        for (; t < k_hi; t += kWaves * kStep) {
+            // S^T: scores of keys t + 8 q .. + 7 in the lane's query rows
+            float s[NR][8];
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int t4 = 0; t4 < 2; ++t4) {
+                    f4 c = {0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) c = Mma<T>::mma(x.k[t4][k], qf[r][k], c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[r][4 * t4 + j] = c[j];
+                }
+            const int t_next = t + kWaves * kStep;
+            const bool more = t_next < k_hi;
+            const int pv_now = pv;
+            if (more) {
+                load_k(t_next, pk_next, x);
+                pv = pv_next;
+                pages(t_next + kWaves * kStep, &pk_next, &pv_next);
+            }
+            // masks: only steps that some row does not see whole
+            const bool ragged = t + kStep > min(k_hi, p_first + 1) || (a.window && t <= p_last - a.window) ||
+                                __ballot(pv_now < 0) != 0;
+            if (ragged) {
+                const int first = t + 8 * q;
+                // keys that do not belong here: their values could be anything
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (pv_now < 0 || first + j >= k_hi)
+#pragma unroll
+                        for (int e = 0; e < PER / 2; ++e) x.v[j][e] = 0;
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int key = first + j;
+                        const bool seen = key < k_hi && key <= pos[r] && pv_now >= 0 && (!a.window || key > pos[r] - a.window);
+                        s[r][j] = seen ? s[r][j] : kNone;
+                    }
+            }
+            uint32_t p[NR][4];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                float top = s[r][0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) top = fmaxf(top, s[r][j]);
+                top *= a.scale_log2;
+                if (__ballot(top > m[r] + kRaise)) {
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    const float raised = fmaxf(top, m[r]);
+                    const float f = raised == kNone ? 1.0f : __builtin_amdgcn_exp2f(m[r] - raised);
+                    m[r] = raised;
+                    l[r] *= f;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) acc[r][j] *= f;
+                }
+                const float ref = m[r] == kNone ? 0.0f : m[r];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][2 * j], a.scale_log2, -ref));
+                    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][2 * j + 1], a.scale_log2, -ref));
+                    p[r][j] = pack2<T>(e0, e1);
+                    l[r] += unpack_sum<T>(p[r][j]);
+                }
+            }
+            if (ragged) {
+                // In a product a weight of 0 times NaN or infinity would reach
+                // rows that do not see the key: such elements leave the
+                // product and are added row by row to those that do see them.
+                uint32_t any = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < PER / 2; ++e) any |= nonfinite<T>(x.v[j][e]);
+                if (__ballot(any != 0)) {
+                    // through this wave's part of LDS: rare, and so free of registers
+                    float* so = sh + wave * ROWS * LD;
+                    float* sp = sh + kWaves * ROWS * (LD + 2) + wave * ROWS * kStep;
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+                        for (int rr = 0; rr < 4; ++rr)
+#pragma unroll
+                            for (int j = 0; j < PER; ++j) so[(16 * r + n16) * LD + D / 4 * q + PER * rr + j] = acc[r][j][rr];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sp[(16 * r + n16) * kStep + 8 * q + j] = half_of<T>(p[r][j / 2], j & 1);
+                    }
+                    wave_lds_fence();
+                    for (int k = 0; k < kStep && t + k < k_hi; ++k) {
+                        const int page = page_of(a.cache, a.batch, table, t + k);
+                        if (page < 0) continue;
+                        const int64_t at = page * a.cache.v_page + head * a.cache.v_head +
+                                           (int64_t)(t + k - (int)a.cache.page_size.div(t + k) * (int)a.cache.page_size.d) * a.cache.v_slot;
+                        for (int d = lane; d < D; d += 64) {
+                            float v;
+                            load_elems<T, 1>(a.cache.v + (at + d) * 2, reinterpret_cast<float(&)[1]>(v));
+                            if (__builtin_isfinite(v)) continue;
+                            for (int row = 0; row < rows; ++row) {
+                                const int pr = past + (row0 + row) / a.group;
+                                if (t + k <= pr && (!a.window || t + k > pr - a.window)) so[row * LD + d] += sp[row * kStep + k] * v;
+                            }
+                        }
+                    }
+                    wave_lds_fence();
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int rr = 0; rr < 4; ++rr)
+#pragma unroll
+                            for (int j = 0; j < PER; ++j) acc[r][j][rr] = so[(16 * r + n16) * LD + D / 4 * q + PER * rr + j];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < PER / 2; ++e) x.v[j][e] &= ~nonfinite<T>(x.v[j][e]);
+                }
+            }
+            // O^T += V^T P^T: dim pairs (2 e, 2 e + 1) of the 8 keys become two A operands
+#pragma unroll
+            for (int e = 0; e < PER / 2; ++e) {
+                u4 even, odd;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    even[j] = __builtin_amdgcn_perm(x.v[2 * j + 1][e], x.v[2 * j][e], 0x05040100u);
+                    odd[j] = __builtin_amdgcn_perm(x.v[2 * j + 1][e], x.v[2 * j][e], 0x07060302u);
+                }
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const u4 pb = {p[r][0], p[r][1], p[r][2], p[r][3]};
+                    acc[r][2 * e] = Mma<T>::mma(even, pb, acc[r][2 * e]);
+                    acc[r][2 * e + 1] = Mma<T>::mma(odd, pb, acc[r][2 * e + 1]);
+                }
+            }
+            if (more) load_v(t_next, pv, x);
+        }
+
+        // the four waves' sums: elements D/4 q + PER rr + j of row n16 (rr: accumulator row)
+        float* sh_m = sh + kWaves * ROWS * LD;
+        float* sh_l = sh_m + kWaves * ROWS;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            l[r] += __shfl_xor(l[r], 16);
+            l[r] += __shfl_xor(l[r], 32);
+            const int at = wave * ROWS + 16 * r + n16;
+            if (q == 0) {
+                sh_m[at] = m[r];
+                sh_l[at] = l[r];
+            }
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) sh[at * LD + D / 4 * q + PER * rr + j] = acc[r][j][rr];
+        }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == seq.units;
+        const int64_t slot = (int64_t)2 * blockIdx.x + (u0 == 0);
+        for (int u = threadIdx.x; u < rows * (D / 4); u += kThreads) {
+            const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
+            float top = kNone;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sh_m[w * ROWS + row]);
+            const float ref = top == kNone ? 0.0f : top;
+            f4 o = {0, 0, 0, 0};
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float f = __builtin_amdgcn_exp2f(sh_m[w * ROWS + row] - ref);
+                sum += f * sh_l[w * ROWS + row];
+                o += f * *reinterpret_cast<const f4*>(&sh[(w * ROWS + row) * LD + d]);
+            }
+            if (whole) {
+                const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+                const int i = (row0 + row) / a.group, h = head * a.group + row0 + row - i * a.group;
+                float v[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
+                store_elems<T, 4>(a.out.data + ((int64_t)(seq.row0 + i) * a.out.token_stride + (int64_t)h * a.out.head_stride + d) * 2, v);
+                if (a.lse && d == 0)
+                    a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = sum > 0.0f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f : (sum != sum ? sum : kNone);
+            } else {
+                *reinterpret_cast<f4*>(&parts.o[(slot * ROWS + row) * D + d]) = o;
+                if (d == 0) parts.ml[slot * ROWS + row] = f2{top, sum};
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Joins the parts of the items that several ranges share: one workgroup an
+// item (blockIdx.x; those behind the last item end at once), its rows in turn.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, Cut cut, uint32_t slots) {
+    constexpr int SG = D <= 64 ? 16 : D <= 128 ? 32 : 64;  // lanes of a row
+    constexpr int NSG = kThreads / SG;
+    __shared__ f4 sh_o[NSG][SG];
+    __shared__ float sh_s[NSG];
+    const int lane = threadIdx.x & 63;
+    // the sequence that holds this item, its first item and its first unit
+    int b = -1;
+    uint32_t item = blockIdx.x, begin = 0, total = 0;
+    for (int b0 = 0; b0 < a.batch.seqs; b0 += 64) {
+        Seq s;
+        s.tiles = s.units = 0;
+        if (b0 + lane < a.batch.seqs) cut_sequence(cut, a.batch, b0 + lane, &s);
+        const uint32_t items = (uint32_t)cut.kv_heads * s.tiles, units = items * s.units;
+        uint32_t ii = items, uu = units;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t ti = (uint32_t)__shfl_up((int)ii, o), tu = (uint32_t)__shfl_up((int)uu, o);
+            if (lane >= o) {
+                ii += ti;
+                uu += tu;
+            }
+        }
+        const uint64_t past = b < 0 ? __ballot(ii > item) : 0;
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            b = b0 + l;
+            begin = total + (uint32_t)__shfl((int)(uu - units), l);
+            item -= (uint32_t)__shfl((int)(ii - items), l);
+        } else if (b < 0) {
+            item -= (uint32_t)__shfl((int)ii, 63);
+        }
+        total += (uint32_t)__shfl((int)uu, 63);
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    if (b < 0) return;
+    const uint32_t grid = min(slots, total);
+    Seq seq;
+    cut_sequence(cut, a.batch, b, &seq);
+    begin = (uint32_t)__builtin_amdgcn_readfirstlane((int)(begin + item * seq.units));
+    // first and last range with units of the item
+    auto range_of = [&](uint32_t unit) {
+        uint32_t w = (uint32_t)((uint64_t)unit * grid / total);
+        while (range_begin(total, w + 1, grid) <= unit) ++w;
+        while (range_begin(total, w, grid) > unit) --w;
+        return w;
+    };
+    const uint32_t w0 = range_of(begin), w1 = range_of(begin + seq.units - 1);
+    if (w0 == w1) return;
+    const int head = (int)(item / seq.tiles), tile = (int)(item - (uint32_t)head * seq.tiles);
+    const int row0 = tile * cut.rows, rows = min(cut.rows, seq.n * a.group - row0);
+    const Parts<D> parts(a.workspace, (int)slots, cut.rows);
+    const int g = threadIdx.x / SG, d = (threadIdx.x & (SG - 1)) * 4;
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        float top = kNone;
+        for (uint32_t w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, parts.ml[((int64_t)2 * w + (w == w0)) * cut.rows + row].x);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        const float ref = top == kNone ? 0.0f : top;
+        f4 o = {0, 0, 0, 0};
+        float sum = 0.0f;
+        for (uint32_t w = w0 + g; w <= w1; w += NSG) {
+            const int64_t slot = (int64_t)2 * w + (w == w0);
+            const f2 ml = parts.ml[slot * cut.rows + row];
+            const float f = __builtin_amdgcn_exp2f(ml.x - ref);
+            sum += f * ml.y;
+            if (d < D) o += f * *reinterpret_cast<const f4*>(&parts.o[(slot * cut.rows + row) * D + d]);
+        }
+        sh_o[g][threadIdx.x & (SG - 1)] = o;
+        if (d == 0) sh_s[g] = sum;
+        __syncthreads();
+        if (g == 0 && d < D) {
+#pragma unroll
+            for (int k = 1; k < NSG; ++k) {
+                o += sh_o[k][threadIdx.x];
+                sum += sh_s[k];
+            }
+            const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+            const int i = (row0 + row) / a.group, h = head * a.group + row0 + row - i * a.group;
+            float v[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
+            store_elems<T, 4>(a.out.data + ((int64_t)(seq.row0 + i) * a.out.token_stride + (int64_t)h * a.out.head_stride + d) * 2, v);
+            if (a.lse && d == 0)
+                a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = sum > 0.0f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f : (sum != sum ? sum : kNone);
+        }
+        __syncthreads();
+    }
+}
+
+int compute_units() {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int rows) {
+    return (int64_t)c.kv_heads * (tokens * (q_heads / c.kv_heads) / rows + std::min<int64_t>(b.seqs, tokens));
+}
+
+Cut make_cut(const AttnArgs& a, const AttnShape& s) {
+    Cut c = {};
+    c.rows = s.rows;
+    c.unit = s.unit;
+    c.group = a.group;
+    c.window = a.window;
+    c.kv_heads = a.cache.kv_heads;
+    c.capacity = (int)std::min<int64_t>((int64_t)a.batch.table_pages * a.cache.page_size.d, 0x7fffffff - 65536);
+    c.tokens = a.tokens;
+    return c;
+}
+
+template <typename T, int D, int NR>
+hipError_t launch(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
+    const Cut cut = make_cut(a, shape);
+    constexpr size_t lds = (size_t)kWaves * 16 * NR * (D + 4 + 2 + kStep) * sizeof(float);
+    if (lds > 65536) {
+        static std::atomic<bool> asked[64];
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return e;
+        if (dev >= 64 || !asked[dev].load(std::memory_order_relaxed)) {
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn<T, D, NR>), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+            if (e != hipSuccess) return e;
+            if (dev < 64) asked[dev].store(true, std::memory_order_relaxed);
+        }
+    }
+    hipLaunchKernelGGL((k_attn<T, D, NR>), dim3(shape.grid), dim3(kThreads), lds, s, a, cut);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t items = item_bound(a.cache, a.batch, a.q_heads, a.tokens, shape.rows);
+    const int by = (int)std::min<int64_t>(shape.rows, std::max<int64_t>(1, 4096 / std::max<int64_t>(1, items)));
+    hipLaunchKernelGGL((k_attn_join<T, D>), dim3((unsigned)items, by), dim3(kThreads), 0, s, a, cut, (uint32_t)shape.grid);
+    return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t launch_rows(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
+    if (shape.rows == 16) return launch<T, D, 1>(a, shape, s);
+    if constexpr (D <= 128) return launch<T, D, 2>(a, shape, s);
+    return hipErrorInvalidValue;
+}
+
+template <typename T>
+hipError_t launch_type(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
+    switch (a.cache.head_dim) {
+        case 64: return launch_rows<T, 64>(a, shape, s);
+        case 96: return launch_rows<T, 96>(a, shape, s);
+        case 128: return launch_rows<T, 128>(a, shape, s);
+        default: return launch_rows<T, 256>(a, shape, s);
+    }
+}
+
+}  // namespace
+
+bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
+
+AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int max_query) {
+    AttnShape s;
+    const int64_t group = q_heads / c.kv_heads;
+    const int64_t most = std::min<int64_t>(max_query > 0 ? max_query : tokens, tokens) * group;
+    s.rows = most <= 16 || c.head_dim > 128 ? 16 : 32;
+    // Unit: 32 keys a wave; larger where that many units would pass 31 bits.
+    s.unit = kWaves * kStep;
+    const int64_t capacity = (int64_t)b.table_pages * c.page_size.d;
+    const int64_t items = item_bound(c, b, q_heads, tokens, s.rows);
+    while (s.unit < (1 << 20) && items * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;
+    s.grid = compute_units() * (s.rows == 16 && c.head_dim <= 128 ? 2 : 1);
+    s.bytes = (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + sizeof(f2));
+    return s;
+}
+
+hipError_t launch_attention(const AttnArgs& a, const AttnShape& shape, int type, hipStream_t s) {
+    return type == Q4_TYPE_F16 ? launch_type<F16>(a, shape, s) : launch_type<BF16>(a, shape, s);
+}
+
+}  // namespace q4
