@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "libq4gemv.so")
 # the read-bandwidth probe the benchmark quotes the GEMV against (not part of the GEMV library)
 STREAM_SRC = "stream.hip"
 STREAM_LIB = os.path.join(HERE, "libq4stream.so")
-SOURCES = ["gemv.hip", "smallm.hip", "prefill.hip", "verify.hip", "q8.hip", "rope.hip", "attention.hip", "api.cpp",
+SOURCES = ["gemv.hip", "smallm.hip", "prefill.hip", "verify.hip", "q8.hip", "rope.hip", "attention.hip", "attn_tile.hip", "api.cpp",
            "kv_api.cpp"]
 ARCH = "gfx950"
 

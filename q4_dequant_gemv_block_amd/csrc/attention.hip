@@ -27,12 +27,11 @@
 // probabilities stay below 2^8, far inside both types), so most steps neither
 // reduce over lanes nor rescale.  Row sums are of the rounded probabilities, so
 // a rounding does not shift a row's weight.
-#include "kv_device.h"
+#include "attn_device.h"
 #include "q4gemv.h"
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 namespace q4 {
 
@@ -41,8 +40,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 constexpr int kStep = 32;         // keys of one step of a wave
-constexpr float kRaise = 8.0f;    // log2 by which a score may exceed the running maximum
-constexpr float kNone = -__builtin_inff();
 
 template <typename T>
 struct Mma;
@@ -61,131 +58,6 @@ struct Mma<BF16> {
     }
 };
 
-// Two floats rounded to T in one dword (first in the low half), and back.
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    typedef typename T::elem e2 __attribute__((ext_vector_type(2)));
-    const e2 v = {(typename T::elem)a, (typename T::elem)b};
-    return __builtin_bit_cast(uint32_t, v);
-}
-template <typename T>
-__device__ __forceinline__ float unpack_sum(uint32_t v) {
-    typedef typename T::elem e2 __attribute__((ext_vector_type(2)));
-    const e2 x = __builtin_bit_cast(e2, v);
-    return (float)x[0] + (float)x[1];
-}
-
-// The halves of a dword that hold NaN or an infinity, as a mask.
-template <typename T>
-__device__ __forceinline__ uint32_t nonfinite(uint32_t v) {
-    constexpr uint32_t e = std::is_same<T, F16>::value ? 0x7C00u : 0x7F80u;
-    return ((v & e) == e ? 0xFFFFu : 0u) | ((v & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
-}
-template <typename T>
-__device__ __forceinline__ float half_of(uint32_t v, int high) {
-    const uint16_t h = (uint16_t)(high ? v >> 16 : v);
-    return (float)__builtin_bit_cast(typename T::elem, h);
-}
-
-// Orders a wave's own LDS accesses (which the hardware runs in order).
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
-// What one sequence asks for.
-struct Seq {
-    int b, row0, n, ctx;  // first row, new tokens, context
-    int tiles, units;     // items of a kv head, units of an item
-};
-
-struct Cut {
-    int rows, unit, group, window, kv_heads, capacity;
-    int64_t tokens;
-    uint32_t total;  // units of all sequences
-};
-
-// n new tokens with the given context: items of a kv head and units of an item
-// (the most that any of its items has; a unit that lies behind an item's last
-// visible key holds no work).
-__device__ __forceinline__ void cut_sequence(const Cut& c, const BatchArg& batch, int b, Seq* s) {
-    const int first = batch.query_start[b], last = batch.query_start[b + 1];
-    s->b = b;
-    s->row0 = first;
-    s->ctx = batch.context_len[b];
-    s->n = first < 0 || last > c.tokens || last < first ? 0 : last - first;
-    const int keys = max(0, min(s->ctx, c.capacity));
-    int span = keys;
-    if (c.window) {
-        const int64_t most = (int64_t)c.window + (c.rows - 1) / c.group + 1 + kStep;
-        span = (int)min((int64_t)keys, most);
-    }
-    s->tiles = (int)(((int64_t)s->n * c.group + c.rows - 1) / c.rows);
-    s->units = s->n ? max(1, (span + c.unit - 1) / c.unit) : 0;
-}
-
-__device__ __forceinline__ uint32_t seq_units(const Cut& c, const BatchArg& batch, int b) {
-    if (b >= batch.seqs) return 0;
-    Seq s;
-    cut_sequence(c, batch, b, &s);
-    return (uint32_t)c.kv_heads * s.tiles * s.units;
-}
-
-__device__ __forceinline__ uint32_t wave_sum_u32(uint32_t v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += (uint32_t)__shfl_xor((int)v, o);
-    return v;
-}
-
-// The sequence that holds unit `at`, and the first unit of that sequence; by
-// whole waves, 64 sequences at a time.
-__device__ __forceinline__ int find_unit(const Cut& c, const BatchArg& batch, uint32_t at, uint32_t* begin) {
-    const int lane = threadIdx.x & 63;
-    uint32_t base = 0;
-    for (int b0 = 0; b0 < batch.seqs; b0 += 64) {
-        const uint32_t u = seq_units(c, batch, b0 + lane);
-        uint32_t incl = u;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const uint32_t t = (uint32_t)__shfl_up((int)incl, o);
-            if (lane >= o) incl += t;
-        }
-        const uint64_t past = __ballot(base + incl > at);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            *begin = base + (uint32_t)__shfl((int)(incl - u), l);
-            return b0 + l;
-        }
-        base += (uint32_t)__shfl((int)incl, 63);
-    }
-    *begin = base;
-    return -1;
-}
-
-__device__ __forceinline__ uint32_t all_units(const Cut& c, const BatchArg& batch) {
-    uint32_t sum = 0;
-    for (int b0 = 0; b0 < batch.seqs; b0 += 64) sum += seq_units(c, batch, b0 + (int)(threadIdx.x & 63));
-    return wave_sum_u32(sum);
-}
-
-// First unit of workgroup w's range.
-__device__ __forceinline__ uint32_t range_begin(uint32_t total, uint32_t w, uint32_t grid) {
-    return (uint32_t)((uint64_t)total * w / grid);
-}
-
-// Parts in the workspace: every workgroup has at most two, one that begins its
-// range (slot 0) and one whose item begins inside it and ends behind it (slot 1).
-template <int D>
-struct Parts {
-    float* o;   // [2 grid][rows][D]
-    f2* ml;     // [2 grid][rows]: maximum (log2), sum
-    int rows;
-    __device__ Parts(void* ws, int grid, int rows_) : rows(rows_) {
-        o = static_cast<float*>(ws);
-        ml = reinterpret_cast<f2*>(o + (int64_t)2 * grid * rows_ * D);
-    }
-};
-
 // 32 keys of one wave in registers.
 template <int D>
 struct Keys {
@@ -194,48 +66,23 @@ struct Keys {
 };
 
 template <typename T, int D, int NR>
-__global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, Cut cut) {
+__global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut cut) {
     constexpr int ROWS = 16 * NR;
     constexpr int PER = D / 16;      // elements of V a lane holds of a key
     constexpr int KS = D / 32;       // k-steps of the first product
     constexpr int LD = D + 4;
     // [wave][ROWS][LD] outputs, [wave][ROWS] maxima, the same of sums, [wave][ROWS][kStep] weights
     extern __shared__ float sh[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, n16 = lane & 15;
-    cut.total = all_units(cut, a.batch);
-    const uint32_t grid = min(gridDim.x, cut.total);  // no range is empty
-    if (blockIdx.x >= grid) return;
-    uint32_t lo = range_begin(cut.total, blockIdx.x, grid);
-    const uint32_t hi = range_begin(cut.total, blockIdx.x + 1, grid);
+    Work work;
+    if (!work.start(cut, a.batch)) return;
+    const Seq& seq = work.seq;
     const Parts<D> parts(a.workspace, (int)gridDim.x, ROWS);
-    uint32_t begin;
-    Seq seq;
-    seq.b = __builtin_amdgcn_readfirstlane(find_unit(cut, a.batch, lo, &begin));
-    if (seq.b < 0) return;
-    begin = (uint32_t)__builtin_amdgcn_readfirstlane((int)begin);
-    cut_sequence(cut, a.batch, seq.b, &seq);
-
-    while (lo < hi) {
-        // the item and its units [u0, u1) of this range
-        while (lo - begin >= (uint32_t)cut.kv_heads * seq.tiles * seq.units) {
-            begin += (uint32_t)cut.kv_heads * seq.tiles * seq.units;
-            if (seq.b + 1 >= a.batch.seqs) return;
-            cut_sequence(cut, a.batch, seq.b + 1, &seq);
-        }
-        const uint32_t item = (lo - begin) / seq.units;
-        const int u0 = (int)((lo - begin) - item * seq.units);
-        const int u1 = (int)min((uint32_t)seq.units, u0 + (hi - lo));
-        lo += u1 - u0;
-        const int head = (int)(item / seq.tiles), tile = (int)(item - (uint32_t)head * seq.tiles);
-        const int row0 = tile * ROWS;
-        const int rows = min(ROWS, seq.n * a.group - row0);
-        const int past = seq.ctx - seq.n;  // position of the first new token
-        const int p_first = past + row0 / a.group, p_last = past + (row0 + rows - 1) / a.group;
-        const int keys = max(0, min(min(seq.ctx, cut.capacity), p_last + 1));
-        const int start = a.window ? max(0, p_first - a.window + 1) / kStep * kStep : 0;
-        const int k_lo = start + u0 * cut.unit;
-        const int k_hi = (int)min((int64_t)keys, (int64_t)start + (int64_t)u1 * cut.unit);
+    Item it;
+    while (work.next(cut, a.batch, &it)) {
+        const int head = it.head, row0 = it.row0, rows = it.rows, past = it.past;
+        const int p_first = it.p_first, p_last = it.p_last, k_lo = it.k_lo, k_hi = it.k_hi;
 
         // queries: B operands, rows n16 of each 16-row tile
         u4 qf[NR][KS];
@@ -454,8 +301,8 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, Cut cut) {
                 for (int j = 0; j < PER; ++j) sh[at * LD + D / 4 * q + PER * rr + j] = acc[r][j][rr];
         }
         __syncthreads();
-        const bool whole = u0 == 0 && u1 == seq.units;
-        const int64_t slot = (int64_t)2 * blockIdx.x + (u0 == 0);
+        const bool whole = it.u0 == 0 && it.u1 == seq.units;
+        const int64_t slot = (int64_t)2 * blockIdx.x + (it.u0 == 0);
         for (int u = threadIdx.x; u < rows * (D / 4); u += kThreads) {
             const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
             float top = kNone;
@@ -471,12 +318,12 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, Cut cut) {
                 o += f * *reinterpret_cast<const f4*>(&sh[(w * ROWS + row) * LD + d]);
             }
             if (whole) {
-                const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+                const float f = row_scale(sum);
                 const int i = (row0 + row) / a.group, h = head * a.group + row0 + row - i * a.group;
                 float v[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
                 store_elems<T, 4>(a.out.data + ((int64_t)(seq.row0 + i) * a.out.token_stride + (int64_t)h * a.out.head_stride + d) * 2, v);
                 if (a.lse && d == 0)
-                    a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = sum > 0.0f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f : (sum != sum ? sum : kNone);
+                    a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = row_lse(top, sum);
             } else {
                 *reinterpret_cast<f4*>(&parts.o[(slot * ROWS + row) * D + d]) = o;
                 if (d == 0) parts.ml[slot * ROWS + row] = f2{top, sum};
@@ -489,7 +336,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, Cut cut) {
 // Joins the parts of the items that several ranges share: one workgroup an
 // item (blockIdx.x; those behind the last item end at once), its rows in turn.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, Cut cut, uint32_t slots) {
+__global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, const Cut cut, uint32_t slots) {
     constexpr int SG = D <= 64 ? 16 : D <= 128 ? 32 : 64;  // lanes of a row
     constexpr int NSG = kThreads / SG;
     __shared__ f4 sh_o[NSG][SG];
@@ -538,8 +385,9 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, Cut cu
     };
     const uint32_t w0 = range_of(begin), w1 = range_of(begin + seq.units - 1);
     if (w0 == w1) return;
-    const int head = (int)(item / seq.tiles), tile = (int)(item - (uint32_t)head * seq.tiles);
-    const int row0 = tile * cut.rows, rows = min(cut.rows, seq.n * a.group - row0);
+    Item it;
+    place_item(cut, seq, item, &it);
+    const int head = it.head, row0 = it.row0, rows = it.rows;
     const Parts<D> parts(a.workspace, (int)slots, cut.rows);
     const int g = threadIdx.x / SG, d = (threadIdx.x & (SG - 1)) * 4;
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
@@ -566,12 +414,12 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, Cut cu
                 o += sh_o[k][threadIdx.x];
                 sum += sh_s[k];
             }
-            const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+            const float f = row_scale(sum);
             const int i = (row0 + row) / a.group, h = head * a.group + row0 + row - i * a.group;
             float v[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
             store_elems<T, 4>(a.out.data + ((int64_t)(seq.row0 + i) * a.out.token_stride + (int64_t)h * a.out.head_stride + d) * 2, v);
             if (a.lse && d == 0)
-                a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = sum > 0.0f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f : (sum != sum ? sum : kNone);
+                a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = row_lse(top, sum);
         }
         __syncthreads();
     }
@@ -589,6 +437,7 @@ int compute_units() {
     return n;
 }
 
+// Most items a call can have: a sequence's rows round up once.
 int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int rows) {
     return (int64_t)c.kv_heads * (tokens * (q_heads / c.kv_heads) / rows + std::min<int64_t>(b.seqs, tokens));
 }
@@ -597,56 +446,63 @@ Cut make_cut(const AttnArgs& a, const AttnShape& s) {
     Cut c = {};
     c.rows = s.rows;
     c.unit = s.unit;
+    c.step = s.step;
     c.group = a.group;
     c.window = a.window;
     c.kv_heads = a.cache.kv_heads;
-    c.capacity = (int)std::min<int64_t>((int64_t)a.batch.table_pages * a.cache.page_size.d, 0x7fffffff - 65536);
+    c.capacity = (int)((int64_t)a.batch.table_pages * a.cache.page_size.d);
     c.tokens = a.tokens;
     return c;
 }
 
 template <typename T, int D, int NR>
 hipError_t launch(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
-    const Cut cut = make_cut(a, shape);
     constexpr size_t lds = (size_t)kWaves * 16 * NR * (D + 4 + 2 + kStep) * sizeof(float);
-    if (lds > 65536) {
-        static std::atomic<bool> asked[64];
-        int dev = 0;
-        hipError_t e = hipGetDevice(&dev);
-        if (e != hipSuccess) return e;
-        if (dev >= 64 || !asked[dev].load(std::memory_order_relaxed)) {
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn<T, D, NR>), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-            if (e != hipSuccess) return e;
-            if (dev < 64) asked[dev].store(true, std::memory_order_relaxed);
-        }
-    }
-    hipLaunchKernelGGL((k_attn<T, D, NR>), dim3(shape.grid), dim3(kThreads), lds, s, a, cut);
-    hipError_t e = hipGetLastError();
+    static LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn<T, D, NR>), lds);
     if (e != hipSuccess) return e;
-    const int64_t items = item_bound(a.cache, a.batch, a.q_heads, a.tokens, shape.rows);
-    const int by = (int)std::min<int64_t>(shape.rows, std::max<int64_t>(1, 4096 / std::max<int64_t>(1, items)));
-    hipLaunchKernelGGL((k_attn_join<T, D>), dim3((unsigned)items, by), dim3(kThreads), 0, s, a, cut, (uint32_t)shape.grid);
+    hipLaunchKernelGGL((k_attn<T, D, NR>), dim3(shape.grid), dim3(kThreads), lds, s, a, make_cut(a, shape));
     return hipGetLastError();
 }
 
 template <typename T, int D>
-hipError_t launch_rows(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
-    if (shape.rows == 16) return launch<T, D, 1>(a, shape, s);
-    if constexpr (D <= 128) return launch<T, D, 2>(a, shape, s);
-    return hipErrorInvalidValue;
+hipError_t launch_dim(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
+    hipError_t e = hipErrorInvalidValue;
+    if (shape.rows >= 128)
+        e = launch_attn_tile<T, D>(a, make_cut(a, shape), shape, s);
+    else if (shape.rows == 16)
+        e = launch<T, D, 1>(a, shape, s);
+    else if constexpr (D <= 128)
+        e = launch<T, D, 2>(a, shape, s);
+    if (e != hipSuccess || !shape.bytes) return e;
+    const int64_t items = item_bound(a.cache, a.batch, a.q_heads, a.tokens, shape.rows);
+    const int by = (int)std::min<int64_t>(shape.rows, std::max<int64_t>(1, 4096 / std::max<int64_t>(1, items)));
+    hipLaunchKernelGGL((k_attn_join<T, D>), dim3((unsigned)items, by), dim3(kThreads), 0, s, a, make_cut(a, shape), (uint32_t)shape.grid);
+    return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_type(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
     switch (a.cache.head_dim) {
-        case 64: return launch_rows<T, 64>(a, shape, s);
-        case 96: return launch_rows<T, 96>(a, shape, s);
-        case 128: return launch_rows<T, 128>(a, shape, s);
-        default: return launch_rows<T, 256>(a, shape, s);
+        case 64: return launch_dim<T, 64>(a, shape, s);
+        case 96: return launch_dim<T, 96>(a, shape, s);
+        case 128: return launch_dim<T, 128>(a, shape, s);
+        default: return launch_dim<T, 256>(a, shape, s);
     }
 }
 
 }  // namespace
+
+hipError_t LdsLimit::raise(const void* kernel, size_t bytes) {
+    if (bytes <= 65536) return hipSuccess;
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    if (dev < 64 && done[dev].load(std::memory_order_relaxed)) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == hipSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
 
 bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
 
@@ -654,14 +510,29 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
     AttnShape s;
     const int64_t group = q_heads / c.kv_heads;
     const int64_t most = std::min<int64_t>(max_query > 0 ? max_query : tokens, tokens) * group;
-    s.rows = most <= 16 || c.head_dim > 128 ? 16 : 32;
-    // Unit: 32 keys a wave; larger where that many units would pass 31 bits.
-    s.unit = kWaves * kStep;
+    const int cus = compute_units();
+    bool split = true;
+    if (most <= (c.head_dim > 128 ? 16 : 32)) {
+        s.rows = most <= 16 ? 16 : 32;
+        s.step = kStep;
+        s.unit = kWaves * kStep;  // a step of each wave
+        s.grid = cus * (s.rows == 16 && c.head_dim <= 128 ? 2 : 1);
+    } else {
+        s.step = s.unit = 64;
+        s.rows = c.head_dim > 128 || item_bound(c, b, q_heads, tokens, 256) < cus ? 128 : 256;
+        s.grid = cus;
+        // Items enough to fill the machine are taken whole, the longest first.
+        if (item_bound(c, b, q_heads, tokens, s.rows) - (int64_t)c.kv_heads * std::min<int64_t>(b.seqs, tokens) >= 2 * cus) {
+            split = false;
+            s.unit = 1 << 30;
+            s.grid = (int)item_bound(c, b, q_heads, tokens, s.rows);
+        }
+    }
+    // Larger units where this many would pass 31 bits.
     const int64_t capacity = (int64_t)b.table_pages * c.page_size.d;
     const int64_t items = item_bound(c, b, q_heads, tokens, s.rows);
-    while (s.unit < (1 << 20) && items * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;
-    s.grid = compute_units() * (s.rows == 16 && c.head_dim <= 128 ? 2 : 1);
-    s.bytes = (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + sizeof(f2));
+    while (s.unit < (1 << 30) && items * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;
+    s.bytes = split ? (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + sizeof(f2)) : 0;
     return s;
 }
 

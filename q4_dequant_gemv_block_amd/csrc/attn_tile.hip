@@ -1,0 +1,355 @@
+// Attention of many new tokens a sequence (prompts and chunks of them) over a
+// paged cache: the same items, units and ranges as k_attn, in tiles that the
+// matrix cores are the bound of.
+//
+// A workgroup of NW waves holds 32 NW query rows, 32 a wave, and goes through
+// its keys 64 at a time.  A tile of K and V goes from HBM or L2 straight into LDS
+// (global_load_lds, 16 bytes a lane), two tiles deep, one barrier a tile.  The
+// products run on v_mfma_f32_32x32x16:
+//   S^T = K Q^T: A = 32 keys from LDS, B = Q^T, which stays in registers;
+//   O^T = V^T P^T: A = V^T by the transposing LDS read (ds_read_b64_tr_b16: 16
+//     lanes read 4 keys of 16 elements and get one element's 4 keys each), B =
+//     P^T, which is what the accumulators of S^T hold: lane (h, n) has the keys
+//     8 (i / 4) + 4 h + i % 4 of query row n, so the two transposing reads of a 16-key
+//     step take keys 4 h .. and 8 + 4 h .. .
+// LDS rows are as long as a head; the 16-byte chunk c of row r lies at c ^ f(r),
+// so that the 16 rows of a K read and the 4 rows x 64 bytes of a V read cover all 64
+// banks (f by row for K, by row % 4 in 64-byte blocks for V; measured without
+// conflicts).  The running maximum is raised as in k_attn.
+#include "attn_device.h"
+#include "q4gemv.h"
+
+namespace q4 {
+
+namespace {
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Mma32;
+template <>
+struct Mma32<F16> {
+    typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f16v mma(u4 a, u4 b, f16v c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+};
+template <>
+struct Mma32<BF16> {
+    typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f16v mma(u4 a, u4 b, f16v c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+};
+
+// l + both halves of p.
+template <typename T>
+__device__ __forceinline__ float add_pair(uint32_t p, float l) {
+    if constexpr (std::is_same<T, F16>::value) {
+        const h2 one = {(_Float16)1.0f, (_Float16)1.0f};
+        return __builtin_amdgcn_fdot2(as_h2(p), one, l, false);
+    } else {
+        return l + (__builtin_bit_cast(float, p << 16) + __builtin_bit_cast(float, p & 0xFFFF0000u));
+    }
+}
+
+// Direct-to-LDS load from a wave's address and a lane's offset: lane i's 16
+// bytes land at lds + 16 i.  Issued through asm so
+// that the compiler does not wait for a tile in flight before it reads the
+// other one; the kernel waits itself (vmcnt) before the tile's barrier.
+__device__ __forceinline__ void load_to_lds(const char* src, uint32_t offset, uint32_t lds) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(src), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+constexpr int kTile = 64;  // keys of a tile
+
+template <int D>
+struct Layout {
+    static constexpr int row = D <= 64 ? 128 : D <= 128 ? 256 : 512;  // bytes of an LDS row
+    static constexpr int chunks = row / 16;
+    static constexpr int bytes = kTile * row;                         // of a tile of K or V
+    static constexpr int per_load = 1024 / row;                       // rows of a wave's load
+    // XOR of a row's chunks
+    static __device__ __forceinline__ int swz_k(int r) { return chunks == 8 ? (r >> 1) & 7 : r & 15; }
+    static __device__ __forceinline__ int swz_v(int r) { return chunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; }
+};
+
+template <typename T, int D, int NW>
+__global__ void __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) k_attn_tile(const AttnArgs a, const Cut cut) {
+    typedef Layout<D> L;
+    constexpr int ROWS = 32 * NW;
+    constexpr int KS = D / 16;                         // k-steps of the first product
+    constexpr int DT = D / 32;                         // 32-element tiles of the output
+    constexpr int LOADS = kTile / L::per_load / NW;    // loads of a wave for K, and for V, of a tile
+    constexpr int GROUPS = 8 / NW;                     // groups of 8 keys they cover
+    constexpr int PER_GROUP = LOADS / GROUPS;
+    extern __shared__ char sh[];  // [2][K, V][64][row], then a flag of each wave
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int h = lane >> 5, n = lane & 31;
+    const uint32_t sh0 = lds_address(sh);
+
+    Work work;
+    if (!work.start(cut, a.batch)) return;
+    const Seq& seq = work.seq;
+    const Parts<D> parts(a.workspace, (int)gridDim.x, ROWS);
+    Item it;
+
+    // where this lane reads in a tile: chunks 2 s + h of K's rows, 64-byte block d of V's
+    int at_k0 = n * L::row + ((h ^ L::swz_k(n)) * 16), at_v0;
+    {
+        const int g = lane >> 4, r = 4 * (g >> 1) + ((lane >> 2) & 3);
+        const int c = 2 * (g & 1) + ((lane & 3) >> 1);
+        at_v0 = r * L::row + ((c ^ L::swz_v(r)) * 16) + (lane & 1) * 8;
+    }
+
+    while (work.next(cut, a.batch, &it)) {
+        const int32_t* table = a.batch.table + seq.b * a.batch.table_stride;
+        const char* kbase = a.cache.k + (int64_t)it.head * a.cache.k_head * 2;
+        const char* vbase = a.cache.v + (int64_t)it.head * a.cache.v_head * 2;
+
+        // this lane's query row and the wave's first and last positions
+        const int row = it.row0 + 32 * wave + n;
+        const int rc = min(row, it.row0 + it.rows - 1);
+        const int qi = rc / a.group, qh = it.head * a.group + rc - qi * a.group;
+        const int pos = it.past + qi;
+        const int w_rows = min(32, it.rows - 32 * wave);  // may be <= 0
+        const int w_first = it.past + (it.row0 + 32 * wave) / a.group;
+        const int w_last = it.past + (it.row0 + 32 * wave + w_rows - 1) / a.group;
+        u4 qf[KS];
+        {
+            const char* src = a.q.data + ((int64_t)(seq.row0 + qi) * a.q.token_stride + (int64_t)qh * a.q.head_stride + 8 * h) * 2;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u4*>(src + 32 * s);
+        }
+        f16v acc[DT];
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+        float m = kNone, l = 0.0f;
+
+        // page of this lane's group (lane % 8) of the tile at key t
+        auto pages = [&](int t) { return page_of(a.cache, a.batch, table, t + 8 * (lane & 7)); };
+        auto fill = [&](int t, int page8, int stage) {
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                const int group = wave * GROUPS + g;
+                const int page = max(__builtin_amdgcn_readlane(page8, group), 0);
+                const uint32_t p = (uint32_t)(t + 8 * group);
+                const uint32_t slot = p - a.cache.page_size.div(p) * a.cache.page_size.d;
+                const char* ks = kbase + ((int64_t)page * a.cache.k_page + (int64_t)slot * a.cache.k_slot) * 2;
+                const char* vs = vbase + ((int64_t)page * a.cache.v_page + (int64_t)slot * a.cache.v_slot) * 2;
+#pragma unroll
+                for (int x = 0; x < PER_GROUP; ++x) {
+                    const int r8 = x * L::per_load + lane / L::chunks;  // row of the group
+                    const int r = 8 * group + r8;
+                    const int ck = (lane % L::chunks) ^ L::swz_k(r), cv = (lane % L::chunks) ^ L::swz_v(r);
+                    const uint32_t to = sh0 + stage * 2 * L::bytes + (8 * group + x * L::per_load) * L::row;
+                    if (D == 8 * L::chunks || ck < D / 8) load_to_lds(ks, r8 * (uint32_t)a.cache.k_slot * 2 + 16 * ck, to);
+                    if (D == 8 * L::chunks || cv < D / 8) load_to_lds(vs, r8 * (uint32_t)a.cache.v_slot * 2 + 16 * cv, to + L::bytes);
+                }
+            }
+        };
+
+        int stage = 0;
+        int page_now = 0, page_next = 0;
+        if (it.k_lo < it.k_hi) {
+            page_now = pages(it.k_lo);
+            fill(it.k_lo, page_now, 0);
+            page_next = pages(it.k_lo + kTile);
+        }
+        for (int t = it.k_lo; t < it.k_hi; t += kTile, stage ^= 1) {
+            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");  // the tile is there, the other one is read
+            const int page8 = page_now;
+            if (t + kTile < it.k_hi) {
+                page_now = page_next;
+                fill(t + kTile, page_now, stage ^ 1);
+                page_next = pages(t + 2 * kTile);
+            }
+            char* tk = sh + stage * 2 * L::bytes;
+            char* tv = tk + L::bytes;
+            const uint32_t valid = (uint32_t)__ballot(page8 >= 0) & 0xFF;  // groups with a place
+
+            // Tiles that not all of the workgroup's rows see whole: values of
+            // keys that do not belong here become 0, and so do NaN and
+            // infinities, which are added below row by row.
+            bool odd = false;
+            if (valid != 0xFF || t + kTile > min(it.k_hi, it.p_first + 1) || (a.window && t <= it.p_last - a.window)) {
+                bool mine = false;
+                for (int u = threadIdx.x; u < kTile * L::chunks; u += NW * 64) {
+                    const int r = u / L::chunks, c = (u % L::chunks) ^ L::swz_v(r);
+                    if (c >= D / 8) continue;
+                    u4* at = reinterpret_cast<u4*>(tv + u * 16);
+                    if (t + r >= it.k_hi || !((valid >> (r >> 3)) & 1)) {
+                        *at = u4{0, 0, 0, 0};
+                    } else {
+                        const u4 v = *at;
+                        const u4 bad = {nonfinite<T>(v.x), nonfinite<T>(v.y), nonfinite<T>(v.z), nonfinite<T>(v.w)};
+                        if (bad.x | bad.y | bad.z | bad.w) {
+                            *at = v & ~bad;
+                            mine = true;
+                        }
+                    }
+                }
+                int* flags = reinterpret_cast<int*>(sh + 4 * L::bytes);
+                const bool wave_odd = __ballot(mine) != 0;
+                if (lane == 0) flags[wave] = wave_odd;
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < NW; ++w) odd |= flags[w] != 0;
+            }
+
+            if (w_rows <= 0 || t > w_last || (a.window && t + kTile <= w_first - a.window + 1)) continue;
+            // (for heads of 256 the addresses are made anew each tile: registers)
+            if constexpr (D > 128) asm volatile("" : "+v"(at_k0), "+v"(at_v0));
+            // S^T
+            f16v s[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    s[u] = Mma32<T>::mma(*reinterpret_cast<const u4*>(tk + (at_k0 ^ (32 * k)) + u * 32 * L::row), qf[k], s[u]);
+                if constexpr (D > 128) __builtin_amdgcn_sched_barrier(0);  // registers: no reads ahead
+            }
+            if (valid != 0xFF || t + kTile > min(it.k_hi, w_first + 1) || (a.window && t <= w_last - a.window)) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 32 * u + 8 * (i >> 2) + 4 * h + (i & 3), key = t + r;
+                        const bool seen = key < it.k_hi && key <= pos && (!a.window || key > pos - a.window) && ((valid >> (r >> 3)) & 1);
+                        s[u][i] = seen ? s[u][i] : kNone;
+                    }
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+            top *= a.scale_log2;
+            if (__ballot(top > m + kRaise)) {
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float raised = fmaxf(top, m);
+                const float f = raised == kNone ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
+                m = raised;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) acc[d] *= f;
+            }
+            const float ref = m == kNone ? 0.0f : m;
+            u4 p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = 8 * (k & 1) + 2 * j;
+                    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][i], a.scale_log2, -ref));
+                    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][i + 1], a.scale_log2, -ref));
+                    p[k][j] = pack2<T>(e0, e1);
+                    l = add_pair<T>(p[k][j], l);
+                }
+            if (odd) {
+                // The elements that left the product, for the rows that see them.
+                for (int k = 0; k < kTile && t + k < it.k_hi; ++k) {
+                    if (!((valid >> (k >> 3)) & 1)) continue;
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)  // keys 16 k4 + 8 (j / 2) + 4 h + 2 (j % 2), + 1
+                            if ((k & ~5) == 16 * k4 + 8 * (j >> 1) + 2 * (j & 1)) w = p[k4][j];
+                    const float weight = half_of<T>((uint32_t)__shfl((int)w, n + 32 * ((k >> 2) & 1)), k & 1);
+                    const bool sees = t + k <= pos && (!a.window || t + k > pos - a.window);
+                    const int page = __builtin_amdgcn_readlane(page8, k >> 3);
+                    const uint32_t slot = (uint32_t)(t + k) - a.cache.page_size.div(t + k) * a.cache.page_size.d;
+                    const char* src = vbase + ((int64_t)page * a.cache.v_page + (int64_t)slot * a.cache.v_slot + 4 * h) * 2;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int i4 = 0; i4 < 4; ++i4) {
+                            float v[4];
+                            load_elems<T, 4>(src + (32 * d + 8 * i4) * 2, v);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (sees && !__builtin_isfinite(v[i])) acc[d][4 * i4 + i] += weight * v[i];
+                        }
+                }
+            }
+            // O^T += V^T P^T
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (D > 128) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    typedef __attribute__((address_space(3))) s4 l_s4;
+                    const char* src = tv + (at_v0 ^ (64 * d)) + 16 * k * L::row;
+                    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)src);
+                    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)(src + 8 * L::row));
+                    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+                    const u2 x = __builtin_bit_cast(u2, lo), y = __builtin_bit_cast(u2, hi);
+                    acc[d] = Mma32<T>::mma(u4{x.x, x.y, y.x, y.y}, p[k], acc[d]);
+                }
+            }
+        }
+        __syncthreads();  // both tiles are read before the next item's
+
+        l += __shfl_xor(l, 32);
+        if (32 * wave + n >= it.rows) continue;
+        if (it.u0 == 0 && it.u1 == seq.units) {
+            const float f = row_scale(l);
+            char* dst = a.out.data + ((int64_t)(seq.row0 + qi) * a.out.token_stride + (int64_t)qh * a.out.head_stride + 4 * h) * 2;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float v[4] = {acc[d][i] * f, acc[d][i + 1] * f, acc[d][i + 2] * f, acc[d][i + 3] * f};
+                    store_elems<T, 4>(dst + (32 * d + 2 * i) * 2, v);
+                }
+            if (a.lse && h == 0) a.lse[(int64_t)(seq.row0 + qi) * a.q_heads + qh] = row_lse(m, l);
+        } else {
+            const int64_t slot = ((int64_t)2 * blockIdx.x + (it.u0 == 0)) * ROWS + 32 * wave + n;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<f4*>(&parts.o[slot * D + 32 * d + 2 * i + 4 * h]) = f4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]};
+            if (h == 0) parts.ml[slot] = f2{m, l};
+        }
+    }
+}
+
+template <typename T, int D, int NW>
+hipError_t launch(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
+    constexpr size_t lds = (size_t)4 * Layout<D>::bytes + NW * sizeof(int);
+    static LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, NW>), lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_attn_tile<T, D, NW>), dim3(shape.grid), dim3(NW * 64), lds, s, a, cut);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+template <typename T, int D>
+hipError_t launch_attn_tile(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
+    if constexpr (D <= 128)
+        if (shape.rows == 256) return launch<T, D, 8>(a, cut, shape, s);
+    return launch<T, D, 4>(a, cut, shape, s);
+}
+
+template hipError_t launch_attn_tile<F16, 64>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);
+template hipError_t launch_attn_tile<F16, 96>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);
+template hipError_t launch_attn_tile<F16, 128>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);
+template hipError_t launch_attn_tile<F16, 256>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);
+template hipError_t launch_attn_tile<BF16, 64>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);
+template hipError_t launch_attn_tile<BF16, 96>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);
+template hipError_t launch_attn_tile<BF16, 128>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);
+template hipError_t launch_attn_tile<BF16, 256>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);
+
+}  // namespace q4

@@ -183,6 +183,8 @@ q4_status check_attention(const char* fn, const q4_kv_cache* cache, const q4_kv_
     if (!aligned(cache->k, 16) || !aligned(cache->v, 16)) return fail(Q4_ERR_MISALIGNED, "%s: the cache must be 16-byte aligned", fn);
     if ((cache->k_page_stride | cache->k_head_stride | cache->k_slot_stride | cache->v_page_stride | cache->v_head_stride | cache->v_slot_stride) % 8)
         return fail(Q4_ERR_MISALIGNED, "%s: the cache's strides must be multiples of 8", fn);
+    if (cache->k_slot_stride > (1 << 26) || cache->v_slot_stride > (1 << 26))
+        return fail(Q4_ERR_INVALID_ARG, "%s: the slots of the cache must not be more than 2^26 elements apart", fn);
     return Q4_OK;
 }
 

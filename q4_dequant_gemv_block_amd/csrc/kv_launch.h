@@ -79,10 +79,11 @@ struct AttnArgs {
 // How a call is cut: a rule on sizes alone, the same for the workspace's size
 // and the launch.
 struct AttnShape {
-    int rows;      // query rows (token, head of the group) of one item
+    int rows;      // query rows (token, head of the group) of one item: 16, 32 (k_attn), 128, 256 (k_attn_tile)
     int unit;      // keys of one unit of work
+    int step;      // keys a kernel takes at a time
     int grid;      // workgroups
-    size_t bytes;  // workspace
+    size_t bytes;  // workspace, 0 where every item is taken whole
 };
 bool attn_head_dim_ok(int head_dim);
 AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int max_query);
