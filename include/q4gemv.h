@@ -545,8 +545,10 @@ typedef struct q4_kv_batch {
     int seqs;             /* >= 1 */
     const int32_t* query_start;
     const int32_t* context_len;
-    int max_query;   /* most new tokens of a sequence, 0 if not known: chooses */
-    int max_context; /* longest context, 0 if not known: the kernel, not the result */
+    /* Most new tokens of a sequence and longest context, 0 if not known: they
+     * choose how the work is cut, and do not bound it. */
+    int max_query;
+    int max_context;
 } q4_kv_batch;
 
 /*
@@ -589,10 +591,11 @@ Q4_API q4_status q4_kv_append(const q4_kv_cache* cache, const q4_kv_batch* batch
                               int64_t tokens, const int32_t* positions, const double* inv_freq, int rot_dim,
                               int layout, float mscale, void* stream);
 
-/* Bytes of device workspace q4_attention_paged needs (0, with the error text
- * set, if the arguments are not valid). */
+/* Bytes of device workspace q4_attention_paged needs; 0 if none, or, with the
+ * error text set, if the arguments are not valid.  It depends on these sizes, on
+ * batch->max_query and max_context and on the current device, not on lengths. */
 Q4_API size_t q4_attention_paged_workspace_bytes(const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads,
-                                                 int64_t tokens);
+                                                 int64_t tokens, int64_t window);
 
 /*
  * out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j  over the cached keys j
@@ -606,8 +609,8 @@ Q4_API size_t q4_attention_paged_workspace_bytes(const q4_kv_cache* cache, const
  *   lse    : NULL, or tokens x q_heads binary32 (written): the natural log of
  *            the sum of exp(scale * q . k_j)
  *   scale  : finite, > 0;  window >= 0 (0: no window)
- *   workspace : q4_attention_paged_workspace_bytes(...) bytes of device memory,
- *            16-byte aligned; its contents on entry do not matter.  Calls that
+ *   workspace : q4_attention_paged_workspace_bytes(...) bytes of device memory
+ *            (may be NULL when that is 0), 16-byte aligned; its contents on entry do not matter.  Calls that
  *            may overlap in time need one each.
  *   head_dim 64, 96, 128 or 256; q_heads a multiple of kv_heads; the cache
  *   16-byte aligned with strides that are multiples of 8.

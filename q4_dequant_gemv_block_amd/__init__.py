@@ -171,7 +171,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.q4_kv_append.restype = st
     lib.q4_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, vp, vp, i32, i32, f32, vp]
     lib.q4_attention_paged_workspace_bytes.restype = ctypes.c_size_t
-    lib.q4_attention_paged_workspace_bytes.argtypes = [vp, vp, i32, i64]
+    lib.q4_attention_paged_workspace_bytes.argtypes = [vp, vp, i32, i64, i64]
     lib.q4_attention_paged.restype = st
     lib.q4_attention_paged.argtypes = [vp, vp, vp, vp, vp, i32, i64, f32, i64, vp, ctypes.c_size_t, vp]
     if path == LIB_PATH:
@@ -813,10 +813,10 @@ def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
     return q_out
 
 
-def attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, tokens: int) -> int:
-    """Bytes of the workspace q4_attention_paged needs for these sizes."""
+def attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, tokens: int, window: int = 0) -> int:
+    """Bytes of the workspace q4_attention_paged needs for these sizes (0: none)."""
     with torch.cuda.device(cache.device):  # the work is cut for this device
-        n = int(load_library().q4_attention_paged_workspace_bytes(cache._ref, batch._ref, q_heads, tokens))
+        n = int(load_library().q4_attention_paged_workspace_bytes(cache._ref, batch._ref, q_heads, tokens, window))
     if n == 0 and last_error():
         raise Q4Error(Q4_ERR_INVALID_ARG, last_error())
     return n
@@ -852,7 +852,7 @@ def q4_attention_paged(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: f
         lp = _ptr(lse, torch.float32, "lse")
     lib = load_library()
     if workspace is None:
-        need = lib.q4_attention_paged_workspace_bytes(cache._ref, batch._ref, h, t)
+        need = lib.q4_attention_paged_workspace_bytes(cache._ref, batch._ref, h, t, window)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     elif workspace.device != dev:
         raise ValueError("workspace must be on %s" % dev)

@@ -66,7 +66,7 @@ struct Keys {
 };
 
 template <typename T, int D, int NR>
-__global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut cut) {
+__global__ void __launch_bounds__(kThreads, NR * D <= 192 ? 2 : 1) k_attn(const AttnArgs a, const Cut cut) {
     constexpr int ROWS = 16 * NR;
     constexpr int PER = D / 16;      // elements of V a lane holds of a key
     constexpr int KS = D / 32;       // k-steps of the first product
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
         for (int r = 0; r < NR; ++r) {
             const int row = row0 + 16 * r + n16;
             const int rc = min(row, row0 + rows - 1);
-            const int i = rc / a.group, h = head * a.group + rc - i * a.group;
+            const int i = (int)cut.group.div(rc), h = head * a.group + rc - i * a.group;
             pos[r] = row < row0 + rows ? past + i : -1;
             const char* src = a.q.data + ((int64_t)(seq.row0 + i) * a.q.token_stride + (int64_t)h * a.q.head_stride + 8 * q) * 2;
 #pragma unroll
@@ -173,19 +173,19 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
             if (ragged) {
                 const int first = t + 8 * q;
                 // keys that do not belong here: their values could be anything
+                const uint32_t here = pv_now < 0 ? 0u : (uint32_t)bits_between(0, k_hi - first);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (pv_now < 0 || first + j >= k_hi)
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t mask = bit_mask(here, j);
 #pragma unroll
-                        for (int e = 0; e < PER / 2; ++e) x.v[j][e] = 0;
+                    for (int e = 0; e < PER / 2; ++e) x.v[j][e] &= mask;
+                }
 #pragma unroll
-                for (int r = 0; r < NR; ++r)
+                for (int r = 0; r < NR; ++r) {
+                    const uint32_t seen = here & (uint32_t)bits_between(a.window ? pos[r] - a.window + 1 - first : 0, pos[r] + 1 - first);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int key = first + j;
-                        const bool seen = key < k_hi && key <= pos[r] && pv_now >= 0 && (!a.window || key > pos[r] - a.window);
-                        s[r][j] = seen ? s[r][j] : kNone;
-                    }
+                    for (int j = 0; j < 8; ++j) s[r][j] = keep_seen(s[r][j], bit_mask(seen, j));
+                }
             }
             uint32_t p[NR][4];
 #pragma unroll
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
                 if (__ballot(top > m[r] + kRaise)) {
                     top = fmaxf(top, __shfl_xor(top, 16));
                     top = fmaxf(top, __shfl_xor(top, 32));
-                    const float raised = fmaxf(top, m[r]);
+                    const float raised = top > m[r] + kRaise ? top : m[r];  // each row by itself
                     const float f = raised == kNone ? 1.0f : __builtin_amdgcn_exp2f(m[r] - raised);
                     m[r] = raised;
                     l[r] *= f;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
-                    for (int e = 0; e < PER / 2; ++e) any |= nonfinite<T>(x.v[j][e]);
+                    for (int e = 0; e < PER / 2; ++e) any |= nonfinite_bits<T>(x.v[j][e]);
                 if (__ballot(any != 0)) {
                     // through this wave's part of LDS: rare, and so free of registers
                     float* so = sh + wave * ROWS * LD;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
                             load_elems<T, 1>(a.cache.v + (at + d) * 2, reinterpret_cast<float(&)[1]>(v));
                             if (__builtin_isfinite(v)) continue;
                             for (int row = 0; row < rows; ++row) {
-                                const int pr = past + (row0 + row) / a.group;
+                                const int pr = past + (int)cut.group.div(row0 + row);
                                 if (t + k <= pr && (!a.window || t + k > pr - a.window)) so[row * LD + d] += sp[row * kStep + k] * v;
                             }
                         }
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
             }
             if (whole) {
                 const float f = row_scale(sum);
-                const int i = (row0 + row) / a.group, h = head * a.group + row0 + row - i * a.group;
+                const int i = (int)cut.group.div(row0 + row), h = head * a.group + row0 + row - i * a.group;
                 float v[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
                 store_elems<T, 4>(a.out.data + ((int64_t)(seq.row0 + i) * a.out.token_stride + (int64_t)h * a.out.head_stride + d) * 2, v);
                 if (a.lse && d == 0)
@@ -333,95 +333,95 @@ __global__ void __launch_bounds__(kThreads) k_attn(const AttnArgs a, const Cut c
     }
 }
 
-// Joins the parts of the items that several ranges share: one workgroup an
-// item (blockIdx.x; those behind the last item end at once), its rows in turn.
+// Joins the parts of the items that several ranges share.  Workgroup (w, y)
+// takes the item that begins in range w and does not end there, if there is
+// one, and every gridDim.y-th batch of its rows: one SG-lane group a row where
+// the parts are few, all groups on one row where they are many.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, const Cut cut, uint32_t slots) {
     constexpr int SG = D <= 64 ? 16 : D <= 128 ? 32 : 64;  // lanes of a row
     constexpr int NSG = kThreads / SG;
     __shared__ f4 sh_o[NSG][SG];
     __shared__ float sh_s[NSG];
-    const int lane = threadIdx.x & 63;
-    // the sequence that holds this item, its first item and its first unit
-    int b = -1;
-    uint32_t item = blockIdx.x, begin = 0, total = 0;
-    for (int b0 = 0; b0 < a.batch.seqs; b0 += 64) {
-        Seq s;
-        s.tiles = s.units = 0;
-        if (b0 + lane < a.batch.seqs) cut_sequence(cut, a.batch, b0 + lane, &s);
-        const uint32_t items = (uint32_t)cut.kv_heads * s.tiles, units = items * s.units;
-        uint32_t ii = items, uu = units;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const uint32_t ti = (uint32_t)__shfl_up((int)ii, o), tu = (uint32_t)__shfl_up((int)uu, o);
-            if (lane >= o) {
-                ii += ti;
-                uu += tu;
-            }
-        }
-        const uint64_t past = b < 0 ? __ballot(ii > item) : 0;
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            b = b0 + l;
-            begin = total + (uint32_t)__shfl((int)(uu - units), l);
-            item -= (uint32_t)__shfl((int)(ii - items), l);
-        } else if (b < 0) {
-            item -= (uint32_t)__shfl((int)ii, 63);
-        }
-        total += (uint32_t)__shfl((int)uu, 63);
-    }
-    b = __builtin_amdgcn_readfirstlane(b);
-    if (b < 0) return;
-    const uint32_t grid = min(slots, total);
-    Seq seq;
-    cut_sequence(cut, a.batch, b, &seq);
-    begin = (uint32_t)__builtin_amdgcn_readfirstlane((int)(begin + item * seq.units));
-    // first and last range with units of the item
-    auto range_of = [&](uint32_t unit) {
-        uint32_t w = (uint32_t)((uint64_t)unit * grid / total);
-        while (range_begin(total, w + 1, grid) <= unit) ++w;
-        while (range_begin(total, w, grid) > unit) --w;
-        return w;
-    };
-    const uint32_t w0 = range_of(begin), w1 = range_of(begin + seq.units - 1);
-    if (w0 == w1) return;
+    Work work;
+    work.sum(cut, a.batch);
+    const uint32_t total = work.total, grid = min(slots, total), w0 = blockIdx.x;
+    if (w0 + 1 >= grid) return;
+    const uint32_t border = range_begin(total, w0 + 1, grid);
+    if (!work.find(cut, a.batch, border)) return;
+    const Seq& seq = work.seq;
+    const uint32_t item = (border - work.begin) / (uint32_t)seq.units;
+    const uint32_t first = work.begin + item * seq.units, last = first + seq.units - 1;
+    if (first == border || first < range_begin(total, w0, grid)) return;
+    uint32_t w1 = (uint32_t)((uint64_t)last * grid / total);  // the range that holds `last`
+    while (range_begin(total, w1 + 1, grid) <= last) ++w1;
+    while (range_begin(total, w1, grid) > last) --w1;
     Item it;
     place_item(cut, seq, item, &it);
-    const int head = it.head, row0 = it.row0, rows = it.rows;
-    const Parts<D> parts(a.workspace, (int)slots, cut.rows);
-    const int g = threadIdx.x / SG, d = (threadIdx.x & (SG - 1)) * 4;
-    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-        float top = kNone;
-        for (uint32_t w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, parts.ml[((int64_t)2 * w + (w == w0)) * cut.rows + row].x);
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-        const float ref = top == kNone ? 0.0f : top;
+    const int R = 1 << cut.rows_log2;
+    const Parts<D> parts(a.workspace, (int)slots, R);
+    const int g = threadIdx.x / SG, lane = threadIdx.x & (SG - 1), d = lane * 4;
+    const bool many = w1 - w0 >= NSG;
+    const int stride = many ? 1 : NSG;
+    for (int row = blockIdx.y * stride + (many ? 0 : g); row < it.rows; row += gridDim.y * stride) {
+        // part of range w: slot 2 w + 1 in the item's first range, else 2 w
+        auto slot_of = [&](uint32_t w) { return ((int64_t)2 * w + (w == w0)) * R + row; };
+        const uint32_t from = w0 + (many ? g : 0), by = many ? NSG : 1;
+        float top = kNone, sum = 0.0f;
         f4 o = {0, 0, 0, 0};
-        float sum = 0.0f;
-        for (uint32_t w = w0 + g; w <= w1; w += NSG) {
-            const int64_t slot = (int64_t)2 * w + (w == w0);
-            const f2 ml = parts.ml[slot * cut.rows + row];
-            const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-            sum += f * ml.y;
-            if (d < D) o += f * *reinterpret_cast<const f4*>(&parts.o[(slot * cut.rows + row) * D + d]);
-        }
-        sh_o[g][threadIdx.x & (SG - 1)] = o;
-        if (d == 0) sh_s[g] = sum;
-        __syncthreads();
-        if (g == 0 && d < D) {
+        for (uint32_t w = from; w <= w1; w += 4 * by) {
+            f2 ml[4];
+            f4 po[4];
 #pragma unroll
-            for (int k = 1; k < NSG; ++k) {
-                o += sh_o[k][threadIdx.x];
-                sum += sh_s[k];
+            for (int k = 0; k < 4; ++k) {
+                const bool in = w + k * by <= w1;
+                ml[k] = in ? parts.ml[slot_of(w + k * by)] : f2{kNone, 0.0f};
+                po[k] = in && d < D ? *reinterpret_cast<const f4*>(&parts.o[slot_of(w + k * by) * D + d]) : f4{0, 0, 0, 0};
             }
+            const float raised = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+            const float ref = raised == kNone ? 0.0f : raised;
+            const float keep = __builtin_amdgcn_exp2f(top - ref);
+            sum *= keep;
+            o *= keep;
+            top = raised;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = __builtin_amdgcn_exp2f(ml[k].x - ref);
+                sum += f * ml[k].y;
+                o += f * po[k];
+            }
+        }
+        if (many) {
+            // all groups' sums to the largest maximum, then over the groups
+            __shared__ float sh_m[NSG];
+            if (lane == 0) sh_m[g] = top;
+            __syncthreads();
+            float all = sh_m[0];
+#pragma unroll
+            for (int k = 1; k < NSG; ++k) all = fmaxf(all, sh_m[k]);
+            const float f = __builtin_amdgcn_exp2f(top - (all == kNone ? 0.0f : all));
+            top = all;
+            sh_o[g][lane] = o * f;
+            if (lane == 0) sh_s[g] = sum * f;
+            __syncthreads();
+            if (g == 0) {
+                o = sh_o[0][lane];
+                sum = sh_s[0];
+#pragma unroll
+                for (int k = 1; k < NSG; ++k) {
+                    o += sh_o[k][lane];
+                    sum += sh_s[k];
+                }
+            }
+            __syncthreads();
+        }
+        if ((!many || g == 0) && d < D) {
             const float f = row_scale(sum);
-            const int i = (row0 + row) / a.group, h = head * a.group + row0 + row - i * a.group;
+            const int i = (int)cut.group.div(it.row0 + row), h = it.head * a.group + it.row0 + row - i * a.group;
             float v[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
             store_elems<T, 4>(a.out.data + ((int64_t)(seq.row0 + i) * a.out.token_stride + (int64_t)h * a.out.head_stride + d) * 2, v);
-            if (a.lse && d == 0)
-                a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = row_lse(top, sum);
+            if (a.lse && d == 0) a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = row_lse(top, sum);
         }
-        __syncthreads();
     }
 }
 
@@ -444,12 +444,12 @@ int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int64_t to
 
 Cut make_cut(const AttnArgs& a, const AttnShape& s) {
     Cut c = {};
-    c.rows = s.rows;
-    c.unit = s.unit;
+    c.rows_log2 = __builtin_ctz(s.rows);
+    c.unit_log2 = __builtin_ctz(s.unit);
     c.step = s.step;
-    c.group = a.group;
     c.window = a.window;
-    c.kv_heads = a.cache.kv_heads;
+    c.group = FastDiv((uint32_t)a.group);
+    c.kv_heads = FastDiv((uint32_t)a.cache.kv_heads);
     c.capacity = (int)((int64_t)a.batch.table_pages * a.cache.page_size.d);
     c.tokens = a.tokens;
     return c;
@@ -475,9 +475,8 @@ hipError_t launch_dim(const AttnArgs& a, const AttnShape& shape, hipStream_t s) 
     else if constexpr (D <= 128)
         e = launch<T, D, 2>(a, shape, s);
     if (e != hipSuccess || !shape.bytes) return e;
-    const int64_t items = item_bound(a.cache, a.batch, a.q_heads, a.tokens, shape.rows);
-    const int by = (int)std::min<int64_t>(shape.rows, std::max<int64_t>(1, 4096 / std::max<int64_t>(1, items)));
-    hipLaunchKernelGGL((k_attn_join<T, D>), dim3((unsigned)items, by), dim3(kThreads), 0, s, a, make_cut(a, shape), (uint32_t)shape.grid);
+    const int by = std::min(16, (shape.most_rows + 7) / 8);
+    hipLaunchKernelGGL((k_attn_join<T, D>), dim3((unsigned)shape.grid - 1, by), dim3(kThreads), 0, s, a, make_cut(a, shape), (uint32_t)shape.grid);
     return hipGetLastError();
 }
 
@@ -506,33 +505,57 @@ hipError_t LdsLimit::raise(const void* kernel, size_t bytes) {
 
 bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
 
-AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int max_query) {
+// Cutting costs what writing the parts and joining them takes, about kJoin us
+// (a launch that waits for the first one) and 2 x rows of parts a workgroup;
+// taking items whole costs what the last workgroups run alone.  Both are
+// estimated from the longest context and the most new tokens of a sequence, as
+// far as the caller knows them: measured, a workgroup of k_attn takes about 1 us
+// for 128 keys of 128 elements, one of k_attn_tile 1.3 us for 64 keys and 128 or 256 rows.
+AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
     AttnShape s;
-    const int64_t group = q_heads / c.kv_heads;
-    const int64_t most = std::min<int64_t>(max_query > 0 ? max_query : tokens, tokens) * group;
+    const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
+    const int64_t longest = max_query > 0 ? std::min<int64_t>(max_query, tokens) : tokens;  // new tokens of a sequence
+    const int64_t most = longest * group;
+    const int64_t seqs = std::min<int64_t>(b.seqs, tokens);
     const int cus = compute_units();
-    bool split = true;
+    double us;  // of a whole item
+    int slots;  // workgroups that run at a time
+    int64_t keys = max_context > 0 ? std::min<int64_t>(max_context, capacity) : capacity;
+    if (window) keys = std::min<int64_t>(keys, window + longest);
     if (most <= (c.head_dim > 128 ? 16 : 32)) {
         s.rows = most <= 16 ? 16 : 32;
         s.step = kStep;
         s.unit = kWaves * kStep;  // a step of each wave
-        s.grid = cus * (s.rows == 16 && c.head_dim <= 128 ? 2 : 1);
+        slots = cus * (s.rows / 16 * c.head_dim <= 192 ? 2 : 1);
+        us = keys / 128.0 * c.head_dim / 128;
     } else {
         s.step = s.unit = 64;
-        s.rows = c.head_dim > 128 || item_bound(c, b, q_heads, tokens, 256) < cus ? 128 : 256;
-        s.grid = cus;
-        // Items enough to fill the machine are taken whole, the longest first.
-        if (item_bound(c, b, q_heads, tokens, s.rows) - (int64_t)c.kv_heads * std::min<int64_t>(b.seqs, tokens) >= 2 * cus) {
-            split = false;
-            s.unit = 1 << 30;
-            s.grid = (int)item_bound(c, b, q_heads, tokens, s.rows);
-        }
+        const int64_t items256 = c.kv_heads * (tokens * group / 256 + seqs / 2);
+        s.rows = c.head_dim > 128 || items256 < 2 * cus ? 128 : 256;
+        slots = s.rows == 128 && c.head_dim <= 128 ? 2 * cus : cus;
+        us = 1.3 * (keys + 63) / 64 * c.head_dim / 128;
+    }
+    s.most_rows = (int)std::min<int64_t>(s.rows, most);
+    // Whole: the longest item, or all of them (a sequence's rows see its context
+    // less half of the new tokens on average) and half an item for what the last
+    // ones run alone.  Cut: ranges of equal units, of which an item counts as
+    // many as its sequence's longest.
+    constexpr double kJoin = 6.0;
+    const double items = (double)c.kv_heads * (tokens * group + (s.rows - 1) * seqs / 2) / s.rows;
+    const double mean = window ? us : us * (1.0 - 0.5 * longest / std::max<double>(keys, longest));
+    const bool whole = items > slots ? mean * items / slots + 0.5 * us <= us * items / slots + kJoin + s.rows / 32
+                                     : us <= us * items / slots + kJoin + s.rows / 32;
+    const int64_t bound = item_bound(c, b, q_heads, tokens, s.rows);
+    if (whole && bound < (int64_t(1) << 31)) {
+        s.unit = 1 << 30;
+        s.grid = (int)bound;
+        s.bytes = 0;
+        return s;
     }
     // Larger units where this many would pass 31 bits.
-    const int64_t capacity = (int64_t)b.table_pages * c.page_size.d;
-    const int64_t items = item_bound(c, b, q_heads, tokens, s.rows);
-    while (s.unit < (1 << 30) && items * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;
-    s.bytes = split ? (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + sizeof(f2)) : 0;
+    while (s.unit < (1 << 30) && bound * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;
+    s.grid = slots;
+    s.bytes = (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + sizeof(f2));
     return s;
 }
 

@@ -39,11 +39,18 @@ __device__ __forceinline__ float unpack_sum(uint32_t v) {
     return (float)x[0] + (float)x[1];
 }
 
-// The halves of a dword that hold NaN or an infinity, as a mask.
+// Bits 15 and 31: the halves of a dword that hold NaN or an infinity (an
+// exponent of ones carries into the sign's place), and those halves as a mask.
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t v) {
+    constexpr uint32_t e = std::is_same<T, F16>::value ? 0x7C007C00u : 0x7F807F80u;
+    constexpr uint32_t one = std::is_same<T, F16>::value ? 0x04000400u : 0x00800080u;
+    return ((v & e) + one) & 0x80008000u;
+}
 template <typename T>
 __device__ __forceinline__ uint32_t nonfinite(uint32_t v) {
-    constexpr uint32_t e = std::is_same<T, F16>::value ? 0x7C00u : 0x7F80u;
-    return ((v & e) == e ? 0xFFFFu : 0u) | ((v & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
+    const uint32_t b = nonfinite_bits<T>(v);
+    return (b << 1) - (b >> 15);
 }
 template <typename T>
 __device__ __forceinline__ float half_of(uint32_t v, int high) {
@@ -57,81 +64,33 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// How a call is cut (AttnShape with its numbers as shifts and products).
+struct Cut {
+    int rows_log2, unit_log2, step;  // an item's keys begin at a multiple of step
+    int window, capacity;            // capacity: tokens a row of the block table holds
+    FastDiv group, kv_heads;
+    int64_t tokens;
+};
+
 // What one sequence asks for.
 struct Seq {
     int b, row0, n, ctx;  // first row, new tokens, context
     int tiles, units;     // items of a kv head, units of an item
 };
 
-struct Cut {
-    int rows, unit, step, group, window, kv_heads, capacity;  // an item's keys begin at a multiple of step
-    int64_t tokens;
-};
-
-// n new tokens with the given context: items of a kv head and units of an item
-// (the most that any of its items has; a unit that lies behind an item's last
-// visible key holds no work).
-__device__ __forceinline__ void cut_sequence(const Cut& c, const BatchArg& batch, int b, Seq* s) {
-    const int first = batch.query_start[b], last = batch.query_start[b + 1];
-    s->b = b;
-    s->row0 = first;
-    s->ctx = batch.context_len[b];
-    s->n = first < 0 || last > c.tokens || last < first ? 0 : last - first;
-    const int keys = max(0, min(s->ctx, c.capacity));
-    int span = keys;
+// Items of a kv head and units of an item (the most that any of the sequence's
+// items has: a unit behind an item's last visible key holds no work).
+__device__ __forceinline__ void cut_sequence(const Cut& c, Seq* s) {
+    int span = max(0, min(s->ctx, c.capacity));
     if (c.window) {
-        const int64_t most = (int64_t)c.window + (c.rows - 1) / c.group + 1 + c.step;
-        span = (int)min((int64_t)keys, most);
+        const int64_t most = (int64_t)c.window + (int)c.group.div((1u << c.rows_log2) - 1) + 1 + c.step;
+        span = (int)min((int64_t)span, most);
     }
-    s->tiles = (int)(((int64_t)s->n * c.group + c.rows - 1) / c.rows);
-    s->units = s->n ? max(1, (span + c.unit - 1) / c.unit) : 0;
+    s->tiles = (int)(((int64_t)s->n * c.group.d + (1 << c.rows_log2) - 1) >> c.rows_log2);
+    s->units = s->n ? max(1, (int)(((int64_t)span + (1 << c.unit_log2) - 1) >> c.unit_log2)) : 0;
 }
 
-__device__ __forceinline__ uint32_t seq_units(const Cut& c, const BatchArg& batch, int b) {
-    if (b >= batch.seqs) return 0;
-    Seq s;
-    cut_sequence(c, batch, b, &s);
-    return (uint32_t)c.kv_heads * s.tiles * s.units;
-}
-
-__device__ __forceinline__ uint32_t wave_sum_u32(uint32_t v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += (uint32_t)__shfl_xor((int)v, o);
-    return v;
-}
-
-// The sequence that holds unit `at`, and the first unit of that sequence; by
-// whole waves, 64 sequences at a time.
-__device__ __forceinline__ int find_unit(const Cut& c, const BatchArg& batch, uint32_t at, uint32_t* begin) {
-    const int lane = threadIdx.x & 63;
-    uint32_t base = 0;
-    for (int b0 = 0; b0 < batch.seqs; b0 += 64) {
-        const uint32_t u = seq_units(c, batch, b0 + lane);
-        uint32_t incl = u;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const uint32_t t = (uint32_t)__shfl_up((int)incl, o);
-            if (lane >= o) incl += t;
-        }
-        const uint64_t past = __ballot(base + incl > at);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            *begin = base + (uint32_t)__shfl((int)(incl - u), l);
-            return b0 + l;
-        }
-        base += (uint32_t)__shfl((int)incl, 63);
-    }
-    *begin = base;
-    return -1;
-}
-
-__device__ __forceinline__ uint32_t all_units(const Cut& c, const BatchArg& batch) {
-    uint32_t sum = 0;
-    for (int b0 = 0; b0 < batch.seqs; b0 += 64) sum += seq_units(c, batch, b0 + (int)(threadIdx.x & 63));
-    return (uint32_t)__builtin_amdgcn_readfirstlane((int)wave_sum_u32(sum));
-}
-
-// First unit of workgroup w's range.
+// First unit of range w of `grid`.
 __device__ __forceinline__ uint32_t range_begin(uint32_t total, uint32_t w, uint32_t grid) {
     return (uint32_t)((uint64_t)total * w / grid);
 }
@@ -149,49 +108,106 @@ struct Item {
 // what takes longest should start first), their kv heads side by side (with 8
 // XCDs taking workgroups in turn, an XCD's L2 then sees few heads).
 __device__ __forceinline__ void place_item(const Cut& c, const Seq& seq, uint32_t item, Item* x) {
-    const int tile = seq.tiles - 1 - (int)(item / (uint32_t)c.kv_heads);
-    x->head = (int)(item % (uint32_t)c.kv_heads);
-    x->row0 = tile * c.rows;
-    x->rows = min(c.rows, seq.n * c.group - x->row0);
+    const int up = (int)c.kv_heads.div(item);
+    x->head = (int)item - up * (int)c.kv_heads.d;
+    x->row0 = (seq.tiles - 1 - up) << c.rows_log2;
+    x->rows = min(1 << c.rows_log2, seq.n * (int)c.group.d - x->row0);
 }
 
-// The items of workgroup blockIdx.x's range.
+// The call's work as whole waves see it: each lane holds the lengths of one of
+// 64 sequences (read once where there are no more), a wave's scan finds the
+// sequence of a unit.
 struct Work {
-    uint32_t lo, hi, begin;
+    uint32_t total;  // units of all sequences
+    uint32_t begin;  // first unit of seq
     Seq seq;
+    uint32_t lo, hi;  // the units left of this workgroup's range
 
+    int base;               // sequence of lane 0
+    int l_row0, l_n, l_ctx; // this lane's sequence
+    uint32_t l_units, l_sum; // its units, and those of the lanes up to it
+
+    __device__ __forceinline__ void load(const Cut& c, const BatchArg& batch, int b0) {
+        const int lane = threadIdx.x & 63;
+        base = b0;
+        Seq s = {};
+        if (b0 + lane < batch.seqs) {
+            const int first = batch.query_start[b0 + lane], last = batch.query_start[b0 + lane + 1];
+            s.ctx = batch.context_len[b0 + lane];
+            s.row0 = first;
+            s.n = first < 0 || last > c.tokens || last < first ? 0 : last - first;
+        }
+        cut_sequence(c, &s);
+        l_row0 = s.row0;
+        l_n = s.n;
+        l_ctx = s.ctx;
+        l_units = l_sum = c.kv_heads.d * s.tiles * s.units;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t t = (uint32_t)__shfl_up((int)l_sum, o);
+            if (lane >= o) l_sum += t;
+        }
+    }
+    __device__ __forceinline__ void pick(const Cut& c, const BatchArg& batch, int b) {
+        if (b - base >= 64) load(c, batch, b);
+        seq.b = b;
+        seq.row0 = __builtin_amdgcn_readlane(l_row0, b - base);
+        seq.n = __builtin_amdgcn_readlane(l_n, b - base);
+        seq.ctx = __builtin_amdgcn_readlane(l_ctx, b - base);
+        cut_sequence(c, &seq);
+    }
+    __device__ __forceinline__ void sum(const Cut& c, const BatchArg& batch) {
+        total = 0;
+        for (int b0 = 0; b0 < batch.seqs; b0 += 64) {
+            load(c, batch, b0);
+            total += (uint32_t)__builtin_amdgcn_readlane((int)l_sum, 63);
+        }
+    }
+    // Picks the sequence that holds a unit (below total).
+    __device__ __forceinline__ bool find(const Cut& c, const BatchArg& batch, uint32_t unit) {
+        begin = 0;
+        for (int b0 = 0; b0 < batch.seqs; b0 += 64) {
+            if (base != b0) load(c, batch, b0);
+            const uint64_t past = __ballot(begin + l_sum > unit);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                begin += (uint32_t)__builtin_amdgcn_readlane((int)(l_sum - l_units), l);
+                pick(c, batch, b0 + l);
+                return true;
+            }
+            begin += (uint32_t)__builtin_amdgcn_readlane((int)l_sum, 63);
+        }
+        return false;
+    }
+
+    // This workgroup's range; next() goes through its items.
     __device__ __forceinline__ bool start(const Cut& c, const BatchArg& batch) {
-        const uint32_t total = all_units(c, batch), grid = min((uint32_t)gridDim.x, total);  // no range is empty
+        sum(c, batch);
+        const uint32_t grid = min((uint32_t)gridDim.x, total);  // no range is empty
         if (blockIdx.x >= grid) return false;
         lo = range_begin(total, blockIdx.x, grid);
         hi = range_begin(total, blockIdx.x + 1, grid);
-        uint32_t first;
-        const int b = __builtin_amdgcn_readfirstlane(find_unit(c, batch, lo, &first));
-        begin = (uint32_t)__builtin_amdgcn_readfirstlane((int)first);
-        if (b < 0) return false;
-        cut_sequence(c, batch, b, &seq);
-        return true;
+        return find(c, batch, lo);
     }
-
     __device__ __forceinline__ bool next(const Cut& c, const BatchArg& batch, Item* x) {
         if (lo >= hi) return false;
-        while (lo - begin >= (uint32_t)c.kv_heads * seq.tiles * seq.units) {
-            begin += (uint32_t)c.kv_heads * seq.tiles * seq.units;
+        while (lo - begin >= c.kv_heads.d * seq.tiles * seq.units) {
+            begin += c.kv_heads.d * seq.tiles * seq.units;
             if (seq.b + 1 >= batch.seqs) return false;
-            cut_sequence(c, batch, seq.b + 1, &seq);
+            pick(c, batch, seq.b + 1);
         }
-        const uint32_t item = (lo - begin) / (uint32_t)seq.units;
+        const uint32_t item = seq.units == 1 ? lo - begin : (lo - begin) / (uint32_t)seq.units;
         x->u0 = (int)((lo - begin) - item * seq.units);
         x->u1 = (int)min((uint32_t)seq.units, x->u0 + (hi - lo));
         lo += x->u1 - x->u0;
         place_item(c, seq, item, x);
         x->past = seq.ctx - seq.n;
-        x->p_first = x->past + x->row0 / c.group;
-        x->p_last = x->past + (x->row0 + x->rows - 1) / c.group;
+        x->p_first = x->past + (int)c.group.div(x->row0);
+        x->p_last = x->past + (int)c.group.div(x->row0 + x->rows - 1);
         const int keys = max(0, min(min(seq.ctx, c.capacity), x->p_last + 1));
-        const int start = c.window ? max(0, x->p_first - c.window + 1) / c.step * c.step : 0;
-        x->k_lo = (int)min((int64_t)keys, start + (int64_t)x->u0 * c.unit);
-        x->k_hi = (int)min((int64_t)keys, start + (int64_t)x->u1 * c.unit);
+        const int start = c.window ? (max(0, x->p_first - c.window + 1) & -c.step) : 0;
+        x->k_lo = (int)min((int64_t)keys, start + ((int64_t)x->u0 << c.unit_log2));
+        x->k_hi = (int)min((int64_t)keys, start + ((int64_t)x->u1 << c.unit_log2));
         return true;
     }
 };
@@ -208,6 +224,19 @@ struct Parts {
         ml = reinterpret_cast<f2*>(o + (int64_t)2 * grid * rows_ * D);
     }
 };
+
+// Bits [from, to) of 64, clamped to them.
+__device__ __forceinline__ uint64_t bits_between(int from, int to) {
+    const uint64_t below_to = to <= 0 ? 0 : to >= 64 ? ~uint64_t(0) : (uint64_t(1) << to) - 1;
+    const uint64_t below_from = from <= 0 ? 0 : from >= 64 ? ~uint64_t(0) : (uint64_t(1) << from) - 1;
+    return below_to & ~below_from;
+}
+// Bit i as 0 or ~0, and s where that is ~0, else -infinity: two vector
+// operations and no lane masks (dozens of which would spill scalar registers).
+__device__ __forceinline__ uint32_t bit_mask(uint32_t bits, int i) { return (uint32_t)__builtin_amdgcn_sbfe((int)bits, i, 1); }
+__device__ __forceinline__ float keep_seen(float s, uint32_t mask) {
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, s) & mask) | (0xFF800000u & ~mask));
+}
 
 // 1 / sum of a row's weights, 0 for a row that sees no key (NaN stays NaN).
 __device__ __forceinline__ float row_scale(float sum) { return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f; }

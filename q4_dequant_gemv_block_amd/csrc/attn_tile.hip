@@ -79,7 +79,7 @@ struct Layout {
 };
 
 template <typename T, int D, int NW>
-__global__ void __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) k_attn_tile(const AttnArgs a, const Cut cut) {
+__global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const AttnArgs a, const Cut cut) {
     typedef Layout<D> L;
     constexpr int ROWS = 32 * NW;
     constexpr int KS = D / 16;                         // k-steps of the first product
@@ -114,11 +114,11 @@ __global__ void __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) k_attn_tile(const At
         // this lane's query row and the wave's first and last positions
         const int row = it.row0 + 32 * wave + n;
         const int rc = min(row, it.row0 + it.rows - 1);
-        const int qi = rc / a.group, qh = it.head * a.group + rc - qi * a.group;
+        const int qi = (int)cut.group.div(rc), qh = it.head * a.group + rc - qi * a.group;
         const int pos = it.past + qi;
         const int w_rows = min(32, it.rows - 32 * wave);  // may be <= 0
-        const int w_first = it.past + (it.row0 + 32 * wave) / a.group;
-        const int w_last = it.past + (it.row0 + 32 * wave + w_rows - 1) / a.group;
+        const int w_first = it.past + (int)cut.group.div(it.row0 + 32 * wave);
+        const int w_last = it.past + (int)cut.group.div(it.row0 + 32 * wave + max(w_rows, 1) - 1);
         u4 qf[KS];
         {
             const char* src = a.q.data + ((int64_t)(seq.row0 + qi) * a.q.token_stride + (int64_t)qh * a.q.head_stride + 8 * h) * 2;
@@ -218,14 +218,20 @@ __global__ void __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) k_attn_tile(const At
                 if constexpr (D > 128) __builtin_amdgcn_sched_barrier(0);  // registers: no reads ahead
             }
             if (valid != 0xFF || t + kTile > min(it.k_hi, w_first + 1) || (a.window && t <= w_last - a.window)) {
+                uint64_t seen = bits_between(a.window ? pos - a.window + 1 - t : 0, min(it.k_hi, pos + 1) - t);
+                if (valid != 0xFF) {  // each group's bit as a byte
+                    uint64_t x = valid;
+                    x = (x | (x << 28)) & 0x0000000F0000000Full;
+                    x = (x | (x << 14)) & 0x0003000300030003ull;
+                    x = (x | (x << 7)) & 0x0101010101010101ull;
+                    seen &= x * 0xFF;
+                }
+                seen >>= 4 * h;  // the lane's keys are 8 (i / 4) + i % 4 of what is left
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = 32 * u + 8 * (i >> 2) + 4 * h + (i & 3), key = t + r;
-                        const bool seen = key < it.k_hi && key <= pos && (!a.window || key > pos - a.window) && ((valid >> (r >> 3)) & 1);
-                        s[u][i] = seen ? s[u][i] : kNone;
-                    }
+                    for (int i = 0; i < 16; ++i)
+                        s[u][i] = keep_seen(s[u][i], bit_mask((uint32_t)(seen >> (32 * u)), 8 * (i >> 2) + (i & 3)));
             }
             float top = s[0][0];
 #pragma unroll
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) k_attn_tile(const At
             top *= a.scale_log2;
             if (__ballot(top > m + kRaise)) {
                 top = fmaxf(top, __shfl_xor(top, 32));
-                const float raised = fmaxf(top, m);
+                const float raised = top > m + kRaise ? top : m;  // each row by itself
                 const float f = raised == kNone ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
                 m = raised;
                 l *= f;

@@ -166,11 +166,14 @@ q4::CacheArg cache_arg(const q4_kv_cache& c) {
     return r;
 }
 
+int window_arg(int64_t window) { return (int)std::min<int64_t>(window, int64_t(1) << 30); }  // a table holds no more
+
 q4::BatchArg batch_arg(const q4_kv_batch& b) {
     return q4::BatchArg{b.block_table, b.table_stride, b.table_pages, b.seqs, b.query_start, b.context_len};
 }
 
-q4_status check_attention(const char* fn, const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads, int64_t tokens) {
+q4_status check_attention(const char* fn, const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads, int64_t tokens,
+                          int64_t window) {
     q4_status st = check_cache(fn, cache);
     if (st) return st;
     st = check_batch(fn, batch, cache);
@@ -185,6 +188,7 @@ q4_status check_attention(const char* fn, const q4_kv_cache* cache, const q4_kv_
         return fail(Q4_ERR_MISALIGNED, "%s: the cache's strides must be multiples of 8", fn);
     if (cache->k_slot_stride > (1 << 26) || cache->v_slot_stride > (1 << 26))
         return fail(Q4_ERR_INVALID_ARG, "%s: the slots of the cache must not be more than 2^26 elements apart", fn);
+    if (window < 0) return fail(Q4_ERR_INVALID_ARG, "%s: window must not be negative", fn);
     return Q4_OK;
 }
 
@@ -283,17 +287,18 @@ q4_status q4_kv_append(const q4_kv_cache* cache, const q4_kv_batch* batch, const
     return hip_status(q4::launch_rope(a, k->type, cache->type, layout, static_cast<hipStream_t>(stream)), "q4_kv_append launch");
 }
 
-size_t q4_attention_paged_workspace_bytes(const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads, int64_t tokens) {
-    if (check_attention("q4_attention_paged_workspace_bytes", cache, batch, q_heads, tokens)) return 0;
+size_t q4_attention_paged_workspace_bytes(const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads, int64_t tokens,
+                                          int64_t window) {
+    if (check_attention("q4_attention_paged_workspace_bytes", cache, batch, q_heads, tokens, window)) return 0;
     ok();
-    return q4::attn_shape(cache_arg(*cache), batch_arg(*batch), q_heads, tokens, batch->max_query).bytes;
+    return q4::attn_shape(cache_arg(*cache), batch_arg(*batch), q_heads, tokens, window_arg(window), batch->max_query, batch->max_context).bytes;
 }
 
 q4_status q4_attention_paged(const q4_kv_cache* cache, const q4_kv_batch* batch, const q4_heads* q, const q4_heads* out,
                              float* lse, int q_heads, int64_t tokens, float scale, int64_t window, void* workspace,
                              size_t workspace_bytes, void* stream) {
     const char* fn = "q4_attention_paged";
-    q4_status st = check_attention(fn, cache, batch, q_heads, tokens);
+    q4_status st = check_attention(fn, cache, batch, q_heads, tokens, window);
     if (st) return st;
     const int dim = cache->head_dim;
     st = check_heads(fn, "q", q, tokens, q_heads, dim, false);
@@ -306,10 +311,9 @@ q4_status q4_attention_paged(const q4_kv_cache* cache, const q4_kv_batch* batch,
     if (!aligned(lse, 4)) return fail(Q4_ERR_MISALIGNED, "%s: lse must be 4-byte aligned", fn);
     if (!(scale > 0.0f) || !std::isfinite(scale) || !std::isfinite(scale * 1.4426950408889634f))
         return fail(Q4_ERR_INVALID_ARG, "%s: scale must be finite and > 0", fn);
-    if (window < 0) return fail(Q4_ERR_INVALID_ARG, "%s: window must not be negative", fn);
     const q4::CacheArg c = cache_arg(*cache);
     const q4::BatchArg b = batch_arg(*batch);
-    const q4::AttnShape shape = q4::attn_shape(c, b, q_heads, tokens, batch->max_query);
+    const q4::AttnShape shape = q4::attn_shape(c, b, q_heads, tokens, window_arg(window), batch->max_query, batch->max_context);
     if (shape.bytes) {
         if (!workspace || workspace_bytes < shape.bytes) return fail(Q4_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, shape.bytes);
         if (!aligned(workspace, 16)) return fail(Q4_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", fn);
@@ -337,7 +341,7 @@ q4_status q4_attention_paged(const q4_kv_cache* cache, const q4_kv_batch* batch,
     a.q_heads = q_heads;
     a.group = q_heads / cache->kv_heads;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.window = (int)std::min<int64_t>(window, int64_t(1) << 30);  // a table holds no more
+    a.window = window_arg(window);
     a.workspace = workspace;
     return hip_status(q4::launch_attention(a, shape, cache->type, static_cast<hipStream_t>(stream)), "q4_attention_paged launch");
 }

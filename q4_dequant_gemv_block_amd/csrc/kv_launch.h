@@ -80,13 +80,14 @@ struct AttnArgs {
 // and the launch.
 struct AttnShape {
     int rows;      // query rows (token, head of the group) of one item: 16, 32 (k_attn), 128, 256 (k_attn_tile)
+    int most_rows; // rows that an item has, as far as the caller knows
     int unit;      // keys of one unit of work
     int step;      // keys a kernel takes at a time
     int grid;      // workgroups
     size_t bytes;  // workspace, 0 where every item is taken whole
 };
 bool attn_head_dim_ok(int head_dim);
-AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int max_query);
+AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context);
 hipError_t launch_attention(const AttnArgs& a, const AttnShape& shape, int type, hipStream_t s);
 
 }  // namespace q4

@@ -133,17 +133,17 @@ def test_attention_refusals(lib, over, want, text):
 
 
 def test_attention_workspace(lib):
-    c, b = cache(), batch()
-    need = lib.q4_attention_paged_workspace_bytes(ref(c), ref(b), 8, 5)
+    c, b = cache(), batch(table_pages=2000, table_stride=2000, max_context=32000)
+    need = lib.q4_attention_paged_workspace_bytes(ref(c), ref(b), 8, 5, 0)
     assert q4.last_error() == ""
     args = (ref(c), ref(b), ref(heads(GIB)), ref(heads(2 * GIB)), None, 8, 5, 0.1, 0)
-    if need:
-        refused(lib, lib.q4_attention_paged(*args, None, 0, None), -3, "workspace")
-        refused(lib, lib.q4_attention_paged(*args, BASE + 80 * GIB, need - 1, None), -3, "workspace")
-        refused(lib, lib.q4_attention_paged(*args, BASE + 80 * GIB + 8, need, None), -2, "workspace")
-        refused(lib, lib.q4_attention_paged(*args, BASE + 16 * GIB, need, None), -1, "overlaps an input")
-        refused(lib, lib.q4_attention_paged(*args, BASE + 2 * GIB, need, None), -1, "must not overlap")
-    assert lib.q4_attention_paged_workspace_bytes(ref(cache(head_dim=80)), ref(b), 8, 5) == 0
+    assert need > 0  # a long context of few heads is cut
+    refused(lib, lib.q4_attention_paged(*args, None, 0, None), -3, "workspace")
+    refused(lib, lib.q4_attention_paged(*args, BASE + 80 * GIB, need - 1, None), -3, "workspace")
+    refused(lib, lib.q4_attention_paged(*args, BASE + 80 * GIB + 8, need, None), -2, "workspace")
+    refused(lib, lib.q4_attention_paged(*args, BASE + 16 * GIB, need, None), -1, "overlaps an input")
+    refused(lib, lib.q4_attention_paged(*args, BASE + 2 * GIB, need, None), -1, "must not overlap")
+    assert lib.q4_attention_paged_workspace_bytes(ref(cache(head_dim=80)), ref(b), 8, 5, 0) == 0
     assert "head_dim" in q4.last_error()
 
 
