@@ -541,7 +541,7 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
     // ones run alone.  Cut: ranges of equal units, of which an item counts as
     // many as its sequence's longest.
     constexpr double kJoin = 6.0;
-    const double items = (double)c.kv_heads * (tokens * group + (s.rows - 1) * seqs / 2) / s.rows;
+    const double items = (double)c.kv_heads * (seqs == 1 ? (tokens * group + s.rows - 1) / s.rows : (tokens * group + s.rows * seqs / 2) / s.rows);
     const double mean = window ? us : us * (1.0 - 0.5 * longest / std::max<double>(keys, longest));
     const bool whole = items > slots ? mean * items / slots + 0.5 * us <= us * items / slots + kJoin + s.rows / 32
                                      : us <= us * items / slots + kJoin + s.rows / 32;

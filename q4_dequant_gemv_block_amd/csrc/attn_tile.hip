@@ -66,6 +66,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 constexpr int kTile = 64;  // keys of a tile
+constexpr int kAhead = 4;  // steps of LDS reads ahead of the products
 
 template <int D>
 struct Layout {
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
 
         int stage = 0;
         int page_now = 0, page_next = 0;
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // the queries are there: no wait for them, and so for tiles, in the loop
         if (it.k_lo < it.k_hi) {
             page_now = pages(it.k_lo);
             fill(it.k_lo, page_now, 0);
@@ -209,13 +211,26 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
             // S^T
             f16v s[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+            // (reads run kAhead k-steps ahead of the products; the scheduler alone
+            // would wait for each read right after it)
+            u4 kf[kAhead][2];
+            auto read_k = [&](int k) {
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    s[u] = Mma32<T>::mma(*reinterpret_cast<const u4*>(tk + (at_k0 ^ (32 * k)) + u * 32 * L::row), qf[k], s[u]);
-                if constexpr (D > 128) __builtin_amdgcn_sched_barrier(0);  // registers: no reads ahead
+                for (int u = 0; u < 2; ++u)
+                    kf[k % kAhead][u] = *reinterpret_cast<const u4*>(tk + (at_k0 ^ (32 * k)) + u * 32 * L::row);
+            };
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) read_k(k);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) s[u] = Mma32<T>::mma(kf[k % kAhead][u], qf[k], s[u]);
+                if (k + kAhead < KS) read_k(k + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (valid != 0xFF || t + kTile > min(it.k_hi, w_first + 1) || (a.window && t <= w_last - a.window)) {
                 uint64_t seen = bits_between(a.window ? pos - a.window + 1 - t : 0, min(it.k_hi, pos + 1) - t);
@@ -288,19 +303,23 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
                 }
             }
             // O^T += V^T P^T
+            u4 vf[kAhead];
+            auto read_v = [&](int i) {
+                typedef __attribute__((address_space(3))) s4 l_s4;
+                typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+                const char* src = tv + (at_v0 ^ (64 * (i % DT))) + 16 * (i / DT) * L::row;
+                const u2 x = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)src));
+                const u2 y = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)(src + 8 * L::row)));
+                vf[i % kAhead] = u4{x.x, x.y, y.x, y.y};
+            };
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (D > 128) __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < kAhead; ++i) read_v(i);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    typedef __attribute__((address_space(3))) s4 l_s4;
-                    const char* src = tv + (at_v0 ^ (64 * d)) + 16 * k * L::row;
-                    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)src);
-                    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)(src + 8 * L::row));
-                    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-                    const u2 x = __builtin_bit_cast(u2, lo), y = __builtin_bit_cast(u2, hi);
-                    acc[d] = Mma32<T>::mma(u4{x.x, x.y, y.x, y.y}, p[k], acc[d]);
-                }
+            for (int i = 0; i < 4 * DT; ++i) {
+                acc[i % DT] = Mma32<T>::mma(vf[i % kAhead], p[i / DT], acc[i % DT]);
+                if (i + kAhead < 4 * DT) read_v(i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         __syncthreads();  // both tiles are read before the next item's
