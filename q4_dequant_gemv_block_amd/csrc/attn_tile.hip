@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 constexpr int kTile = 64;  // keys of a tile
-constexpr int kAhead = 4;  // steps of LDS reads ahead of the products
+constexpr int kAheadK = 4, kAheadV = 3;  // LDS reads ahead of the products
 
 template <int D>
 struct Layout {
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
     constexpr int LOADS = kTile / L::per_load / NW;    // loads of a wave for K, and for V, of a tile
     constexpr int GROUPS = 8 / NW;                     // groups of 8 keys they cover
     constexpr int PER_GROUP = LOADS / GROUPS;
-    extern __shared__ char sh[];  // [2][K, V][64][row], then a flag of each wave
+    extern __shared__ char sh[];  // K [2][64][row], V [2][64][row], then a flag of each wave
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int h = lane >> 5, n = lane & 31;
     const uint32_t sh0 = lds_address(sh);
@@ -135,45 +135,94 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
 
         // page of this lane's group (lane % 8) of the tile at key t
         auto pages = [&](int t) { return page_of(a.cache, a.batch, table, t + 8 * (lane & 7)); };
-        auto fill = [&](int t, int page8, int stage) {
+        // K (or V) of the tile at key t into one of its two places
+        auto fill = [&](int t, int page8, const char* base, int64_t page_stride, int64_t slot_stride, uint32_t to, bool values) {
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
                 const int group = wave * GROUPS + g;
                 const int page = max(__builtin_amdgcn_readlane(page8, group), 0);
                 const uint32_t p = (uint32_t)(t + 8 * group);
                 const uint32_t slot = p - a.cache.page_size.div(p) * a.cache.page_size.d;
-                const char* ks = kbase + ((int64_t)page * a.cache.k_page + (int64_t)slot * a.cache.k_slot) * 2;
-                const char* vs = vbase + ((int64_t)page * a.cache.v_page + (int64_t)slot * a.cache.v_slot) * 2;
+                const char* src = base + ((int64_t)page * page_stride + (int64_t)slot * slot_stride) * 2;
 #pragma unroll
                 for (int x = 0; x < PER_GROUP; ++x) {
                     const int r8 = x * L::per_load + lane / L::chunks;  // row of the group
                     const int r = 8 * group + r8;
-                    const int ck = (lane % L::chunks) ^ L::swz_k(r), cv = (lane % L::chunks) ^ L::swz_v(r);
-                    const uint32_t to = sh0 + stage * 2 * L::bytes + (8 * group + x * L::per_load) * L::row;
-                    if (D == 8 * L::chunks || ck < D / 8) load_to_lds(ks, r8 * (uint32_t)a.cache.k_slot * 2 + 16 * ck, to);
-                    if (D == 8 * L::chunks || cv < D / 8) load_to_lds(vs, r8 * (uint32_t)a.cache.v_slot * 2 + 16 * cv, to + L::bytes);
+                    const int c = (lane % L::chunks) ^ (values ? L::swz_v(r) : L::swz_k(r));
+                    if (D == 8 * L::chunks || c < D / 8)
+                        load_to_lds(src, r8 * (uint32_t)slot_stride * 2 + 16 * c, to + (8 * group + x * L::per_load) * L::row);
                 }
             }
         };
+        auto fill_k = [&](int t, int page8, int stage) {
+            fill(t, page8, kbase, a.cache.k_page, a.cache.k_slot, sh0 + stage * L::bytes, false);
+        };
+        auto fill_v = [&](int t, int page8, int stage) {
+            fill(t, page8, vbase, a.cache.v_page, a.cache.v_slot, sh0 + (2 + stage) * L::bytes, true);
+        };
+        // K fragments (k-step, 32-key half) in the order the products take them
+        u4 kf[kAheadK];
+        int at_k = at_k0, at_v = at_v0;  // in the tile to read next: toggled, its places are a power of 2 apart
+        auto read_k = [&](int i) {
+            kf[i % kAheadK] = *reinterpret_cast<const u4*>(sh + (at_k ^ (32 * (i >> 1))) + (i & 1) * 32 * L::row);
+        };
+        // V fragments (16 keys, 32 elements)
+        u4 vf[kAheadV];
+        auto read_v = [&](int i) {
+            typedef __attribute__((address_space(3))) s4 l_s4;
+            typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+            const char* src = sh + 2 * L::bytes + (at_v ^ (64 * (i % DT))) + 16 * (i / DT) * L::row;
+            const u2 x = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)src));
+            const u2 y = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)(src + 8 * L::row)));
+            vf[i % kAheadV] = u4{x.x, x.y, y.x, y.y};
+        };
+        int page0 = 0, page1 = 0, page2 = 0;  // pages of this tile, the next one and the one behind that
+        float top;                            // the maximum of the scores in `now` (no masks)
 
-        int stage = 0;
-        int page_now = 0, page_next = 0;
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // the queries are there: no wait for them, and so for tiles, in the loop
-        if (it.k_lo < it.k_hi) {
-            page_now = pages(it.k_lo);
-            fill(it.k_lo, page_now, 0);
-            page_next = pages(it.k_lo + kTile);
-        }
-        for (int t = it.k_lo; t < it.k_hi; t += kTile, stage ^= 1) {
-            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");  // the tile is there, the other one is read
-            const int page8 = page_now;
-            if (t + kTile < it.k_hi) {
-                page_now = page_next;
-                fill(t + kTile, page_now, stage ^ 1);
-                page_next = pages(t + 2 * kTile);
+        // S^T of a tile by itself.
+        float now[32];  // scores of this tile
+        auto scores = [&]() {
+            f16v s[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i) {
+                read_k(i);
+                s[i & 1] = Mma32<T>::mma(kf[i % kAheadK], qf[i >> 1], s[i & 1]);
             }
-            char* tk = sh + stage * 2 * L::bytes;
-            char* tv = tk + L::bytes;
+            top = s[0][0];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                now[i] = s[i >> 4][i & 15];
+                top = fmaxf(top, now[i]);
+            }
+        };
+
+        if (it.k_lo < it.k_hi) {
+            const int t = it.k_lo;
+            page0 = pages(t);
+            page1 = pages(t + kTile);
+            page2 = pages(t + 2 * kTile);
+            fill_k(t, page0, 0);
+            fill_v(t, page0, 0);
+            if (t + kTile < it.k_hi) fill_k(t + kTile, page1, 1);
+            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+            scores();
+        }
+        // One tile: its scores are in `now`, the next one's follow there.
+        int stage = 0;
+        for (int t = it.k_lo; t < it.k_hi; t += kTile, stage ^= 1, at_v ^= L::bytes) {
+            at_k ^= L::bytes;
+            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");  // V of this tile and K of the next are there, the places of K of this one and V of the last free
+            const bool more = t + kTile < it.k_hi;
+            const int page8 = page0;
+            if (more) fill_v(t + kTile, page1, stage ^ 1);
+            if (t + 2 * kTile < it.k_hi) fill_k(t + 2 * kTile, page2, stage);
+            page0 = page1;
+            page1 = page2;
+            page2 = pages(t + 3 * kTile);
             const uint32_t valid = (uint32_t)__ballot(page8 >= 0) & 0xFF;  // groups with a place
 
             // Tiles that not all of the workgroup's rows see whole: values of
@@ -182,6 +231,7 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
             bool odd = false;
             if (valid != 0xFF || t + kTile > min(it.k_hi, it.p_first + 1) || (a.window && t <= it.p_last - a.window)) {
                 bool mine = false;
+                char* tv = sh + (2 + stage) * L::bytes;
                 for (int u = threadIdx.x; u < kTile * L::chunks; u += NW * 64) {
                     const int r = u / L::chunks, c = (u % L::chunks) ^ L::swz_v(r);
                     if (c >= D / 8) continue;
@@ -204,34 +254,8 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
 #pragma unroll
                 for (int w = 0; w < NW; ++w) odd |= flags[w] != 0;
             }
-
-            if (w_rows <= 0 || t > w_last || (a.window && t + kTile <= w_first - a.window + 1)) continue;
-            // (for heads of 256 the addresses are made anew each tile: registers)
-            if constexpr (D > 128) asm volatile("" : "+v"(at_k0), "+v"(at_v0));
-            // S^T
-            f16v s[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
-            // (reads run kAhead k-steps ahead of the products; the scheduler alone
-            // would wait for each read right after it)
-            u4 kf[kAhead][2];
-            auto read_k = [&](int k) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    kf[k % kAhead][u] = *reinterpret_cast<const u4*>(tk + (at_k0 ^ (32 * k)) + u * 32 * L::row);
-            };
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) read_k(k);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) s[u] = Mma32<T>::mma(kf[k % kAhead][u], qf[k], s[u]);
-                if (k + kAhead < KS) read_k(k + kAhead);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int i = 0; i < kAheadK; ++i) read_k(i);
             if (valid != 0xFF || t + kTile > min(it.k_hi, w_first + 1) || (a.window && t <= w_last - a.window)) {
                 uint64_t seen = bits_between(a.window ? pos - a.window + 1 - t : 0, min(it.k_hi, pos + 1) - t);
                 if (valid != 0xFF) {  // each group's bit as a byte
@@ -242,17 +266,15 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
                     seen &= x * 0xFF;
                 }
                 seen >>= 4 * h;  // the lane's keys are 8 (i / 4) + i % 4 of what is left
+                top = kNone;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[u][i] = keep_seen(s[u][i], bit_mask((uint32_t)(seen >> (32 * u)), 8 * (i >> 2) + (i & 3)));
+                    for (int i = 0; i < 16; ++i) {
+                        now[16 * u + i] = keep_seen(now[16 * u + i], bit_mask((uint32_t)(seen >> (32 * u)), 8 * (i >> 2) + (i & 3)));
+                        top = fmaxf(top, now[16 * u + i]);
+                    }
             }
-            float top = s[0][0];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
             top *= a.scale_log2;
             if (__ballot(top > m + kRaise)) {
                 top = fmaxf(top, __shfl_xor(top, 32));
@@ -264,17 +286,56 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
                 for (int d = 0; d < DT; ++d) acc[d] *= f;
             }
             const float ref = m == kNone ? 0.0f : m;
+
+            // The next tile's scores on the matrix cores while this one's
+            // weights are made: a product, a read ahead and a share of the
+            // exponentials at a time, those in three stages (exponent, exp2,
+            // rounding and sum) so that no instruction waits for the one before.
             u4 p[4];
+            f16v next[2];
+            constexpr int STEPS = 2 * KS;
+            auto exponent = [&](int j) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = 8 * (k & 1) + 2 * j;
-                    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][i], a.scale_log2, -ref));
-                    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][i + 1], a.scale_log2, -ref));
-                    p[k][j] = pack2<T>(e0, e1);
-                    l = add_pair<T>(p[k][j], l);
+                for (int e = 0; e < 2; ++e) {
+                    now[2 * j + e] = __builtin_fmaf(now[2 * j + e], a.scale_log2, -ref);
                 }
+            };
+            auto power = [&](int j) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    now[2 * j + e] = __builtin_amdgcn_exp2f(now[2 * j + e]);
+                }
+            };
+            auto weight = [&](int j) {
+                p[j >> 2][j & 3] = pack2<T>(now[2 * j], now[2 * j + 1]);
+                l = add_pair<T>(p[j >> 2][j & 3], l);
+            };
+            // pairs [16 s / STEPS, 16 (s + 1) / STEPS) (rounded up) belong to step s
+            auto share = [&](int s, auto what) {
+#pragma unroll
+                for (int e = 0; e < (16 + STEPS - 1) / STEPS; ++e) {
+                    const int j = (16 * s + STEPS - 1) / STEPS + e;
+                    if (j < (16 * (s + 1) + STEPS - 1) / STEPS && j < 16) what(j);
+                }
+            };
+            share(0, exponent);
+            share(1, exponent);
+            share(0, power);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) next[u][i] = 0.0f;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                next[s & 1] = Mma32<T>::mma(kf[s % kAheadK], qf[s >> 1], next[s & 1]);
+                if (s + kAheadK < STEPS) read_k(s + kAheadK);
+                if (s >= STEPS - kAheadV) read_v(s - (STEPS - kAheadV));
+                share(s + 2, exponent);
+                share(s + 1, power);
+                share(s, weight);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             if (odd) {
                 // The elements that left the product, for the rows that see them.
                 for (int k = 0; k < kTile && t + k < it.k_hi; ++k) {
@@ -299,30 +360,28 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 if (sees && !__builtin_isfinite(v[i])) acc[d][4 * i4 + i] += weight * v[i];
+                            __builtin_amdgcn_sched_barrier(0);  // registers: one load at a time
                         }
                 }
             }
-            // O^T += V^T P^T
-            u4 vf[kAhead];
-            auto read_v = [&](int i) {
-                typedef __attribute__((address_space(3))) s4 l_s4;
-                typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-                const char* src = tv + (at_v0 ^ (64 * (i % DT))) + 16 * (i / DT) * L::row;
-                const u2 x = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)src));
-                const u2 y = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)(src + 8 * L::row)));
-                vf[i % kAhead] = u4{x.x, x.y, y.x, y.y};
-            };
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) read_v(i);
-            __builtin_amdgcn_sched_barrier(0);
+            // O^T += V^T P^T, and the maximum of the next tile's scores
+            top = next[0][0];
 #pragma unroll
             for (int i = 0; i < 4 * DT; ++i) {
-                acc[i % DT] = Mma32<T>::mma(vf[i % kAhead], p[i / DT], acc[i % DT]);
-                if (i + kAhead < 4 * DT) read_v(i + kAhead);
+                acc[i % DT] = Mma32<T>::mma(vf[i % kAheadV], p[i / DT], acc[i % DT]);
+                if (i + kAheadV < 4 * DT) read_v(i + kAheadV);
+#pragma unroll
+                for (int e = 0; e < (8 + DT - 1) / DT; ++e) {
+                    const int j = (8 * i + DT - 1) / DT + e;
+                    if (j < (8 * (i + 1) + DT - 1) / DT) {
+                        now[j] = next[j >> 4][j & 15];
+                        top = fmaxf(top, now[j]);
+                    }
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        __syncthreads();  // both tiles are read before the next item's
+        __syncthreads();  // all tiles are read before the next item's
 
         l += __shfl_xor(l, 32);
         if (32 * wave + n >= it.rows) continue;
