@@ -37,8 +37,7 @@ namespace q4 {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * 64;
+constexpr int kThreads = 256;     // of a joining workgroup
 constexpr int kStep = 32;         // keys of one step of a wave
 
 template <typename T>
@@ -65,9 +64,13 @@ struct Keys {
     uint32_t v[8][D / 32];     // key 8 q + t: elements D/16 i ..
 };
 
+// Waves of a workgroup of k_attn, one workgroup a CU: as many as its registers
+// allow (two a SIMD, one where 32 rows of 128 or heads of 256 take over 256).
+constexpr int attn_waves(int head_dim, int rows) { return head_dim * rows <= 16 * 192 ? 8 : 4; }
+
 template <typename T, int D, int NR>
-__global__ void __launch_bounds__(kThreads, NR * D <= 192 ? 2 : 1) k_attn(const AttnArgs a, const Cut cut) {
-    constexpr int ROWS = 16 * NR;
+__global__ void __launch_bounds__(attn_waves(D, 16 * NR) * 64) k_attn(const AttnArgs a, const Cut cut) {
+    constexpr int ROWS = 16 * NR, kWaves = attn_waves(D, ROWS), kThreads = 64 * kWaves;
     constexpr int PER = D / 16;      // elements of V a lane holds of a key
     constexpr int KS = D / 32;       // k-steps of the first product
     constexpr int LD = D + 4;
@@ -457,18 +460,19 @@ Cut make_cut(const AttnArgs& a, const AttnShape& s) {
 
 template <typename T, int D, int NR>
 hipError_t launch(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
-    constexpr size_t lds = (size_t)kWaves * 16 * NR * (D + 4 + 2 + kStep) * sizeof(float);
+    constexpr int waves = attn_waves(D, 16 * NR);
+    constexpr size_t lds = (size_t)waves * 16 * NR * (D + 4 + 2 + kStep) * sizeof(float);
     static LdsLimit limit;
     const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn<T, D, NR>), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn<T, D, NR>), dim3(shape.grid), dim3(kThreads), lds, s, a, make_cut(a, shape));
+    hipLaunchKernelGGL((k_attn<T, D, NR>), dim3(shape.grid), dim3(64 * waves), lds, s, a, make_cut(a, shape));
     return hipGetLastError();
 }
 
 template <typename T, int D>
 hipError_t launch_dim(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
     hipError_t e = hipErrorInvalidValue;
-    if (shape.rows >= 128)
+    if (shape.rows == 128)
         e = launch_attn_tile<T, D>(a, make_cut(a, shape), shape, s);
     else if (shape.rows == 16)
         e = launch<T, D, 1>(a, shape, s);
@@ -509,8 +513,8 @@ bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256
 // (a launch that waits for the first one) and 2 x rows of parts a workgroup;
 // taking items whole costs what the last workgroups run alone.  Both are
 // estimated from the longest context and the most new tokens of a sequence, as
-// far as the caller knows them: measured, a workgroup of k_attn takes about 1 us
-// for 128 keys of 128 elements, one of k_attn_tile 1.3 us for 64 keys and 128 or 256 rows.
+// far as the caller knows them: measured, a step of k_attn's
+// waves takes about 1 us, a workgroup of k_attn_tile (of two on a CU) 2.4 us for 64 keys.
 AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
     AttnShape s;
     const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
@@ -525,15 +529,14 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
     if (most <= (c.head_dim > 128 ? 16 : 32)) {
         s.rows = most <= 16 ? 16 : 32;
         s.step = kStep;
-        s.unit = kWaves * kStep;  // a step of each wave
-        slots = cus * (s.rows / 16 * c.head_dim <= 192 ? 2 : 1);
-        us = keys / 128.0 * c.head_dim / 128;
+        s.unit = attn_waves(c.head_dim, s.rows) * kStep;  // a step of each wave
+        slots = cus;
+        us = 1.0 * keys / s.unit;
     } else {
         s.step = s.unit = 64;
-        const int64_t items256 = c.kv_heads * (tokens * group / 256 + seqs / 2);
-        s.rows = c.head_dim > 128 || items256 < 2 * cus ? 128 : 256;
-        slots = s.rows == 128 && c.head_dim <= 128 ? 2 * cus : cus;
-        us = 1.3 * (keys + 63) / 64 * c.head_dim / 128;
+        s.rows = 128;
+        slots = c.head_dim <= 128 ? 2 * cus : cus;
+        us = 2.4 * (keys + 63) / 64 * c.head_dim / 128;
     }
     s.most_rows = (int)std::min<int64_t>(s.rows, most);
     // Whole: the longest item, or all of them (a sequence's rows see its context

@@ -2,10 +2,11 @@
 // paged cache: the same items, units and ranges as k_attn, in tiles that the
 // matrix cores are the bound of.
 //
-// A workgroup of NW waves holds 32 NW query rows, 32 a wave, and goes through
-// its keys 64 at a time.  A tile of K and V goes from HBM or L2 straight into LDS
-// (global_load_lds, 16 bytes a lane), two tiles deep, one barrier a tile.  The
-// products run on v_mfma_f32_32x32x16:
+// A workgroup of 4 waves holds 128 query rows, 32 a wave, and goes through its
+// keys 64 at a time; two of them share a CU (8 waves of 256 rows that share the
+// tiles were no faster: 606 us against 578 for a prompt of 8192).  K and V go from
+// HBM or L2 straight into LDS (global_load_lds, 16 bytes a lane), two tiles of each
+// deep, one barrier a tile.  The products run on v_mfma_f32_32x32x16:
 //   S^T = K Q^T: A = 32 keys from LDS, B = Q^T, which stays in registers;
 //   O^T = V^T P^T: A = V^T by the transposing LDS read (ds_read_b64_tr_b16: 16
 //     lanes read 4 keys of 16 elements and get one element's 4 keys each), B =
@@ -15,7 +16,9 @@
 // LDS rows are as long as a head; the 16-byte chunk c of row r lies at c ^ f(r),
 // so that the 16 rows of a K read and the 4 rows x 64 bytes of a V read cover all 64
 // banks (f by row for K, by row % 4 in 64-byte blocks for V; measured without
-// conflicts).  The running maximum is raised as in k_attn.
+// conflicts).  The running maximum is raised as in k_attn.  A wave works on two
+// tiles at once: the products of the next tile's scores are issued between the
+// exponentials of this one's, so that neither unit waits for the other.
 #include "attn_device.h"
 #include "q4gemv.h"
 
@@ -66,6 +69,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 constexpr int kTile = 64;  // keys of a tile
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kAheadK = 4, kAheadV = 3;  // LDS reads ahead of the products
 
 template <int D>
@@ -79,10 +83,10 @@ struct Layout {
     static __device__ __forceinline__ int swz_v(int r) { return chunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; }
 };
 
-template <typename T, int D, int NW>
-__global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const AttnArgs a, const Cut cut) {
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const AttnArgs a, const Cut cut) {
     typedef Layout<D> L;
-    constexpr int ROWS = 32 * NW;
+    constexpr int NW = kWaves, ROWS = 32 * NW;
     constexpr int KS = D / 16;                         // k-steps of the first product
     constexpr int DT = D / 32;                         // 32-element tiles of the output
     constexpr int LOADS = kTile / L::per_load / NW;    // loads of a wave for K, and for V, of a tile
@@ -205,6 +209,7 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
             page0 = pages(t);
             page1 = pages(t + kTile);
             page2 = pages(t + 2 * kTile);
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // with the queries: no wait for them, and so for tiles, in the loop
             fill_k(t, page0, 0);
             fill_v(t, page0, 0);
             if (t + kTile < it.k_hi) fill_k(t + kTile, page1, 1);
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
             if (valid != 0xFF || t + kTile > min(it.k_hi, it.p_first + 1) || (a.window && t <= it.p_last - a.window)) {
                 bool mine = false;
                 char* tv = sh + (2 + stage) * L::bytes;
-                for (int u = threadIdx.x; u < kTile * L::chunks; u += NW * 64) {
+                for (int u = threadIdx.x; u < kTile * L::chunks; u += kThreads) {
                     const int r = u / L::chunks, c = (u % L::chunks) ^ L::swz_v(r);
                     if (c >= D / 8) continue;
                     u4* at = reinterpret_cast<u4*>(tv + u * 16);
@@ -408,23 +413,16 @@ __global__ void __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) k_attn_tile(const A
     }
 }
 
-template <typename T, int D, int NW>
-hipError_t launch(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
-    constexpr size_t lds = (size_t)4 * Layout<D>::bytes + NW * sizeof(int);
-    static LdsLimit limit;
-    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, NW>), lds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<T, D, NW>), dim3(shape.grid), dim3(NW * 64), lds, s, a, cut);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 template <typename T, int D>
 hipError_t launch_attn_tile(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
-    if constexpr (D <= 128)
-        if (shape.rows == 256) return launch<T, D, 8>(a, cut, shape, s);
-    return launch<T, D, 4>(a, cut, shape, s);
+    constexpr size_t lds = (size_t)4 * Layout<D>::bytes + kWaves * sizeof(int);
+    static LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D>), lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_attn_tile<T, D>), dim3(shape.grid), dim3(kThreads), lds, s, a, cut);
+    return hipGetLastError();
 }
 
 template hipError_t launch_attn_tile<F16, 64>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);
