@@ -23,6 +23,8 @@
 //     byte permutes into D/16 A operands; row i of operand j is element
 //     D/16 i + j.  The accumulators of lane (q, n) are then the consecutive
 //     elements D/4 q .. of query row n.
+// V's loads are non-temporal: a load takes whole 128-byte lines, once (212 -> 196 us
+// for 61 sequences of up to 8192 keys; K's, which take half lines, gain nothing).
 // The running maximum is raised only when a score exceeds it by 2^8 (the
 // probabilities stay below 2^8, far inside both types), so most steps neither
 // reduce over lanes nor rescale.  Row sums are of the rounded probabilities, so
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(attn_waves(D, 16 * NR) * 64) k_attn(const Attn
 #pragma unroll
             for (int t8 = 0; t8 < 8; ++t8) {
                 typedef uint32_t raw __attribute__((ext_vector_type(PER / 2), aligned(4)));
-                const raw r = *(__attribute__((address_space(1))) const raw*)(src + t8 * 2 * a.cache.v_slot);
+                const raw r = __builtin_nontemporal_load((__attribute__((address_space(1))) const raw*)(src + t8 * 2 * a.cache.v_slot));
 #pragma unroll
                 for (int j = 0; j < PER / 2; ++j) x.v[t8][j] = r[j];
             }
@@ -479,7 +481,8 @@ hipError_t launch_dim(const AttnArgs& a, const AttnShape& shape, hipStream_t s) 
     else if constexpr (D <= 128)
         e = launch<T, D, 2>(a, shape, s);
     if (e != hipSuccess || !shape.bytes) return e;
-    const int by = std::min(16, (shape.most_rows + 7) / 8);
+    // Few items have many parts each: a workgroup a row; else one for eight rows.
+    const int by = std::min(16, shape.few ? shape.most_rows : (shape.most_rows + 7) / 8);
     hipLaunchKernelGGL((k_attn_join<T, D>), dim3((unsigned)shape.grid - 1, by), dim3(kThreads), 0, s, a, make_cut(a, shape), (uint32_t)shape.grid);
     return hipGetLastError();
 }
@@ -509,55 +512,56 @@ hipError_t LdsLimit::raise(const void* kernel, size_t bytes) {
 
 bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
 
-// Cutting costs what writing the parts and joining them takes, about kJoin us
-// (a launch that waits for the first one) and 2 x rows of parts a workgroup;
-// taking items whole costs what the last workgroups run alone.  Both are
-// estimated from the longest context and the most new tokens of a sequence, as
-// far as the caller knows them: measured, a step of k_attn's
-// waves takes about 1 us, a workgroup of k_attn_tile (of two on a CU) 2.4 us for 64 keys.
+// Items are taken whole or cut.  Cutting costs a launch that waits for the
+// first one (measured 5 to 7 us) and the parts' way to memory and back; taking items
+// whole costs what the longest of them takes alone.  Both are estimated from the
+// longest context and the most new tokens of a sequence, as far as the caller
+// knows them.  Measured, a workgroup takes 3 us for a step of k_attn's waves (8 x
+// 32 keys of 128: a CU's loads in flight bound it) and 1.5 us for a tile of k_attn_tile.
 AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
-    AttnShape s;
+    AttnShape s = {};
     const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
     const int64_t longest = max_query > 0 ? std::min<int64_t>(max_query, tokens) : tokens;  // new tokens of a sequence
     const int64_t most = longest * group;
     const int64_t seqs = std::min<int64_t>(b.seqs, tokens);
     const int cus = compute_units();
-    double us;  // of a whole item
-    int slots;  // workgroups that run at a time
     int64_t keys = max_context > 0 ? std::min<int64_t>(max_context, capacity) : capacity;
     if (window) keys = std::min<int64_t>(keys, window + longest);
+    double us;  // of a whole item
+    int slots;  // workgroups that run at a time
     if (most <= (c.head_dim > 128 ? 16 : 32)) {
         s.rows = most <= 16 ? 16 : 32;
         s.step = kStep;
-        s.unit = attn_waves(c.head_dim, s.rows) * kStep;  // a step of each wave
         slots = cus;
-        us = 1.0 * keys / s.unit;
+        us = 3.0 * keys * c.head_dim / (256 * 128);
     } else {
-        s.step = s.unit = 64;
         s.rows = 128;
+        s.step = 64;
         slots = c.head_dim <= 128 ? 2 * cus : cus;
-        us = 2.4 * (keys + 63) / 64 * c.head_dim / 128;
+        us = 1.5 * (keys + 63) / 64 * c.head_dim / 128;
     }
+    s.unit = 64;
     s.most_rows = (int)std::min<int64_t>(s.rows, most);
     // Whole: the longest item, or all of them (a sequence's rows see its context
     // less half of the new tokens on average) and half an item for what the last
     // ones run alone.  Cut: ranges of equal units, of which an item counts as
     // many as its sequence's longest.
-    constexpr double kJoin = 6.0;
     const double items = (double)c.kv_heads * (seqs == 1 ? (tokens * group + s.rows - 1) / s.rows : (tokens * group + s.rows * seqs / 2) / s.rows);
     const double mean = window ? us : us * (1.0 - 0.5 * longest / std::max<double>(keys, longest));
-    const bool whole = items > slots ? mean * items / slots + 0.5 * us <= us * items / slots + kJoin + s.rows / 32
-                                     : us <= us * items / slots + kJoin + s.rows / 32;
+    const double parts = std::min<double>(slots, items * keys / s.unit);
+    const double join = 7.5 + parts * s.most_rows * c.head_dim * 8 / 4e6;  // written and read at about 4 TB/s
+    const double cut = us * items / slots + join;
+    const bool whole = items > slots ? mean * items / slots + 0.5 * us <= cut : us <= cut;
     const int64_t bound = item_bound(c, b, q_heads, tokens, s.rows);
     if (whole && bound < (int64_t(1) << 31)) {
         s.unit = 1 << 30;
         s.grid = (int)bound;
-        s.bytes = 0;
         return s;
     }
     // Larger units where this many would pass 31 bits.
     while (s.unit < (1 << 30) && bound * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;
     s.grid = slots;
+    s.few = items * 8 <= slots;
     s.bytes = (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + sizeof(f2));
     return s;
 }

@@ -212,8 +212,13 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             __builtin_amdgcn_s_waitcnt(0x0F70);  // with the queries: no wait for them, and so for tiles, in the loop
             fill_k(t, page0, 0);
             fill_v(t, page0, 0);
-            if (t + kTile < it.k_hi) fill_k(t + kTile, page1, 1);
-            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+            if (t + kTile < it.k_hi) {
+                fill_k(t + kTile, page1, 1);
+                fill_v(t + kTile, page1, 1);
+                asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(3 * LOADS) : "memory");  // the first tile's K is there
+            } else {
+                asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LOADS) : "memory");
+            }
             scores();
         }
         // One tile: its scores are in `now`, the next one's follow there.
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");  // V of this tile and K of the next are there, the places of K of this one and V of the last free
             const bool more = t + kTile < it.k_hi;
             const int page8 = page0;
-            if (more) fill_v(t + kTile, page1, stage ^ 1);
+            if (more && t > it.k_lo) fill_v(t + kTile, page1, stage ^ 1);  // the second tile's is on its way
             if (t + 2 * kTile < it.k_hi) fill_k(t + 2 * kTile, page2, stage);
             page0 = page1;
             page1 = page2;
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                 int* flags = reinterpret_cast<int*>(sh + 4 * L::bytes);
                 const bool wave_odd = __ballot(mine) != 0;
                 if (lane == 0) flags[wave] = wave_odd;
-                __syncthreads();
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // LDS alone: the next tiles stay in flight
 #pragma unroll
                 for (int w = 0; w < NW; ++w) odd |= flags[w] != 0;
             }

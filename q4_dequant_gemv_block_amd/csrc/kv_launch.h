@@ -84,6 +84,7 @@ struct AttnShape {
     int unit;      // keys of one unit of work
     int step;      // keys a kernel takes at a time
     int grid;      // workgroups
+    bool few;      // far fewer items than workgroups
     size_t bytes;  // workspace, 0 where every item is taken whole
 };
 bool attn_head_dim_ok(int head_dim);
