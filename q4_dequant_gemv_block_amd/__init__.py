@@ -639,16 +639,14 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     return torch.tensor(freq, dtype=torch.float64, device=device), mscale
 
 
-def _heads(t: torch.Tensor, name: str, device=None) -> Heads:
+def _heads(t: torch.Tensor, name: str, device) -> Heads:
     """Tokens x heads x head_dim with the elements of a head side by side; other strides are free."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     kind = _TYPES.get(t.dtype)
     if kind is None:
         raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, t.dtype))
-    if not t.is_cuda:
-        raise ValueError("%s must be on a GPU" % name)
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError("%s must be on %s" % (name, device))
     if t.dim() != 3:
         raise ValueError("%s must be [tokens, heads, head_dim]" % name)
@@ -658,13 +656,16 @@ def _heads(t: torch.Tensor, name: str, device=None) -> Heads:
     return Heads(t.data_ptr(), st, sh, kind)
 
 
-def _vector(t: torch.Tensor, dtype, name: str, n: int, device) -> int:
-    p = _ptr(t, dtype, name)
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError("%s must be %s [%d]" % (name, dtype, n))
+def _vector(t: torch.Tensor, dtype, name: str, n: int | None, device) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.device != device:
         raise ValueError("%s must be on %s" % (name, device))
-    return p
+    if t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_contiguous():
+        raise ValueError("%s must be contiguous, %s" % (name, "[%d]" % n if n is not None else "of one dimension"))
+    return t.data_ptr()
 
 
 def _layout(layout: str) -> int:
@@ -680,9 +681,24 @@ def _on(device, stream):
         if stream.device != device:
             raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
+    if device.type == "cuda" and torch.cuda.current_device() != device.index:
         return torch.cuda.device(device)
     return None
+
+
+def _current_stream(device) -> int:
+    """The handle of the device's current stream (torch.cuda.current_stream makes an object of it, for 3 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _cuda(t, name: str):
+    """The GPU a tensor is on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError("%s must be on a GPU" % name)
+    return device
 
 
 def q4_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layout: str = "half",
@@ -692,23 +708,24 @@ def q4_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
     (int32 [T], float64 [r / 2]; rope_frequencies makes them), the others as they are.  Pairs are elements i and
     i + r/2 ("half") or 2i and 2i + 1 ("interleaved"), results times mscale.  out: like x in shape, of any of the
     types, and may be x itself.  Turning by -positions undoes it and is its gradient."""
-    on = _on(x.device, stream) if x.is_cuda else None
+    dev = _cuda(x, "x")
+    on = _on(dev, stream)
     if on is not None:
         with on:
             return q4_rope(x, positions, inv_freq, layout, mscale, out)
-    hx = _heads(x, "x")
+    hx = _heads(x, "x", dev)
     t, h, d = x.shape
     if out is None:
-        out = torch.empty((t, h, d), dtype=x.dtype, device=x.device)
+        out = torch.empty((t, h, d), dtype=x.dtype, device=dev)
     elif out.shape != x.shape:
         raise ValueError("out must have x's shape")
-    ho = _heads(out, "out", x.device)
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be float64 [rot_dim / 2]")
-    r = inv_freq.shape[0]
-    _check(load_library().q4_rope(ctypes.byref(hx), ctypes.byref(ho), _vector(positions, torch.int32, "positions", t, x.device),
-                                  _vector(inv_freq, torch.float64, "inv_freq", r, x.device), t, h, d, 2 * r,
-                                  _layout(layout), mscale, _stream()))
+    ho = _heads(out, "out", dev)
+    freq = _vector(inv_freq, torch.float64, "inv_freq", None, dev)
+    status = (_lib or load_library()).q4_rope(
+        ctypes.byref(hx), ctypes.byref(ho), _vector(positions, torch.int32, "positions", t, dev), freq, t, h, d,
+        2 * inv_freq.shape[0], _layout(layout), mscale, _current_stream(dev))
+    if status:
+        _check(status)
     return out
 
 
@@ -783,9 +800,8 @@ def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
     dev = cache.device
     hk, hv = _heads(k, "k", dev), _heads(v, "v", dev)
     t = k.shape[0]
-    want = (t, cache.kv_heads, cache.head_dim)
-    if tuple(k.shape) != want or tuple(v.shape) != want:
-        raise ValueError("k and v must be [T, %d, %d]" % want[1:])
+    if k.shape != v.shape or k.shape[1] != cache.kv_heads or k.shape[2] != cache.head_dim:
+        raise ValueError("k and v must be [T, %d, %d]" % (cache.kv_heads, cache.head_dim))
     rq = ro = None
     heads = 0
     if q is not None:
@@ -794,22 +810,23 @@ def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
         if q.shape[0] != t or q.shape[2] != cache.head_dim:
             raise ValueError("q must be [T=%d, heads, %d]" % (t, cache.head_dim))
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=cache.dtype, device=dev)
+            q_out = torch.empty((t, heads, cache.head_dim), dtype=cache.dtype, device=dev)
         elif q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
         ho = _heads(q_out, "q_out", dev)
         rq, ro = ctypes.byref(hq), ctypes.byref(ho)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    r = 0
+    r, freq = 0, None
     if inv_freq is not None:
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must be float64 [rot_dim / 2]")
+        freq = _vector(inv_freq, torch.float64, "inv_freq", None, dev)
         r = inv_freq.shape[0]
-    _check(load_library().q4_kv_append(
+    status = (_lib or load_library()).q4_kv_append(
         cache._ref, batch._ref, ctypes.byref(hk), ctypes.byref(hv), rq, ro, heads, t,
         None if positions is None else _vector(positions, torch.int32, "positions", t, dev),
-        _vector(inv_freq, torch.float64, "inv_freq", r, dev) if r else None, 2 * r, _layout(layout), mscale, _stream()))
+        freq if r else None, 2 * r, _layout(layout), mscale, _current_stream(dev))
+    if status:
+        _check(status)
     return q_out
 
 
@@ -850,15 +867,19 @@ def q4_attention_paged(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: f
         if tuple(lse.shape) != (t, h) or lse.device != dev:
             raise ValueError("lse must be float32 [T, heads] on %s" % dev)
         lp = _ptr(lse, torch.float32, "lse")
-    lib = load_library()
+    lib = _lib or load_library()
+    wp, wb = None, 0
     if workspace is None:
-        need = lib.q4_attention_paged_workspace_bytes(cache._ref, batch._ref, h, t, window)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    elif workspace.device != dev:
-        raise ValueError("workspace must be on %s" % dev)
-    wp, wb = (None, 0) if workspace is None else (_ptr(workspace, torch.uint8, "workspace"), workspace.numel())
-    _check(lib.q4_attention_paged(cache._ref, batch._ref, ctypes.byref(hq), ctypes.byref(ho), lp, h, t,
-                                  scale if scale is not None else d ** -0.5, window, wp, wb, _stream()))
+        wb = lib.q4_attention_paged_workspace_bytes(cache._ref, batch._ref, h, t, window)
+        if wb:
+            workspace = torch.empty(wb, dtype=torch.uint8, device=dev)
+            wp = workspace.data_ptr()
+    else:
+        wp, wb = _vector(workspace, torch.uint8, "workspace", None, dev), workspace.shape[0]
+    status = lib.q4_attention_paged(cache._ref, batch._ref, ctypes.byref(hq), ctypes.byref(ho), lp, h, t,
+                                    scale if scale is not None else d ** -0.5, window, wp, wb, _current_stream(dev))
+    if status:
+        _check(status)
     return out
 
 
