@@ -12,19 +12,18 @@
 // them writes the part's sums, maxima and unnormalised outputs in 32 bits, and
 // a second launch joins the parts.
 //
-// A wave takes 32 keys at a time from HBM straight into registers, with no LDS
-// and no data movement between lanes:
-//   S^T = K Q^T on v_mfma_f32_16x16x32: two tiles of 16 keys.  Tile a holds the
-//     keys 8 (m / 4) + 4 a + m % 4 in its rows m, so that the lane that gets
-//     rows 4 q .. 4 q + 3 of both tiles has the 8 consecutive keys 8 q .. 8 q + 7
-//     of one query row - which is the B operand P^T of the second product.
-//   O^T = V^T P^T: lane (q, i) reads D/16 consecutive elements of keys 8 q .. 8 q
-//     + 7 (16 lanes read a whole row of V), and transposes its 8 x D/16 block by
-//     byte permutes into D/16 A operands; row i of operand j is element
-//     D/16 i + j.  The accumulators of lane (q, n) are then the consecutive
-//     elements D/4 q .. of query row n.
-// V's loads are non-temporal: a load takes whole 128-byte lines, once (212 -> 196 us
-// for 61 sequences of up to 8192 keys; K's, which take half lines, gain nothing).
+// A wave takes 32 keys at a time, straight from HBM into its own part of LDS
+// (global_load_lds, whole rows, 16 bytes a lane), so that waves never wait for each
+// other: while it works on V, the next step's K is on its way into the place that
+// K left, and the next V follows into V's.
+//   S^T = K Q^T on v_mfma_f32_16x16x32, 16 keys a tile: lane (q, n) gets the keys 4 q
+//     .. 4 q + 3 of both tiles for query row n, which is the B operand P^T of
+//   O^T = V^T P^T, whose A operand the transposing LDS reads give for the same keys.
+// Rows lie in LDS as long as a head, their 16-byte chunks XORed by the row so that
+// the reads of both products use all 64 banks.  Loading to registers instead, K in
+// the operand's layout (half lines of 16 rows a load), took 2.4 us for a step of 8
+// waves on a CU, this 1.5.
+// The loads are non-temporal: each 128-byte line is used once.
 // The running maximum is raised only when a score exceeds it by 2^8 (the
 // probabilities stay below 2^8, far inside both types), so most steps neither
 // reduce over lanes nor rescale.  Row sums are of the rounded probabilities, so
@@ -59,31 +58,47 @@ struct Mma<BF16> {
     }
 };
 
-// 32 keys of one wave in registers.
-template <int D>
-struct Keys {
-    u4 k[2][D / 32];           // tile a: A operand of k-step s
-    uint32_t v[8][D / 32];     // key 8 q + t: elements D/16 i ..
+// Waves of a workgroup of k_attn, one workgroup a CU: as many as 128 KiB of LDS
+// hold 32 keys of K and V for.
+constexpr int attn_waves(int head_dim) { return head_dim <= 128 ? 8 : 4; }
+
+// Places in LDS: a wave's 32 rows of K, then as many of V.
+template <int D, int NR>
+struct Layout : LdsRow<D> {
+    typedef LdsRow<D> R;
+    static constexpr int loads = kStep / R::per_load;     // of K, and of V, a step
+    static constexpr int bytes = kStep * R::row;
+    static constexpr int waves = attn_waves(D);
+    static constexpr int lines = D + 4;                   // floats of a row of outputs
+    // after the keys, in their place: outputs of all waves, their maxima and sums
+    static constexpr int merge = waves * 16 * NR * (lines + 2) * 4;
+    static constexpr int total = merge > 2 * waves * bytes ? merge : 2 * waves * bytes;
+    // V's transposing reads take 32 bytes of 8 rows at a time
+    static __device__ __forceinline__ int swz_v(int r) { return R::chunks == 8 ? ((r >> 1) & 3) << 1 : (r & 7) << 1; }
 };
 
-// Waves of a workgroup of k_attn, one workgroup a CU: as many as its registers
-// allow (two a SIMD, one where 32 rows of 128 or heads of 256 take over 256).
-constexpr int attn_waves(int head_dim, int rows) { return head_dim * rows <= 16 * 192 ? 8 : 4; }
-
 template <typename T, int D, int NR>
-__global__ void __launch_bounds__(attn_waves(D, 16 * NR) * 64) k_attn(const AttnArgs a, const Cut cut) {
-    constexpr int ROWS = 16 * NR, kWaves = attn_waves(D, ROWS), kThreads = 64 * kWaves;
-    constexpr int PER = D / 16;      // elements of V a lane holds of a key
-    constexpr int KS = D / 32;       // k-steps of the first product
-    constexpr int LD = D + 4;
-    // [wave][ROWS][LD] outputs, [wave][ROWS] maxima, the same of sums, [wave][ROWS][kStep] weights
-    extern __shared__ float sh[];
+__global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const AttnArgs a, const Cut cut) {
+    typedef Layout<D, NR> L;
+    constexpr int ROWS = 16 * NR, kWaves = L::waves;
+    constexpr int KS = D / 32;  // k-steps of the first product
+    constexpr int DT = D / 16;  // 16-element tiles of the output
+    extern __shared__ char sh[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, n16 = lane & 15;
     Work work;
     if (!work.start(cut, a.batch)) return;
     const Seq& seq = work.seq;
     const Parts<D> parts(a.workspace, (int)gridDim.x, ROWS);
+    // this wave's K and V, and where the lane reads in them
+    char* my = sh + wave * 2 * L::bytes;
+    const uint32_t my_lds = lds_address(my);
+    const char* at_k = my + n16 * L::row;
+    const int chunk_k = q ^ L::swz_k(n16);
+    const int row_v = 4 * q + (n16 >> 2);
+    const char* at_v = my + L::bytes + row_v * L::row + (n16 & 1) * 8;
+    const int chunk_v = ((n16 & 3) >> 1) ^ L::swz_v(row_v);
+    const bool one_page = a.cache.page_size.d % kStep == 0;  // a step's keys lie in one page
     Item it;
     while (work.next(cut, a.batch, &it)) {
         const int head = it.head, row0 = it.row0, rows = it.rows, past = it.past;
@@ -102,94 +117,117 @@ __global__ void __launch_bounds__(attn_waves(D, 16 * NR) * 64) k_attn(const Attn
 #pragma unroll
             for (int s = 0; s < KS; ++s) qf[r][s] = *reinterpret_cast<const u4*>(src + 64 * s);
         }
-        f4 acc[NR][PER];
+        f4 acc[NR][DT];
         float m[NR], l[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             m[r] = kNone;
             l[r] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < PER; ++j) acc[r][j] = f4{0, 0, 0, 0};
+            for (int j = 0; j < DT; ++j) acc[r][j] = f4{0, 0, 0, 0};
         }
-        const int32_t* table = a.batch.table + seq.b * a.batch.table_stride;
-        const char* kbase = a.cache.k + (int64_t)head * a.cache.k_head * 2 + 16 * q;
-        const char* vbase = a.cache.v + (int64_t)head * a.cache.v_head * 2 + n16 * PER * 2;
+        // (no kernel of the call writes the table: constant, and so read by scalar loads)
+        typedef const __attribute__((address_space(4))) int32_t c_i32;
+        c_i32* table = (c_i32*)(uintptr_t)(a.batch.table + seq.b * a.batch.table_stride);
+        const char* kbase = a.cache.k + (int64_t)head * a.cache.k_head * 2;
+        const char* vbase = a.cache.v + (int64_t)head * a.cache.v_head * 2;
 
-        // pages of the two groups of 8 keys this lane reads in the step at key t
-        auto pages = [&](int t, int* pk, int* pv) {
-            *pk = page_of(a.cache, a.batch, table, t + 8 * (n16 >> 2));
-            *pv = page_of(a.cache, a.batch, table, t + 8 * q);
+        // The pages of a step's four groups of 8 keys (scalar loads: a wait for
+        // them does not wait for the keys on their way).
+        struct Pages {
+            int p[4];
         };
-        auto load_k = [&](int t, int page, Keys<D>& x) {
-            const uint32_t p = (uint32_t)(t + 8 * (n16 >> 2));
-            const uint32_t slot = p - a.cache.page_size.div(p) * a.cache.page_size.d + (n16 & 3);
-            const char* src = kbase + ((int64_t)max(page, 0) * a.cache.k_page + (int64_t)slot * a.cache.k_slot) * 2;
+        auto pages = [&](int t) {
+            Pages x;
 #pragma unroll
-            for (int t4 = 0; t4 < 2; ++t4)
-#pragma unroll
-                for (int s = 0; s < KS; ++s) x.k[t4][s] = *(g_u4*)(src + t4 * 8 * a.cache.k_slot + 64 * s);
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t column = a.cache.page_size.div((uint32_t)(t + 8 * g));
+                const int page = table[min(column, (uint32_t)a.batch.table_pages - 1)];
+                x.p[g] = column < (uint32_t)a.batch.table_pages && (uint32_t)page < a.cache.pages ? page : -1;
+                if (one_page) {
+                    x.p[1] = x.p[2] = x.p[3] = x.p[0];
+                    break;
+                }
+            }
+            return x;
         };
-        auto load_v = [&](int t, int page, Keys<D>& x) {
-            const uint32_t p = (uint32_t)(t + 8 * q);
-            const uint32_t slot = p - a.cache.page_size.div(p) * a.cache.page_size.d;
-            const char* src = vbase + ((int64_t)max(page, 0) * a.cache.v_page + (int64_t)slot * a.cache.v_slot) * 2;
+        auto fill = [&](int t, const Pages& x, const char* base, int64_t page_stride, int64_t slot_stride, uint32_t to, bool values) {
 #pragma unroll
-            for (int t8 = 0; t8 < 8; ++t8) {
-                typedef uint32_t raw __attribute__((ext_vector_type(PER / 2), aligned(4)));
-                const raw r = __builtin_nontemporal_load((__attribute__((address_space(1))) const raw*)(src + t8 * 2 * a.cache.v_slot));
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t p = (uint32_t)(t + 8 * g);
+                const uint32_t slot = p - a.cache.page_size.div(p) * a.cache.page_size.d;
+                const char* src = base + ((int64_t)max(x.p[g], 0) * page_stride + (int64_t)slot * slot_stride) * 2;
 #pragma unroll
-                for (int j = 0; j < PER / 2; ++j) x.v[t8][j] = r[j];
+                for (int k = 0; k < L::loads / 4; ++k) {
+                    const int r8 = k * L::per_load + lane / L::chunks, r = 8 * g + r8;
+                    const int c = (lane % L::chunks) ^ (values ? L::swz_v(r) : L::swz_k(r));
+                    if (D == 8 * L::chunks || c < D / 8)
+                        load_to_lds_once(src, r8 * (uint32_t)slot_stride * 2 + 16 * c, to + (8 * g + k * L::per_load) * L::row);
+                }
             }
         };
+        auto fill_k = [&](int t, const Pages& x) { fill(t, x, kbase, a.cache.k_page, a.cache.k_slot, my_lds, false); };
+        auto fill_v = [&](int t, const Pages& x) { fill(t, x, vbase, a.cache.v_page, a.cache.v_slot, my_lds + L::bytes, true); };
 
-        Keys<D> x;
         int t = k_lo + wave * kStep;
-        int pk, pv, pk_next, pv_next;
+        Pages now = {}, next = {};
+        if (t < k_hi) now = pages(t);
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // the queries: no wait for them in the loop
         if (t < k_hi) {
-            pages(t, &pk, &pv);
-            load_k(t, pk, x);
-            load_v(t, pv, x);
-            pages(t + kWaves * kStep, &pk_next, &pv_next);
+            fill_k(t, now);
+            fill_v(t, now);
+            next = pages(t + kWaves * kStep);
         }
         for (; t < k_hi; t += kWaves * kStep) {
-            // S^T: scores of keys t + 8 q .. + 7 in the lane's query rows
-            float s[NR][8];
-#pragma unroll
-            for (int r = 0; r < NR; ++r)
-#pragma unroll
-                for (int t4 = 0; t4 < 2; ++t4) {
-                    f4 c = {0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) c = Mma<T>::mma(x.k[t4][k], qf[r][k], c);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[r][4 * t4 + j] = c[j];
-                }
             const int t_next = t + kWaves * kStep;
             const bool more = t_next < k_hi;
-            const int pv_now = pv;
+            // S^T: keys 4 q + j and 16 + 4 q + j in the lane's query rows
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L::loads) : "memory");  // K is there, V on its way
+            float s[NR][8];
+            {
+                u4 kf[2][KS];
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) kf[u][k] = *reinterpret_cast<const u4*>(at_k + ((chunk_k ^ (4 * k)) * 16) + u * 16 * L::row);
+                __builtin_amdgcn_sched_barrier(0);  // all reads before the products
+                f4 c[NR][2];
+#pragma unroll
+                for (int r = 0; r < NR; ++r) c[r][0] = c[r][1] = f4{0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) c[r][u] = Mma<T>::mma(kf[u][k], qf[r][k], c[r][u]);
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[r][j] = c[r][j >> 2][j & 3];
+            }
+            const Pages here = now;
             if (more) {
-                load_k(t_next, pk_next, x);
-                pv = pv_next;
-                pages(t_next + kWaves * kStep, &pk_next, &pv_next);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // K is read
+                fill_k(t_next, next);
+                now = next;
+                next = pages(t_next + kWaves * kStep);
             }
             // masks: only steps that some row does not see whole
-            const bool ragged = t + kStep > min(k_hi, p_first + 1) || (a.window && t <= p_last - a.window) ||
-                                __ballot(pv_now < 0) != 0;
+            uint32_t valid = 0;  // groups with a place
+#pragma unroll
+            for (int g = 0; g < 4; ++g) valid |= (here.p[g] >= 0 ? 1u : 0u) << g;
+            const bool ragged = t + kStep > min(k_hi, p_first + 1) || (a.window && t <= p_last - a.window) || valid != 15;
+            uint32_t places = 0xFFFFFFFFu;  // keys of the step that are there
             if (ragged) {
-                const int first = t + 8 * q;
-                // keys that do not belong here: their values could be anything
-                const uint32_t here = pv_now < 0 ? 0u : (uint32_t)bits_between(0, k_hi - first);
+                places = (uint32_t)bits_between(0, k_hi - t);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t mask = bit_mask(here, j);
-#pragma unroll
-                    for (int e = 0; e < PER / 2; ++e) x.v[j][e] &= mask;
-                }
+                for (int g = 0; g < 4; ++g)
+                    if (!((valid >> g) & 1)) places &= ~(0xFFu << (8 * g));
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                    const uint32_t seen = here & (uint32_t)bits_between(a.window ? pos[r] - a.window + 1 - first : 0, pos[r] + 1 - first);
+                    const uint32_t seen = places & (uint32_t)bits_between(a.window ? pos[r] - a.window + 1 - t : 0, pos[r] + 1 - t);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[r][j] = keep_seen(s[r][j], bit_mask(seen, j));
+                    for (int j = 0; j < 8; ++j) s[r][j] = keep_seen(s[r][j], bit_mask(seen >> (4 * q), 16 * (j >> 2) + (j & 3)));
                 }
             }
             uint32_t p[NR][4];
@@ -207,7 +245,7 @@ __global__ void __launch_bounds__(attn_waves(D, 16 * NR) * 64) k_attn(const Attn
                     m[r] = raised;
                     l[r] *= f;
 #pragma unroll
-                    for (int j = 0; j < PER; ++j) acc[r][j] *= f;
+                    for (int j = 0; j < DT; ++j) acc[r][j] *= f;
                 }
                 const float ref = m[r] == kNone ? 0.0f : m[r];
 #pragma unroll
@@ -215,81 +253,90 @@ __global__ void __launch_bounds__(attn_waves(D, 16 * NR) * 64) k_attn(const Attn
                     const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][2 * j], a.scale_log2, -ref));
                     const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][2 * j + 1], a.scale_log2, -ref));
                     p[r][j] = pack2<T>(e0, e1);
-                    l[r] += unpack_sum<T>(p[r][j]);
+                    l[r] = add_pair<T>(p[r][j], l[r]);
                 }
             }
+            if (more)
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L::loads) : "memory");  // V is there, the next K on its way
+            else
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             if (ragged) {
-                // In a product a weight of 0 times NaN or infinity would reach
-                // rows that do not see the key: such elements leave the
-                // product and are added row by row to those that do see them.
+                // Values of keys that do not belong here become 0.  So do NaN and
+                // infinities - in a product a weight of 0 times them would reach
+                // rows that do not see the key - and are added row by row to
+                // those that do.
                 uint32_t any = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < PER / 2; ++e) any |= nonfinite_bits<T>(x.v[j][e]);
+                for (int k = 0; k < L::loads; ++k) {
+                    const int r = k * L::per_load + lane / L::chunks;
+                    u4* at = reinterpret_cast<u4*>(my + L::bytes + k * 1024 + lane * 16);
+                    const int c = (lane % L::chunks) ^ L::swz_v(r);
+                    if (D != 8 * L::chunks && c >= D / 8) continue;
+                    const u4 v = *at;
+                    const uint32_t keep = bit_mask(places >> (r & 31), 0);
+                    const u4 bad = {nonfinite<T>(v.x), nonfinite<T>(v.y), nonfinite<T>(v.z), nonfinite<T>(v.w)};
+                    any |= (bad.x | bad.y | bad.z | bad.w) & keep;
+                    *at = v & ~bad & keep;
+                }
+                wave_lds_fence();
                 if (__ballot(any != 0)) {
-                    // through this wave's part of LDS: rare, and so free of registers
-                    float* so = sh + wave * ROWS * LD;
-                    float* sp = sh + kWaves * ROWS * (LD + 2) + wave * ROWS * kStep;
+                    for (int k = 0; k < kStep; ++k) {
+                        if (!((places >> k) & 1)) continue;
+                        const int page = k < 16 ? (k < 8 ? here.p[0] : here.p[1]) : (k < 24 ? here.p[2] : here.p[3]);
+                        const uint32_t slot = (uint32_t)(t + k) - a.cache.page_size.div(t + k) * a.cache.page_size.d;
+                        const char* src = vbase + ((int64_t)page * a.cache.v_page + (int64_t)slot * a.cache.v_slot + 4 * q) * 2;
+                        float w[NR];
+                        bool sees[NR];
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
+                        for (int r = 0; r < NR; ++r) {
+                            uint32_t pr = 0;  // keys 16 (j / 2) + 4 q + 2 (j % 2), + 1
 #pragma unroll
-                        for (int rr = 0; rr < 4; ++rr)
+                            for (int j = 0; j < 4; ++j)
+                                if ((k & ~13) == 16 * (j >> 1) + 2 * (j & 1)) pr = p[r][j];
+                            w[r] = half_of<T>((uint32_t)__shfl((int)pr, n16 + 16 * ((k >> 2) & 3)), k & 1);
+                            sees[r] = t + k <= pos[r] && (!a.window || t + k > pos[r] - a.window);
+                        }
 #pragma unroll
-                            for (int j = 0; j < PER; ++j) so[(16 * r + n16) * LD + D / 4 * q + PER * rr + j] = acc[r][j][rr];
+                        for (int d = 0; d < DT; ++d) {
+                            float v[4];
+                            load_elems<T, 4>(src + 32 * d, v);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) sp[(16 * r + n16) * kStep + 8 * q + j] = half_of<T>(p[r][j / 2], j & 1);
-                    }
-                    wave_lds_fence();
-                    for (int k = 0; k < kStep && t + k < k_hi; ++k) {
-                        const int page = page_of(a.cache, a.batch, table, t + k);
-                        if (page < 0) continue;
-                        const int64_t at = page * a.cache.v_page + head * a.cache.v_head +
-                                           (int64_t)(t + k - (int)a.cache.page_size.div(t + k) * (int)a.cache.page_size.d) * a.cache.v_slot;
-                        for (int d = lane; d < D; d += 64) {
-                            float v;
-                            load_elems<T, 1>(a.cache.v + (at + d) * 2, reinterpret_cast<float(&)[1]>(v));
-                            if (__builtin_isfinite(v)) continue;
-                            for (int row = 0; row < rows; ++row) {
-                                const int pr = past + (int)cut.group.div(row0 + row);
-                                if (t + k <= pr && (!a.window || t + k > pr - a.window)) so[row * LD + d] += sp[row * kStep + k] * v;
-                            }
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int r = 0; r < NR; ++r)
+                                    if (sees[r] && !__builtin_isfinite(v[i])) acc[r][d][i] += w[r] * v[i];
+                            __builtin_amdgcn_sched_barrier(0);  // registers: one load at a time
                         }
                     }
-                    wave_lds_fence();
+                }
+            }
+            // O^T += V^T P^T
+            constexpr int HALF = DT / 2;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                u4 vf[HALF];
+#pragma unroll
+                for (int d = 0; d < HALF; ++d) {
+                    const char* src = at_v + ((chunk_v ^ (2 * (b * HALF + d))) * 16);
+                    vf[d] = read_transposed(src, src + 16 * L::row);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int d = 0; d < HALF; ++d)
 #pragma unroll
                     for (int r = 0; r < NR; ++r)
-#pragma unroll
-                        for (int rr = 0; rr < 4; ++rr)
-#pragma unroll
-                            for (int j = 0; j < PER; ++j) acc[r][j][rr] = so[(16 * r + n16) * LD + D / 4 * q + PER * rr + j];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-#pragma unroll
-                        for (int e = 0; e < PER / 2; ++e) x.v[j][e] &= ~nonfinite<T>(x.v[j][e]);
-                }
+                        acc[r][b * HALF + d] = Mma<T>::mma(vf[d], u4{p[r][0], p[r][1], p[r][2], p[r][3]}, acc[r][b * HALF + d]);
             }
-            // O^T += V^T P^T: dim pairs (2 e, 2 e + 1) of the 8 keys become two A operands
-#pragma unroll
-            for (int e = 0; e < PER / 2; ++e) {
-                u4 even, odd;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    even[j] = __builtin_amdgcn_perm(x.v[2 * j + 1][e], x.v[2 * j][e], 0x05040100u);
-                    odd[j] = __builtin_amdgcn_perm(x.v[2 * j + 1][e], x.v[2 * j][e], 0x07060302u);
-                }
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const u4 pb = {p[r][0], p[r][1], p[r][2], p[r][3]};
-                    acc[r][2 * e] = Mma<T>::mma(even, pb, acc[r][2 * e]);
-                    acc[r][2 * e + 1] = Mma<T>::mma(odd, pb, acc[r][2 * e + 1]);
-                }
+            if (more) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // V is read
+                fill_v(t_next, now);
             }
-            if (more) load_v(t_next, pv, x);
         }
 
-        // the four waves' sums: elements D/4 q + PER rr + j of row n16 (rr: accumulator row)
-        float* sh_m = sh + kWaves * ROWS * LD;
+        // the waves' sums: elements 16 d + 4 q .. of row n16, in the place of the keys
+        __syncthreads();
+        float* sh_o = reinterpret_cast<float*>(sh);
+        float* sh_m = sh_o + kWaves * ROWS * L::lines;
         float* sh_l = sh_m + kWaves * ROWS;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -301,14 +348,12 @@ __global__ void __launch_bounds__(attn_waves(D, 16 * NR) * 64) k_attn(const Attn
                 sh_l[at] = l[r];
             }
 #pragma unroll
-            for (int rr = 0; rr < 4; ++rr)
-#pragma unroll
-                for (int j = 0; j < PER; ++j) sh[at * LD + D / 4 * q + PER * rr + j] = acc[r][j][rr];
+            for (int d = 0; d < DT; ++d) *reinterpret_cast<f4*>(&sh_o[at * L::lines + 16 * d + 4 * q]) = acc[r][d];
         }
         __syncthreads();
         const bool whole = it.u0 == 0 && it.u1 == seq.units;
         const int64_t slot = (int64_t)2 * blockIdx.x + (it.u0 == 0);
-        for (int u = threadIdx.x; u < rows * (D / 4); u += kThreads) {
+        for (int u = threadIdx.x; u < rows * (D / 4); u += 64 * kWaves) {
             const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
             float top = kNone;
 #pragma unroll
@@ -320,15 +365,14 @@ __global__ void __launch_bounds__(attn_waves(D, 16 * NR) * 64) k_attn(const Attn
             for (int w = 0; w < kWaves; ++w) {
                 const float f = __builtin_amdgcn_exp2f(sh_m[w * ROWS + row] - ref);
                 sum += f * sh_l[w * ROWS + row];
-                o += f * *reinterpret_cast<const f4*>(&sh[(w * ROWS + row) * LD + d]);
+                o += f * *reinterpret_cast<const f4*>(&sh_o[(w * ROWS + row) * L::lines + d]);
             }
             if (whole) {
                 const float f = row_scale(sum);
                 const int i = (int)cut.group.div(row0 + row), h = head * a.group + row0 + row - i * a.group;
                 float v[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
                 store_elems<T, 4>(a.out.data + ((int64_t)(seq.row0 + i) * a.out.token_stride + (int64_t)h * a.out.head_stride + d) * 2, v);
-                if (a.lse && d == 0)
-                    a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = row_lse(top, sum);
+                if (a.lse && d == 0) a.lse[(int64_t)(seq.row0 + i) * a.q_heads + h] = row_lse(top, sum);
             } else {
                 *reinterpret_cast<f4*>(&parts.o[(slot * ROWS + row) * D + d]) = o;
                 if (d == 0) parts.ml[slot * ROWS + row] = f2{top, sum};
@@ -462,12 +506,11 @@ Cut make_cut(const AttnArgs& a, const AttnShape& s) {
 
 template <typename T, int D, int NR>
 hipError_t launch(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
-    constexpr int waves = attn_waves(D, 16 * NR);
-    constexpr size_t lds = (size_t)waves * 16 * NR * (D + 4 + 2 + kStep) * sizeof(float);
+    constexpr size_t lds = Layout<D, NR>::total;
     static LdsLimit limit;
     const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn<T, D, NR>), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn<T, D, NR>), dim3(shape.grid), dim3(64 * waves), lds, s, a, make_cut(a, shape));
+    hipLaunchKernelGGL((k_attn<T, D, NR>), dim3(shape.grid), dim3(64 * Layout<D, NR>::waves), lds, s, a, make_cut(a, shape));
     return hipGetLastError();
 }
 
@@ -478,7 +521,7 @@ hipError_t launch_dim(const AttnArgs& a, const AttnShape& shape, hipStream_t s) 
         e = launch_attn_tile<T, D>(a, make_cut(a, shape), shape, s);
     else if (shape.rows == 16)
         e = launch<T, D, 1>(a, shape, s);
-    else if constexpr (D <= 128)
+    else
         e = launch<T, D, 2>(a, shape, s);
     if (e != hipSuccess || !shape.bytes) return e;
     // Few items have many parts each: a workgroup a row; else one for eight rows.
@@ -529,7 +572,7 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
     if (window) keys = std::min<int64_t>(keys, window + longest);
     double us;  // of a whole item
     int slots;  // workgroups that run at a time
-    if (most <= (c.head_dim > 128 ? 16 : 32)) {
+    if (most <= 32) {
         s.rows = most <= 16 ? 16 : 32;
         s.step = kStep;
         slots = cus;

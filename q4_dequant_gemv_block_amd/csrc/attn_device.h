@@ -245,4 +245,53 @@ __device__ __forceinline__ float row_lse(float top, float sum) {
     return sum > 0.0f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f : (sum != sum ? sum : kNone);
 }
 
+// l + both halves of p.
+template <typename T>
+__device__ __forceinline__ float add_pair(uint32_t p, float l) {
+    if constexpr (std::is_same<T, F16>::value) {
+        const h2 one = {(_Float16)1.0f, (_Float16)1.0f};
+        return __builtin_amdgcn_fdot2(as_h2(p), one, l, false);
+    } else {
+        return l + (__builtin_bit_cast(float, p << 16) + __builtin_bit_cast(float, p & 0xFFFF0000u));
+    }
+}
+
+// Direct-to-LDS load from a wave's address and a lane's offset: lane i's 16
+// bytes land at lds + 16 i.  Issued through asm so
+// that the compiler does not wait for a tile in flight before it reads the
+// other one; the kernel waits itself (vmcnt) before the tile's barrier.
+__device__ __forceinline__ void load_to_lds(const char* src, uint32_t offset, uint32_t lds) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(src), "{m0}"(lds) : "memory");
+}
+// The same for lines that nobody reads again.
+__device__ __forceinline__ void load_to_lds_once(const char* src, uint32_t offset, uint32_t lds) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(offset), "s"(src), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// Two transposing reads (ds_read_b64_tr_b16): in each, 16 lanes give the places of
+// 4 rows x 16 elements (lane i: 8 bytes, elements 4 (i % 4) .. of row i / 4), and
+// lane i gets element i of the 4 rows.
+__device__ __forceinline__ u4 read_transposed(const char* first, const char* second) {
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4 l_s4;
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    const u2 x = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)first));
+    const u2 y = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)second));
+    return u4{x.x, x.y, y.x, y.y};
+}
+
+// A head's row in LDS, as direct loads fill it: 1024 bytes a wave's load.
+template <int D>
+struct LdsRow {
+    static constexpr int row = D <= 64 ? 128 : D <= 128 ? 256 : 512;  // bytes
+    static constexpr int chunks = row / 16;                           // of 16 bytes
+    static constexpr int per_load = 1024 / row;                       // rows of a load
+    // XOR of a row's chunks for K, whose reads take one chunk of 16 rows: it
+    // spreads those over all 64 banks.
+    static __device__ __forceinline__ int swz_k(int r) { return chunks == 8 ? (r >> 1) & 7 : r & 15; }
+};
+
 }  // namespace q4

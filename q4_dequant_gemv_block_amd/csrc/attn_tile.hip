@@ -27,7 +27,6 @@ namespace q4 {
 namespace {
 
 typedef float f16v __attribute__((ext_vector_type(16)));
-typedef short s4 __attribute__((ext_vector_type(4)));
 
 template <typename T>
 struct Mma32;
@@ -46,41 +45,16 @@ struct Mma32<BF16> {
     }
 };
 
-// l + both halves of p.
-template <typename T>
-__device__ __forceinline__ float add_pair(uint32_t p, float l) {
-    if constexpr (std::is_same<T, F16>::value) {
-        const h2 one = {(_Float16)1.0f, (_Float16)1.0f};
-        return __builtin_amdgcn_fdot2(as_h2(p), one, l, false);
-    } else {
-        return l + (__builtin_bit_cast(float, p << 16) + __builtin_bit_cast(float, p & 0xFFFF0000u));
-    }
-}
-
-// Direct-to-LDS load from a wave's address and a lane's offset: lane i's 16
-// bytes land at lds + 16 i.  Issued through asm so
-// that the compiler does not wait for a tile in flight before it reads the
-// other one; the kernel waits itself (vmcnt) before the tile's barrier.
-__device__ __forceinline__ void load_to_lds(const char* src, uint32_t offset, uint32_t lds) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(src), "{m0}"(lds) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
-}
-
 constexpr int kTile = 64;  // keys of a tile
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kAheadK = 4, kAheadV = 3;  // LDS reads ahead of the products
 
+// Places in LDS (rows and their swizzles as described above).
 template <int D>
-struct Layout {
-    static constexpr int row = D <= 64 ? 128 : D <= 128 ? 256 : 512;  // bytes of an LDS row
-    static constexpr int chunks = row / 16;
-    static constexpr int bytes = kTile * row;                         // of a tile of K or V
-    static constexpr int per_load = 1024 / row;                       // rows of a wave's load
-    // XOR of a row's chunks
-    static __device__ __forceinline__ int swz_k(int r) { return chunks == 8 ? (r >> 1) & 7 : r & 15; }
-    static __device__ __forceinline__ int swz_v(int r) { return chunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; }
+struct Layout : LdsRow<D> {
+    typedef LdsRow<D> R;
+    static constexpr int bytes = kTile * R::row;  // of a tile of K or V
+    static __device__ __forceinline__ int swz_v(int r) { return R::chunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; }
 };
 
 template <typename T, int D>
@@ -173,12 +147,8 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
         // V fragments (16 keys, 32 elements)
         u4 vf[kAheadV];
         auto read_v = [&](int i) {
-            typedef __attribute__((address_space(3))) s4 l_s4;
-            typedef uint32_t u2 __attribute__((ext_vector_type(2)));
             const char* src = sh + 2 * L::bytes + (at_v ^ (64 * (i % DT))) + 16 * (i / DT) * L::row;
-            const u2 x = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)src));
-            const u2 y = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((l_s4*)(src + 8 * L::row)));
-            vf[i % kAheadV] = u4{x.x, x.y, y.x, y.y};
+            vf[i % kAheadV] = read_transposed(src, src + 8 * L::row);
         };
         int page0 = 0, page1 = 0, page2 = 0;  // pages of this tile, the next one and the one behind that
         float top;                            // the maximum of the scores in `now` (no masks)
