@@ -559,8 +559,8 @@ bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256
 // first one (measured 5 to 7 us) and the parts' way to memory and back; taking items
 // whole costs what the longest of them takes alone.  Both are estimated from the
 // longest context and the most new tokens of a sequence, as far as the caller
-// knows them.  Measured, a workgroup takes 3 us for a step of k_attn's waves (8 x
-// 32 keys of 128: a CU's loads in flight bound it) and 1.5 us for a tile of k_attn_tile.
+// knows them.  Measured, a workgroup takes 1.6 us for a step of k_attn's waves (8 x
+// 32 keys of 128) and 1.5 us for a tile of k_attn_tile.
 AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
     AttnShape s = {};
     const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
@@ -576,7 +576,7 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
         s.rows = most <= 16 ? 16 : 32;
         s.step = kStep;
         slots = cus;
-        us = 3.0 * keys * c.head_dim / (256 * 128);
+        us = 1.7 * keys * c.head_dim / (256 * 128);
     } else {
         s.rows = 128;
         s.step = 64;
