@@ -75,6 +75,16 @@ CASES = [
     ([(1, 900), (20, 900), (100, 130)], 24, 8, 2, 128, 100),
     ([(300, 1000)], 32, 4, 1, 96, 257),
     ([(64, 300)], 64, 2, 1, 256, 33),
+    ([(5, 300), (6, 77), (1, 1)], 16, 10, 2, 64, 0),     # 17 .. 32 rows of a kv head
+    ([(5, 300), (6, 77), (1, 1)], 24, 10, 2, 96, 50),
+    ([(5, 2000), (6, 77), (1, 1)], 16, 10, 2, 128, 0),
+    ([(5, 300), (6, 1500), (1, 1)], 8, 10, 2, 256, 0),
+    ([(64, 4000)], 32, 4, 2, 128, 0),                    # few items of many rows: cut
+    ([(40, 5000), (130, 2500)], 64, 4, 1, 64, 3001),
+    ([(33, 3500)], 16, 2, 1, 256, 0),
+    ([(1, 6000)], 16, 2, 1, 256, 0),
+    ([(1, 20000), (1, 3)], 128, 8, 1, 128, 0),
+    ([(1, 9000)] + [(0, 50)] * 70 + [(1, 100)] * 3, 64, 4, 1, 96, 0),  # more than 64 sequences, most without new tokens
 ]
 
 
@@ -201,6 +211,110 @@ def test_workspace_and_stream():
     got = q4.q4_attention_paged(cache, dev, dq, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+def test_captured_with_new_lengths():
+    """A graph of a decode step (append and attention) replayed with other lengths, tables and tokens in the same
+    tensors, a second graph of the same cache in between and eager work too: every replay as the eager call."""
+    q4 = lib()
+    page, hk, hq, dim = 16, 2, 8, 128
+    steps = [[(1, 40), (1, 700), (1, 3)], [(1, 41), (1, 701), (1, 4)], [(1, 1), (1, 2000), (0, 77)], [(1, 500), (0, 0), (1, 16)]]
+    batches = [kv_ref.Batch(lens, page, spare=300, seed=i, columns=130) for i, lens in enumerate(steps)]
+    pages = max(b.pages for b in batches)
+    g = torch.Generator().manual_seed(1)
+    kc, vc = (torch.randn(pages, hk, page, dim, generator=g).half().cuda() for _ in range(2))
+    cache = q4.KVCache(kc, vc)
+    table, start, ctx = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((3, 130), (4,), (3,)))
+    batch = q4.KVBatch(table, start, ctx, max_query_len=1, max_context_len=2080)
+    packed = torch.zeros(3, (hq + 2 * hk) * dim, device="cuda")
+    q, k, v = packed.view(3, -1, dim).split([hq, hk, hk], 1)
+    freq, _ = q4.rope_frequencies(dim)
+    out, out2 = (torch.zeros(3, hq, dim, dtype=torch.float16, device="cuda") for _ in range(2))
+
+    def step(to):
+        turned = q4.q4_kv_append(cache, batch, k, v, q=q, inv_freq=freq)
+        q4.q4_attention_paged(cache, batch, turned, out=to)
+
+    def load(i):
+        b = batches[i % len(steps)]
+        table.copy_(torch.from_numpy(b.table))
+        start.copy_(torch.from_numpy(b.start))
+        ctx.copy_(torch.tensor(b.ctx, dtype=torch.int32))
+        packed.copy_(torch.randn(packed.shape, generator=g))
+
+    load(0)
+    step(out)
+    torch.cuda.synchronize()
+    graphs = []
+    for to in (out, out2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(to)
+        graphs.append(graph)
+    for i in range(8):
+        load(i)
+        out.fill_(3.0)
+        out2.fill_(3.0)
+        kc0, vc0 = kc.clone(), vc.clone()
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        got_k, got_v = kc.clone(), vc.clone()
+        kc.copy_(kc0)
+        vc.copy_(vc0)
+        want = torch.full_like(out, 3.0)
+        step(want)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(out2, want), i
+        assert torch.equal(kc, got_k) and torch.equal(vc, got_v), i
+
+
+def test_layer_step_with_the_products():
+    """A decoder layer's attention block as a program runs it: the q, k and v products (GEMV of one token, small-M of
+    a chunk) into packed rows, append with rotation, attention, the o product; against the same chain in 64 bits from
+    the products' own outputs on."""
+    import oracle
+    import synth
+    q4 = lib()
+    hidden, hq, hk, dim, page = 512, 8, 2, 64, 16
+    rows = (hq + 2 * hk) * dim
+    wq = synth.q4_0(synth.DEFAULT_SEED, 7001, rows, hidden)
+    wo = synth.q4_0(synth.DEFAULT_SEED, 7002, hidden, hq * dim)
+    dwq, dwo = torch.from_numpy(wq).cuda(), torch.from_numpy(wo).cuda()
+    kc, vc = (torch.zeros(12, hk, page, dim, dtype=torch.float16, device="cuda") for _ in range(2))
+    cache = q4.KVCache(kc, vc)
+    freq, _ = q4.rope_frequencies(dim)
+    table = torch.tensor([[7, 2, 9, 4, 0, 11]], dtype=torch.int32, device="cuda")
+    done = 0
+    keys, values = [], []
+    for n in (16, 1, 1, 5, 1):  # a chunk of the prompt, decode, a draft's verify
+        x = torch.from_numpy(synth.f16_normal(synth.DEFAULT_SEED, 7100 + done, n * hidden).reshape(n, hidden)).cuda()
+        packed = q4.q4_0_gemv(dwq, x[0].contiguous()).view(1, -1) if n == 1 else q4.q4_0_gemm_smallm(dwq, x)
+        q, k, v = packed.view(n, -1, dim).split([hq, hk, hk], 1)
+        batch = q4.KVBatch(table, torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                           torch.tensor([done + n], dtype=torch.int32, device="cuda"), max_query_len=n, max_context_len=96)
+        turned = q4.q4_kv_append(cache, batch, k, v, q=q, inv_freq=freq)
+        out = q4.q4_attention_paged(cache, batch, turned)
+        y = q4.q4_0_gemv(dwo, out.view(-1)) if n == 1 else q4.q4_0_gemm_smallm(dwo, out.view(n, -1))
+        torch.cuda.synchronize()
+        # the oracle's cache: the same roundings to 16 bits as the operators document
+        pos = torch.arange(done, done + n)
+        keys.append(kv_ref.rotate(k.double().cpu(), pos, freq.cpu(), "half").half())
+        values.append(v.half().cpu())
+        at = [(int(table[0, p // page]), p % page) for p in range(done + n)]
+        got_k = torch.stack([kc[a, :, s] for a, s in at]).cpu()
+        got_v = torch.stack([vc[a, :, s] for a, s in at]).cpu()
+        assert torch.equal(got_v, torch.cat(values))
+        want_k = torch.cat(keys).double()
+        # a value next to a border between two halves may go to the other one: a step of it
+        assert bool(((got_k.double() - want_k).abs() <= 2.0 ** -10 * want_k.abs() + 2.0 ** -24).all())
+        ref = kv_ref.Batch([(n, done + n)], page)
+        ref.table, ref.pages = table.cpu().numpy(), 12
+        want, _, bound, _ = kv_ref.attention(turned.cpu(), kc.cpu(), vc.cpu(), ref, dim ** -0.5, 0)
+        assert bool(((out.double().cpu() - want).abs() <= bound).all())
+        y_ref, a_ref = oracle.gemm_rows(wo, hq * dim, out.cpu().numpy().reshape(n, -1))
+        assert bool((np.abs(y.cpu().numpy().reshape(n, -1) - y_ref.reshape(n, -1)) <= oracle.TOL * a_ref.reshape(n, -1)).all())
+        done += n
 
 
 def test_far_offsets():
