@@ -252,7 +252,9 @@ __device__ __forceinline__ float add_pair(uint32_t p, float l) {
         const h2 one = {(_Float16)1.0f, (_Float16)1.0f};
         return __builtin_amdgcn_fdot2(as_h2(p), one, l, false);
     } else {
-        return l + (__builtin_bit_cast(float, p << 16) + __builtin_bit_cast(float, p & 0xFFFF0000u));
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        const b2 one = {(__bf16)1.0f, (__bf16)1.0f};
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, p), one, l, false);
     }
 }
 

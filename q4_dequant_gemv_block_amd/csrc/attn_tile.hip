@@ -47,7 +47,6 @@ struct Mma32<BF16> {
 
 constexpr int kTile = 64;  // keys of a tile
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kAheadK = 4, kAheadV = 3;  // LDS reads ahead of the products
 
 // Places in LDS (rows and their swizzles as described above).
 template <int D>
@@ -63,6 +62,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
     constexpr int NW = kWaves, ROWS = 32 * NW;
     constexpr int KS = D / 16;                         // k-steps of the first product
     constexpr int DT = D / 32;                         // 32-element tiles of the output
+    constexpr int kAheadK = D == 128 ? 3 : 4, kAheadV = D == 128 ? 2 : 3;  // LDS reads ahead of the products, as registers allow
     constexpr int LOADS = kTile / L::per_load / NW;    // loads of a wave for K, and for V, of a tile
     constexpr int GROUPS = 8 / NW;                     // groups of 8 keys they cover
     constexpr int PER_GROUP = LOADS / GROUPS;
@@ -154,9 +154,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
         float top;                            // the maximum of the scores in `now` (no masks)
 
         // S^T of a tile by itself.
-        float now[32];  // scores of this tile
-        auto scores = [&]() {
-            f16v s[2];
+        auto scores = [&](f16v (&s)[2]) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -168,11 +166,9 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             }
             top = s[0][0];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                now[i] = s[i >> 4][i & 15];
-                top = fmaxf(top, now[i]);
-            }
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i >> 4][i & 15]);
         };
+        f16v even[2], odds[2];  // scores of this tile and of the next one, in turn
 
         if (it.k_lo < it.k_hi) {
             const int t = it.k_lo;
@@ -189,11 +185,11 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             } else {
                 asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LOADS) : "memory");
             }
-            scores();
+            scores(even);
         }
-        // One tile: its scores are in `now`, the next one's follow there.
+        // One tile: its scores are in `now`, the next one's will be in `next`.
         int stage = 0;
-        for (int t = it.k_lo; t < it.k_hi; t += kTile, stage ^= 1, at_v ^= L::bytes) {
+        auto tile = [&](int t, f16v (&now)[2], f16v (&next)[2]) {
             at_k ^= L::bytes;
             asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");  // V of this tile and K of the next are there, the places of K of this one and V of the last free
             const bool more = t + kTile < it.k_hi;
@@ -251,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        now[16 * u + i] = keep_seen(now[16 * u + i], bit_mask((uint32_t)(seen >> (32 * u)), 8 * (i >> 2) + (i & 3)));
-                        top = fmaxf(top, now[16 * u + i]);
+                        now[u][i] = keep_seen(now[u][i], bit_mask((uint32_t)(seen >> (32 * u)), 8 * (i >> 2) + (i & 3)));
+                        top = fmaxf(top, now[u][i]);
                     }
             }
             top *= a.scale_log2;
@@ -272,22 +268,21 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             // exponentials at a time, those in three stages (exponent, exp2,
             // rounding and sum) so that no instruction waits for the one before.
             u4 p[4];
-            f16v next[2];
             constexpr int STEPS = 2 * KS;
             auto exponent = [&](int j) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    now[2 * j + e] = __builtin_fmaf(now[2 * j + e], a.scale_log2, -ref);
+                    now[j >> 3][2 * (j & 7) + e] = __builtin_fmaf(now[j >> 3][2 * (j & 7) + e], a.scale_log2, -ref);
                 }
             };
             auto power = [&](int j) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    now[2 * j + e] = __builtin_amdgcn_exp2f(now[2 * j + e]);
+                    now[j >> 3][2 * (j & 7) + e] = __builtin_amdgcn_exp2f(now[j >> 3][2 * (j & 7) + e]);
                 }
             };
             auto weight = [&](int j) {
-                p[j >> 2][j & 3] = pack2<T>(now[2 * j], now[2 * j + 1]);
+                p[j >> 2][j & 3] = pack2<T>(now[j >> 3][2 * (j & 7)], now[j >> 3][2 * (j & 7) + 1]);
                 l = add_pair<T>(p[j >> 2][j & 3], l);
             };
             // pairs [16 s / STEPS, 16 (s + 1) / STEPS) (rounded up) belong to step s
@@ -345,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                 }
             }
             // O^T += V^T P^T, and the maximum of the next tile's scores
+            __builtin_amdgcn_s_setprio(1);  // the wave that has its weights goes first: the CU's other waves then have theirs to make (2 to 3 %)
             top = next[0][0];
 #pragma unroll
             for (int i = 0; i < 4 * DT; ++i) {
@@ -353,17 +349,24 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
 #pragma unroll
                 for (int e = 0; e < (8 + DT - 1) / DT; ++e) {
                     const int j = (8 * i + DT - 1) / DT + e;
-                    if (j < (8 * (i + 1) + DT - 1) / DT) {
-                        now[j] = next[j >> 4][j & 15];
-                        top = fmaxf(top, now[j]);
-                    }
+                    if (j < (8 * (i + 1) + DT - 1) / DT) top = fmaxf(top, next[j >> 4][j & 15]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+            __builtin_amdgcn_s_setprio(0);
+            stage ^= 1;
+            at_v ^= L::bytes;
+        };
+        for (int t = it.k_lo; t < it.k_hi; t += 2 * kTile) {
+            tile(t, even, odds);
+            if (t + kTile < it.k_hi) tile(t + kTile, odds, even);
         }
         __syncthreads();  // all tiles are read before the next item's
 
         l += __shfl_xor(l, 32);
+        // (lane numbers anew: addresses made from them would be held through the loop)
+        int n = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+        asm volatile("" : "+v"(n), "+v"(h));
         if (32 * wave + n >= it.rows) continue;
         if (it.u0 == 0 && it.u1 == seq.units) {
             const float f = row_scale(l);
