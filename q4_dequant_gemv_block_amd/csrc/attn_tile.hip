@@ -27,6 +27,7 @@ namespace q4 {
 namespace {
 
 typedef float f16v __attribute__((ext_vector_type(16)));
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 
 template <typename T>
 struct Mma32;
@@ -206,21 +207,32 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             // infinities, which are added below row by row.
             bool odd = false;
             if (valid != 0xFF || t + kTile > min(it.k_hi, it.p_first + 1) || (a.window && t <= it.p_last - a.window)) {
-                bool mine = false;
                 char* tv = sh + (2 + stage) * L::bytes;
-                for (int u = threadIdx.x; u < kTile * L::chunks; u += kThreads) {
-                    const int r = u / L::chunks, c = (u % L::chunks) ^ L::swz_v(r);
-                    if (c >= D / 8) continue;
+                int thread = threadIdx.x;
+                asm volatile("" : "+v"(thread));  // made anew: addresses from it would be held through the loop
+                constexpr int MINE = kTile * L::chunks / kThreads;  // chunks a thread looks at
+                const bool full = t + kTile <= it.k_hi && valid == 0xFF;
+                us2 most = {0, 0};  // the largest magnitude, as bits
+#pragma unroll
+                for (int k = 0; k < MINE; ++k) {
+                    const int u = thread + k * kThreads, r = u / L::chunks;
+                    if (D != 8 * L::chunks && ((u % L::chunks) ^ L::swz_v(r)) >= D / 8) continue;
                     u4* at = reinterpret_cast<u4*>(tv + u * 16);
-                    if (t + r >= it.k_hi || !((valid >> (r >> 3)) & 1)) {
+                    if (!full && (t + r >= it.k_hi || !((valid >> (r >> 3)) & 1))) {
                         *at = u4{0, 0, 0, 0};
-                    } else {
+                        continue;
+                    }
+                    const u4 v = *at & 0x7FFF7FFFu;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) most = __builtin_elementwise_max(most, __builtin_bit_cast(us2, (uint32_t)v[e]));
+                }
+                constexpr unsigned short infinity = std::is_same<T, F16>::value ? 0x7C00 : 0x7F80;
+                const bool mine = max(most.x, most.y) >= infinity;
+                if (mine) {
+                    for (int u = thread; u < kTile * L::chunks; u += kThreads) {
+                        u4* at = reinterpret_cast<u4*>(tv + u * 16);
                         const u4 v = *at;
-                        const u4 bad = {nonfinite<T>(v.x), nonfinite<T>(v.y), nonfinite<T>(v.z), nonfinite<T>(v.w)};
-                        if (bad.x | bad.y | bad.z | bad.w) {
-                            *at = v & ~bad;
-                            mine = true;
-                        }
+                        *at = v & ~u4{nonfinite<T>(v.x), nonfinite<T>(v.y), nonfinite<T>(v.z), nonfinite<T>(v.w)};
                     }
                 }
                 int* flags = reinterpret_cast<int*>(sh + 4 * L::bytes);
