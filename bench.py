@@ -1,7 +1,7 @@
 """Benchmark of the Q4_0 dequantize-and-multiply path on one MI355X.
 
     python bench.py [--gpus 1] [--steps K] [--warmup W]
-                    [--workload sweep|gemv|lmhead|lmhead_norm|handoff|q8|verify|smallm|prefill|copy|stream]
+                    [--workload sweep|gemv|lmhead|lmhead_norm|handoff|q8|verify|smallm|prefill|attention|copy|stream]
                     [--m M] [--pattern P --wg-per-cu W]
 
 Default workload ("sweep"): the 27B-shaped decode weight sweep, 64 layers x
@@ -20,7 +20,9 @@ Other workloads print the same kind of line for the single 5120x5120 GEMV
 the LM head with argmax (with the final norm fused: lmhead_norm), the stage
 hand-off (a 22-layer range ending in the binary16 hidden state: handoff), the Q8_0 GEMV over a
 small dense model's layers (q8), the greedy
-verify of an M-row draft, small-M (--m) and prefill (--m) over the sweep.
+verify of an M-row draft, small-M (--m) and prefill (--m) over the sweep, and
+the cache append and attention of a decode step of M sequences over a small
+dense model's layers (attention).
 """
 from __future__ import annotations
 
@@ -51,7 +53,9 @@ def log(*a):
 KERNEL_SOURCE = {"sweep": ["gemv.hip"], "gemv": ["gemv.hip"], "lmhead": ["gemv.hip"], "lmhead_norm": ["gemv.hip"],
                  "handoff": ["gemv.hip"], "q8": ["gemv.hip", "q8.hip"],
                  "smallm": ["smallm.hip"],
-                 "prefill": ["prefill.hip"], "verify": ["smallm.hip", "gemv.hip", "verify.hip"]}
+                 "prefill": ["prefill.hip"], "verify": ["smallm.hip", "gemv.hip", "verify.hip"],
+                 "attention": ["rope.hip", "attention.hip", "attn_tile.hip", "attn_device.h", "kv_device.h",
+                               "kv_launch.h", "kv_api.cpp"]}
 
 
 def kernel_source_hash(workload: str) -> str:
@@ -584,6 +588,54 @@ def bench_gemm(args, prefill: bool):
             **extra}
 
 
+def bench_attention(args):
+    """What lies between the q/k/v and the o products of a decode step, for M
+    sequences of 4,096 tokens and the small dense model's 36 layers (32 query
+    and 8 key/value heads of 128): the new token's keys and values appended
+    with their rotation, then attention.  One step = the 72 calls, captured
+    into one HIP graph."""
+    import torch
+    q4 = load_q4()
+    m = args.m or 8
+    layers, hq, hk, dim, page, ctx = 36, 32, 8, 128, 64, 4096
+    need = ctx // page
+    gen = torch.Generator(device="cuda").manual_seed(SEED)
+    freq, _ = q4.rope_frequencies(dim, 1e6)
+    table = torch.randperm(m * need, device="cuda", generator=gen).to(torch.int32).view(m, need)
+    batch = q4.KVBatch(table, torch.arange(m + 1, dtype=torch.int32, device="cuda"),
+                       torch.full((m,), ctx, dtype=torch.int32, device="cuda"), max_query_len=1, max_context_len=ctx)
+    state = []
+    for _ in range(layers):
+        k, v = (torch.randn((m * need, hk, page, dim), generator=gen, device="cuda", dtype=torch.float16)
+                for _ in range(2))
+        packed = torch.randn((m, hq + 2 * hk, dim), generator=gen, device="cuda")
+        state.append((q4.KVCache(k, v), packed.split([hq, hk, hk], 1),
+                      torch.empty((m, hq, dim), dtype=torch.float16, device="cuda")))
+
+    def calls():
+        for cache, (q, k, v), out in state:
+            turned = q4.q4_kv_append(cache, batch, k, v, q=q, inv_freq=freq)
+            q4.q4_attention_paged(cache, batch, turned, out=out)
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    ms = time_steps(graph.replay, args.steps, args.warmup, settle_s=SETTLE_S)
+    bytes_ = layers * m * (2 * ctx * hk * dim * 2 + (hq + 2 * hk) * dim * 4 + 3 * hq * dim * 2 + 2 * hk * dim * 2)
+    gbs = bytes_ / (ms * 1e-3) / 1e9
+    return {"metric": "cache append and attention of a decode step, HBM GB/s (%d sequences of %d tokens)" % (m, ctx),
+            "value": round(gbs, 2), "unit": "GB/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+            "ms_per_step": round(ms, 5), "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+            "dtype": "f16->f32", "data": "synthetic",
+            "config": {"workload": "append + attention, %d sequences x %d tokens, 36 layers of 32/8 heads of 128, "
+                                   "one graph" % (m, ctx)},
+            "us_per_layer": round(ms * 1000.0 / layers, 3),
+            "roofline": {"bound": "hbm", "achieved": round(gbs, 2), "peak": PEAK_HBM_GBS, "unit": "GB/s",
+                         "frac": round(gbs / PEAK_HBM_GBS, 4), "traffic": counter_traffic("attention"),
+                         "kernel": "q4::k_attn + q4::k_attn_join"}}
+
+
 STREAM_BYTES = 16 << 30
 # (pattern, workgroups of 256 threads per CU) of the read-ceiling probe: 0/1
 # grid-stride cached / non-temporal loads, 2/3 one contiguous range per
@@ -709,7 +761,7 @@ def main():
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--workload", default="sweep",
                     choices=["sweep", "gemv", "lmhead", "lmhead_norm", "handoff", "q8", "verify", "smallm",
-                             "prefill", "copy", "stream"])
+                             "prefill", "attention", "copy", "stream"])
     ap.add_argument("--m", type=int, default=0)
     ap.add_argument("--pattern", type=int, default=-1, help="stream: one probe pattern (0..4) instead of all")
     ap.add_argument("--wg-per-cu", type=int, default=2, help="stream: workgroups per CU with --pattern")
@@ -732,7 +784,7 @@ def main():
         sys.exit(1)
     fn = {"sweep": bench_sweep, "gemv": bench_gemv, "lmhead": bench_lmhead, "lmhead_norm": bench_lmhead_norm,
           "handoff": bench_handoff, "q8": bench_q8,
-          "verify": bench_verify, "copy": bench_copy, "stream": bench_stream,
+          "verify": bench_verify, "attention": bench_attention, "copy": bench_copy, "stream": bench_stream,
           "smallm": lambda a: bench_gemm(a, False), "prefill": lambda a: bench_gemm(a, True)}[args.workload]
     out = fn(args)
     print(json.dumps(out), flush=True)
