@@ -517,7 +517,7 @@ hipError_t launch(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
 template <typename T, int D>
 hipError_t launch_dim(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
     hipError_t e = hipErrorInvalidValue;
-    if (shape.rows == 128)
+    if (shape.rows >= 64)
         e = launch_attn_tile<T, D>(a, make_cut(a, shape), shape, s);
     else if (shape.rows == 16)
         e = launch<T, D, 1>(a, shape, s);
@@ -555,14 +555,15 @@ hipError_t LdsLimit::raise(const void* kernel, size_t bytes) {
 
 bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
 
-// Items are taken whole or cut.  Cutting costs a launch that waits for the
-// first one (measured 5 to 7 us) and the parts' way to memory and back; taking items
-// whole costs what the longest of them takes alone.  Both are estimated from the
-// longest context and the most new tokens of a sequence, as far as the caller
-// knows them.  Measured, a workgroup takes 1.6 us for a step of k_attn's waves (8 x
-// 32 keys of 128) and 1.5 us for a tile of k_attn_tile.
+// How a call is cut: the rows of an item, and whether items are taken whole or
+// in parts.  Parts cost a launch that waits for the first one (measured 5 to 7
+// us) and their way to memory and back; whole items cost what the longest of
+// them takes alone.  Both are estimated from the longest context and the most
+// new tokens of a sequence, as far as the caller knows them, and the cheapest
+// way is taken.  Measured (head_dim 128): a step of k_attn's waves (256 keys) takes
+// 1.7 us, a tile of k_attn_tile 1.1 us (64 rows) or 1.5 us (128) for a workgroup
+// alone on a CU and 1.3 or 1.9 us where two share it, the join of two waves 0.6 us.
 AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
-    AttnShape s = {};
     const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
     const int64_t longest = max_query > 0 ? std::min<int64_t>(max_query, tokens) : tokens;  // new tokens of a sequence
     const int64_t most = longest * group;
@@ -570,43 +571,50 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
     const int cus = compute_units();
     int64_t keys = max_context > 0 ? std::min<int64_t>(max_context, capacity) : capacity;
     if (window) keys = std::min<int64_t>(keys, window + longest);
-    double us;  // of a whole item
-    int slots;  // workgroups that run at a time
+    // A sequence's rows see its context less half of the new tokens on average.
+    const double seen = window ? 1.0 : 1.0 - 0.5 * longest / std::max<double>(keys, longest);
+    AttnShape best = {};
+    double best_us = 0;
+    auto consider = [&](int rows, int step, int slots, double alone, double shared) {  // us of a whole item
+        AttnShape s = {};
+        s.rows = rows;
+        s.step = step;
+        s.unit = 64;
+        s.most_rows = (int)std::min<int64_t>(rows, most);
+        const double items = (double)c.kv_heads * (longest * seqs == tokens ? seqs * ((most + rows - 1) / rows) : (tokens * group + rows * seqs / 2) / rows);
+        const double us = items > cus ? shared : alone;
+        const double whole = items > slots ? us * seen * items / slots + 0.5 * us : us;
+        // ranges of equal units, of which an item counts as many as its sequence's longest
+        const double parts = std::min<double>(slots, items * keys / s.unit);
+        const double join = 7.5 + parts * s.most_rows * c.head_dim * 8 / 4e6;  // written and read at about 4 TB/s
+        const double cut = shared * items / slots + join;
+        const int64_t bound = item_bound(c, b, q_heads, tokens, rows);
+        if (whole <= cut && bound < (int64_t(1) << 31)) {
+            s.unit = 1 << 30;
+            s.grid = (int)bound;
+        } else {
+            // larger units where this many would pass 31 bits
+            while (s.unit < (1 << 30) && bound * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;
+            s.grid = slots;
+            s.few = items * 8 <= slots;
+            s.bytes = (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + sizeof(f2));
+        }
+        if (!best.rows || std::min(whole, cut) < best_us) {
+            best = s;
+            best_us = std::min(whole, cut);
+        }
+    };
+    const double dim = c.head_dim / 128.0;
     if (most <= 32) {
-        s.rows = most <= 16 ? 16 : 32;
-        s.step = kStep;
-        slots = cus;
-        us = 1.7 * keys * c.head_dim / (256 * 128);
+        const double us = 1.7 * keys / 256 * dim;
+        consider(most <= 16 ? 16 : 32, kStep, cus, us, us);
     } else {
-        s.rows = 128;
-        s.step = 64;
-        slots = c.head_dim <= 128 ? 2 * cus : cus;
-        us = 1.5 * (keys + 63) / 64 * c.head_dim / 128;
+        const double tiles = (keys + 63) / 64 * dim;
+        const int slots = c.head_dim <= 128 ? 2 * cus : cus;
+        consider(64, 64, slots, 1.1 * tiles + 0.6, 1.3 * tiles + 0.6);
+        consider(128, 64, slots, 1.5 * tiles, 1.9 * tiles);
     }
-    s.unit = 64;
-    s.most_rows = (int)std::min<int64_t>(s.rows, most);
-    // Whole: the longest item, or all of them (a sequence's rows see its context
-    // less half of the new tokens on average) and half an item for what the last
-    // ones run alone.  Cut: ranges of equal units, of which an item counts as
-    // many as its sequence's longest.
-    const double items = (double)c.kv_heads * (seqs == 1 ? (tokens * group + s.rows - 1) / s.rows : (tokens * group + s.rows * seqs / 2) / s.rows);
-    const double mean = window ? us : us * (1.0 - 0.5 * longest / std::max<double>(keys, longest));
-    const double parts = std::min<double>(slots, items * keys / s.unit);
-    const double join = 7.5 + parts * s.most_rows * c.head_dim * 8 / 4e6;  // written and read at about 4 TB/s
-    const double cut = us * items / slots + join;
-    const bool whole = items > slots ? mean * items / slots + 0.5 * us <= cut : us <= cut;
-    const int64_t bound = item_bound(c, b, q_heads, tokens, s.rows);
-    if (whole && bound < (int64_t(1) << 31)) {
-        s.unit = 1 << 30;
-        s.grid = (int)bound;
-        return s;
-    }
-    // Larger units where this many would pass 31 bits.
-    while (s.unit < (1 << 30) && bound * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;
-    s.grid = slots;
-    s.few = items * 8 <= slots;
-    s.bytes = (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + sizeof(f2));
-    return s;
+    return best;
 }
 
 hipError_t launch_attention(const AttnArgs& a, const AttnShape& shape, int type, hipStream_t s) {

@@ -2,11 +2,14 @@
 // paged cache: the same items, units and ranges as k_attn, in tiles that the
 // matrix cores are the bound of.
 //
-// A workgroup of 4 waves holds 128 query rows, 32 a wave, and goes through its
-// keys 64 at a time; two of them share a CU (8 waves of 256 rows that share the
-// tiles were no faster: 606 us against 578 for a prompt of 8192).  K and V go from
-// HBM or L2 straight into LDS (global_load_lds, 16 bytes a lane), two tiles of each
-// deep, one barrier a tile.  The products run on v_mfma_f32_32x32x16:
+// A workgroup of 4 waves holds 64 U query rows and goes through its keys 64 at a
+// time.  With U = 2 a wave has 32 rows and all keys; with U = 1, for calls whose rows
+// leave the machine idle, two waves share 32 rows, 32 keys of a tile each, and join
+// at the end (a prompt of 256 tokens and 40 heads 14.1 -> 11.7 us).  Two workgroups
+// share a CU (8 waves of 256 rows that share the tiles were no faster: 606 us
+// against 578 for a prompt of 8192).  K and V go from HBM or L2 straight into LDS
+// (global_load_lds, 16 bytes a lane), two tiles of each deep, one barrier a tile.
+// The products run on v_mfma_f32_32x32x16:
 //   S^T = K Q^T: A = 32 keys from LDS, B = Q^T, which stays in registers;
 //   O^T = V^T P^T: A = V^T by the transposing LDS read (ds_read_b64_tr_b16: 16
 //     lanes read 4 keys of 16 elements and get one element's 4 keys each), B =
@@ -57,19 +60,22 @@ struct Layout : LdsRow<D> {
     static __device__ __forceinline__ int swz_v(int r) { return R::chunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; }
 };
 
-template <typename T, int D>
+template <typename T, int D, int U>
 __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const AttnArgs a, const Cut cut) {
     typedef Layout<D> L;
-    constexpr int NW = kWaves, ROWS = 32 * NW;
+    constexpr int NW = kWaves, ROWS = 64 * U;
+    constexpr int PAIRS = 8 * U;                       // pairs of scores of a tile a lane has
     constexpr int KS = D / 16;                         // k-steps of the first product
     constexpr int DT = D / 32;                         // 32-element tiles of the output
-    constexpr int kAheadK = D == 128 ? 3 : 4, kAheadV = D == 128 ? 2 : 3;  // LDS reads ahead of the products, as registers allow
+    constexpr int kAheadK = U * D == 256 ? 3 : 4, kAheadV = U * D == 256 ? 2 : 3;  // LDS reads ahead of the products, as registers allow
     constexpr int LOADS = kTile / L::per_load / NW;    // loads of a wave for K, and for V, of a tile
     constexpr int GROUPS = 8 / NW;                     // groups of 8 keys they cover
     constexpr int PER_GROUP = LOADS / GROUPS;
     extern __shared__ char sh[];  // K [2][64][row], V [2][64][row], then a flag of each wave
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int h = lane >> 5, n = lane & 31;
+    const int rows32 = U == 2 ? wave : wave & 1;      // the wave's 32 rows of the item's
+    const int first = U == 2 ? 0 : 32 * (wave >> 1);  // its first key of a tile
     const uint32_t sh0 = lds_address(sh);
 
     Work work;
@@ -79,11 +85,11 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
     Item it;
 
     // where this lane reads in a tile: chunks 2 s + h of K's rows, 64-byte block d of V's
-    int at_k0 = n * L::row + ((h ^ L::swz_k(n)) * 16), at_v0;
+    int at_k0 = (first + n) * L::row + ((h ^ L::swz_k(n)) * 16), at_v0;
     {
         const int g = lane >> 4, r = 4 * (g >> 1) + ((lane >> 2) & 3);
         const int c = 2 * (g & 1) + ((lane & 3) >> 1);
-        at_v0 = r * L::row + ((c ^ L::swz_v(r)) * 16) + (lane & 1) * 8;
+        at_v0 = (first + r) * L::row + ((c ^ L::swz_v(r)) * 16) + (lane & 1) * 8;
     }
 
     while (work.next(cut, a.batch, &it)) {
@@ -92,13 +98,13 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
         const char* vbase = a.cache.v + (int64_t)it.head * a.cache.v_head * 2;
 
         // this lane's query row and the wave's first and last positions
-        const int row = it.row0 + 32 * wave + n;
+        const int row = it.row0 + 32 * rows32 + n;
         const int rc = min(row, it.row0 + it.rows - 1);
         const int qi = (int)cut.group.div(rc), qh = it.head * a.group + rc - qi * a.group;
         const int pos = it.past + qi;
-        const int w_rows = min(32, it.rows - 32 * wave);  // may be <= 0
-        const int w_first = it.past + (int)cut.group.div(it.row0 + 32 * wave);
-        const int w_last = it.past + (int)cut.group.div(it.row0 + 32 * wave + max(w_rows, 1) - 1);
+        const int w_rows = min(32, it.rows - 32 * rows32);  // may be <= 0
+        const int w_first = it.past + (int)cut.group.div(it.row0 + 32 * rows32);
+        const int w_last = it.past + (int)cut.group.div(it.row0 + 32 * rows32 + max(w_rows, 1) - 1);
         u4 qf[KS];
         {
             const char* src = a.q.data + ((int64_t)(seq.row0 + qi) * a.q.token_stride + (int64_t)qh * a.q.head_stride + 8 * h) * 2;
@@ -143,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
         u4 kf[kAheadK];
         int at_k = at_k0, at_v = at_v0;  // in the tile to read next: toggled, its places are a power of 2 apart
         auto read_k = [&](int i) {
-            kf[i % kAheadK] = *reinterpret_cast<const u4*>(sh + (at_k ^ (32 * (i >> 1))) + (i & 1) * 32 * L::row);
+            kf[i % kAheadK] = *reinterpret_cast<const u4*>(sh + (at_k ^ (32 * (i / U))) + i % U * 32 * L::row);
         };
         // V fragments (16 keys, 32 elements)
         u4 vf[kAheadV];
@@ -155,21 +161,21 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
         float top;                            // the maximum of the scores in `now` (no masks)
 
         // S^T of a tile by itself.
-        auto scores = [&](f16v (&s)[2]) {
+        auto scores = [&](f16v (&s)[U]) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2 * KS; ++i) {
+            for (int i = 0; i < U * KS; ++i) {
                 read_k(i);
-                s[i & 1] = Mma32<T>::mma(kf[i % kAheadK], qf[i >> 1], s[i & 1]);
+                s[i % U] = Mma32<T>::mma(kf[i % kAheadK], qf[i / U], s[i % U]);
             }
             top = s[0][0];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i >> 4][i & 15]);
+            for (int i = 0; i < 16 * U; ++i) top = fmaxf(top, s[i >> 4][i & 15]);
         };
-        f16v even[2], odds[2];  // scores of this tile and of the next one, in turn
+        f16v even[U], odds[U];  // scores of this tile and of the next one, in turn
 
         if (it.k_lo < it.k_hi) {
             const int t = it.k_lo;
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
         }
         // One tile: its scores are in `now`, the next one's will be in `next`.
         int stage = 0;
-        auto tile = [&](int t, f16v (&now)[2], f16v (&next)[2]) {
+        auto tile = [&](int t, f16v (&now)[U], f16v (&next)[U]) {
             at_k ^= L::bytes;
             asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");  // V of this tile and K of the next are there, the places of K of this one and V of the last free
             const bool more = t + kTile < it.k_hi;
@@ -253,10 +259,10 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                     x = (x | (x << 7)) & 0x0101010101010101ull;
                     seen &= x * 0xFF;
                 }
-                seen >>= 4 * h;  // the lane's keys are 8 (i / 4) + i % 4 of what is left
+                seen >>= first + 4 * h;  // the lane's keys are 8 (i / 4) + i % 4 of what is left
                 top = kNone;
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         now[u][i] = keep_seen(now[u][i], bit_mask((uint32_t)(seen >> (32 * u)), 8 * (i >> 2) + (i & 3)));
@@ -279,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             // weights are made: a product, a read ahead and a share of the
             // exponentials at a time, those in three stages (exponent, exp2,
             // rounding and sum) so that no instruction waits for the one before.
-            u4 p[4];
-            constexpr int STEPS = 2 * KS;
+            u4 p[2 * U];
+            constexpr int STEPS = U * KS;
             auto exponent = [&](int j) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -297,25 +303,25 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                 p[j >> 2][j & 3] = pack2<T>(now[j >> 3][2 * (j & 7)], now[j >> 3][2 * (j & 7) + 1]);
                 l = add_pair<T>(p[j >> 2][j & 3], l);
             };
-            // pairs [16 s / STEPS, 16 (s + 1) / STEPS) (rounded up) belong to step s
+            // pairs [PAIRS s / STEPS, PAIRS (s + 1) / STEPS) (rounded up) belong to step s
             auto share = [&](int s, auto what) {
 #pragma unroll
-                for (int e = 0; e < (16 + STEPS - 1) / STEPS; ++e) {
-                    const int j = (16 * s + STEPS - 1) / STEPS + e;
-                    if (j < (16 * (s + 1) + STEPS - 1) / STEPS && j < 16) what(j);
+                for (int e = 0; e < (PAIRS + STEPS - 1) / STEPS; ++e) {
+                    const int j = (PAIRS * s + STEPS - 1) / STEPS + e;
+                    if (j < (PAIRS * (s + 1) + STEPS - 1) / STEPS && j < PAIRS) what(j);
                 }
             };
             share(0, exponent);
             share(1, exponent);
             share(0, power);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) next[u][i] = 0.0f;
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                next[s & 1] = Mma32<T>::mma(kf[s % kAheadK], qf[s >> 1], next[s & 1]);
+                next[s % U] = Mma32<T>::mma(kf[s % kAheadK], qf[s / U], next[s % U]);
                 if (s + kAheadK < STEPS) read_k(s + kAheadK);
                 if (s >= STEPS - kAheadV) read_v(s - (STEPS - kAheadV));
                 share(s + 2, exponent);
@@ -325,14 +331,14 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             }
             if (odd) {
                 // The elements that left the product, for the rows that see them.
-                for (int k = 0; k < kTile && t + k < it.k_hi; ++k) {
+                for (int k = first; k < first + 32 * U && t + k < it.k_hi; ++k) {
                     if (!((valid >> (k >> 3)) & 1)) continue;
                     uint32_t w = 0;
 #pragma unroll
-                    for (int k4 = 0; k4 < 4; ++k4)
+                    for (int k4 = 0; k4 < 2 * U; ++k4)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)  // keys 16 k4 + 8 (j / 2) + 4 h + 2 (j % 2), + 1
-                            if ((k & ~5) == 16 * k4 + 8 * (j >> 1) + 2 * (j & 1)) w = p[k4][j];
+                            if (((k - first) & ~5) == 16 * k4 + 8 * (j >> 1) + 2 * (j & 1)) w = p[k4][j];
                     const float weight = half_of<T>((uint32_t)__shfl((int)w, n + 32 * ((k >> 2) & 1)), k & 1);
                     const bool sees = t + k <= pos && (!a.window || t + k > pos - a.window);
                     const int page = __builtin_amdgcn_readlane(page8, k >> 3);
@@ -355,9 +361,9 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             __builtin_amdgcn_s_setprio(1);  // the wave that has its weights goes first: the CU's other waves then have theirs to make (2 to 3 %)
             top = next[0][0];
 #pragma unroll
-            for (int i = 0; i < 4 * DT; ++i) {
+            for (int i = 0; i < 2 * U * DT; ++i) {
                 acc[i % DT] = Mma32<T>::mma(vf[i % kAheadV], p[i / DT], acc[i % DT]);
-                if (i + kAheadV < 4 * DT) read_v(i + kAheadV);
+                if (i + kAheadV < 2 * U * DT) read_v(i + kAheadV);
 #pragma unroll
                 for (int e = 0; e < (8 + DT - 1) / DT; ++e) {
                     const int j = (8 * i + DT - 1) / DT + e;
@@ -375,11 +381,44 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
         }
         __syncthreads();  // all tiles are read before the next item's
 
+        if constexpr (U == 1) {
+            // the other 32 keys of each tile, from the wave that has them
+            int lane = threadIdx.x & 63;
+            asm volatile("" : "+v"(lane));
+            f4* other = reinterpret_cast<f4*>(sh) + (rows32 * DT * 4) * 64 + lane;
+            f2* other_ml = reinterpret_cast<f2*>(sh + 2 * DT * 4 * 64 * sizeof(f4)) + rows32 * 64 + lane;
+            if (first) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        other[(4 * d + i) * 64] = f4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+                *other_ml = f2{m, l};
+            }
+            __syncthreads();
+            if (!first) {
+                const f2 ml = *other_ml;
+                const float both = fmaxf(m, ml.x), ref = both == kNone ? 0.0f : both;
+                const float f0 = __builtin_amdgcn_exp2f(m - ref), f1 = __builtin_amdgcn_exp2f(ml.x - ref);
+                m = both;
+                l = l * f0 + ml.y * f1;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f4 o = other[(4 * d + i) * 64];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[d][4 * i + e] = acc[d][4 * i + e] * f0 + o[e] * f1;
+                    }
+            }
+            __syncthreads();
+            if (first) continue;
+        }
         l += __shfl_xor(l, 32);
         // (lane numbers anew: addresses made from them would be held through the loop)
         int n = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
         asm volatile("" : "+v"(n), "+v"(h));
-        if (32 * wave + n >= it.rows) continue;
+        if (32 * rows32 + n >= it.rows) continue;
         if (it.u0 == 0 && it.u1 == seq.units) {
             const float f = row_scale(l);
             char* dst = a.out.data + ((int64_t)(seq.row0 + qi) * a.out.token_stride + (int64_t)qh * a.out.head_stride + 4 * h) * 2;
@@ -392,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                 }
             if (a.lse && h == 0) a.lse[(int64_t)(seq.row0 + qi) * a.q_heads + qh] = row_lse(m, l);
         } else {
-            const int64_t slot = ((int64_t)2 * blockIdx.x + (it.u0 == 0)) * ROWS + 32 * wave + n;
+            const int64_t slot = ((int64_t)2 * blockIdx.x + (it.u0 == 0)) * ROWS + 32 * rows32 + n;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -403,16 +442,21 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
     }
 }
 
+template <typename T, int D, int U>
+hipError_t launch(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
+    constexpr size_t lds = (size_t)4 * Layout<D>::bytes + kWaves * sizeof(int);
+    static LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, U>), lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_attn_tile<T, D, U>), dim3(shape.grid), dim3(kThreads), lds, s, a, cut);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 template <typename T, int D>
 hipError_t launch_attn_tile(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
-    constexpr size_t lds = (size_t)4 * Layout<D>::bytes + kWaves * sizeof(int);
-    static LdsLimit limit;
-    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D>), lds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<T, D>), dim3(shape.grid), dim3(kThreads), lds, s, a, cut);
-    return hipGetLastError();
+    return shape.rows == 128 ? launch<T, D, 2>(a, cut, shape, s) : launch<T, D, 1>(a, cut, shape, s);
 }
 
 template hipError_t launch_attn_tile<F16, 64>(const AttnArgs&, const Cut&, const AttnShape&, hipStream_t);

@@ -79,7 +79,7 @@ struct AttnArgs {
 // How a call is cut: a rule on sizes alone, the same for the workspace's size
 // and the launch.
 struct AttnShape {
-    int rows;      // query rows (token, head of the group) of one item: 16, 32 (k_attn), 128 (k_attn_tile)
+    int rows;      // query rows (token, head of the group) of one item: 16, 32 (k_attn), 64, 128 (k_attn_tile)
     int most_rows; // rows that an item has, as far as the caller knows
     int unit;      // keys of one unit of work
     int step;      // keys a kernel takes at a time
