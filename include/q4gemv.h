@@ -513,8 +513,8 @@ typedef struct q4_heads {
 
 /* A paged key/value cache: element d of kv head h in slot s of page p at
  * k[p * k_page_stride + h * k_head_stride + s * k_slot_stride + d], v alike
- * (strides in elements).  Which pages a sequence holds is in its row of
- * q4_kv_batch's block table. */
+ * (strides in elements; both may be parts of one tensor).  Which pages a
+ * sequence holds is in its row of q4_kv_batch's block table. */
 typedef struct q4_kv_cache {
     void* k;
     void* v;

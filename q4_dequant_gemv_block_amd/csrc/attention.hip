@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, const 
     const Seq& seq = work.seq;
     const uint32_t item = (border - work.begin) / (uint32_t)seq.units;
     const uint32_t first = work.begin + item * seq.units, last = first + seq.units - 1;
-    if (first == border || first < range_begin(total, w0, grid)) return;
+    if (first == border || first < range_begin(total, w0, grid) || last >= total) return;
     uint32_t w1 = (uint32_t)((uint64_t)last * grid / total);  // the range that holds `last`
     while (range_begin(total, w1 + 1, grid) <= last) ++w1;
     while (range_begin(total, w1, grid) > last) --w1;
@@ -523,7 +523,7 @@ hipError_t launch_dim(const AttnArgs& a, const AttnShape& shape, hipStream_t s) 
         e = launch<T, D, 1>(a, shape, s);
     else
         e = launch<T, D, 2>(a, shape, s);
-    if (e != hipSuccess || !shape.bytes) return e;
+    if (e != hipSuccess || !shape.bytes || shape.grid < 2) return e;
     // Few items have many parts each: a workgroup a row; else one for eight rows.
     const int by = std::min(16, shape.few ? shape.most_rows : (shape.most_rows + 7) / 8);
     hipLaunchKernelGGL((k_attn_join<T, D>), dim3((unsigned)shape.grid - 1, by), dim3(kThreads), 0, s, a, make_cut(a, shape), (uint32_t)shape.grid);

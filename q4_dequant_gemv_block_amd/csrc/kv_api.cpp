@@ -151,14 +151,21 @@ bool overlaps_batch(Span x, const q4_kv_batch* b) {
            overlap(x, span(b->query_start, 4 * (uint64_t)(b->seqs + 1))) || overlap(x, span(b->context_len, 4 * (uint64_t)b->seqs));
 }
 
-q4::HeadsArg heads_arg(const q4_heads& x) { return q4::HeadsArg{static_cast<char*>(x.data), x.token_stride, x.head_stride}; }
+// (strides of a single token or head are never used: as 0 they do not decide about alignment)
+q4::HeadsArg heads_arg(const q4_heads& x, int64_t tokens, int heads) {
+    return q4::HeadsArg{static_cast<char*>(x.data), tokens > 1 ? x.token_stride : 0, heads > 1 ? x.head_stride : 0};
+}
 
 q4::CacheArg cache_arg(const q4_kv_cache& c) {
     q4::CacheArg r;
     r.k = static_cast<char*>(c.k);
     r.v = static_cast<char*>(c.v);
-    r.k_page = c.k_page_stride; r.k_head = c.k_head_stride; r.k_slot = c.k_slot_stride;
-    r.v_page = c.v_page_stride; r.v_head = c.v_head_stride; r.v_slot = c.v_slot_stride;
+    r.k_page = c.pages > 1 ? c.k_page_stride : 0;
+    r.v_page = c.pages > 1 ? c.v_page_stride : 0;
+    r.k_head = c.kv_heads > 1 ? c.k_head_stride : 0;
+    r.v_head = c.kv_heads > 1 ? c.v_head_stride : 0;
+    r.k_slot = c.k_slot_stride;
+    r.v_slot = c.v_slot_stride;
     r.pages = (uint32_t)c.pages;
     r.page_size = q4::FastDiv((uint32_t)c.page_size);
     r.kv_heads = c.kv_heads;
@@ -184,7 +191,8 @@ q4_status check_attention(const char* fn, const q4_kv_cache* cache, const q4_kv_
     if (q_heads % cache->kv_heads) return fail(Q4_ERR_INVALID_ARG, "%s: q_heads = %d must be a multiple of kv_heads = %d", fn, q_heads, cache->kv_heads);
     if (tokens * q_heads > (int64_t(1) << 30)) return fail(Q4_ERR_INVALID_ARG, "%s: more than 2^30 query rows", fn);
     if (!aligned(cache->k, 16) || !aligned(cache->v, 16)) return fail(Q4_ERR_MISALIGNED, "%s: the cache must be 16-byte aligned", fn);
-    if ((cache->k_page_stride | cache->k_head_stride | cache->k_slot_stride | cache->v_page_stride | cache->v_head_stride | cache->v_slot_stride) % 8)
+    const q4::CacheArg c = cache_arg(*cache);
+    if ((c.k_page | c.k_head | c.k_slot | c.v_page | c.v_head | c.v_slot) % 8)
         return fail(Q4_ERR_MISALIGNED, "%s: the cache's strides must be multiples of 8", fn);
     if (cache->k_slot_stride > (1 << 26) || cache->v_slot_stride > (1 << 26))
         return fail(Q4_ERR_INVALID_ARG, "%s: the slots of the cache must not be more than 2^26 elements apart", fn);
@@ -216,8 +224,8 @@ q4_status q4_rope(const q4_heads* x, const q4_heads* out, const int32_t* positio
     if (overlap(ro.all, span(positions, 4 * (uint64_t)tokens)) || overlap(ro.all, span(inv_freq, 4 * (uint64_t)rot_dim)))
         return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps positions or inv_freq", fn);
     q4::RopeArgs a = {};
-    a.in[0] = heads_arg(*x);
-    a.out = heads_arg(*out);
+    a.in[0] = heads_arg(*x, tokens, heads);
+    a.out = heads_arg(*out, tokens, heads);
     a.heads[0] = heads;
     a.positions = positions;
     a.inv_freq = inv_freq;
@@ -245,6 +253,7 @@ q4_status q4_kv_append(const q4_kv_cache* cache, const q4_kv_batch* batch, const
     if (st) return st;
     st = check_heads(fn, "v", v, tokens, cache->kv_heads, dim, false);
     if (st) return st;
+    if (cache->k == cache->v) return fail(Q4_ERR_INVALID_ARG, "%s: the cache's keys and values are the same memory", fn);
     if (k->type != v->type || (q && q->type != k->type)) return fail(Q4_ERR_INVALID_ARG, "%s: q, k and v must have one type", fn);
     if (!q != !q_out) return fail(Q4_ERR_INVALID_ARG, "%s: q and q_out go together", fn);
     if (!aligned(positions, 4)) return fail(Q4_ERR_MISALIGNED, "%s: positions must be 4-byte aligned", fn);
@@ -268,12 +277,12 @@ q4_status q4_kv_append(const q4_kv_cache* cache, const q4_kv_batch* batch, const
             return fail(Q4_ERR_INVALID_ARG, "%s: the cache overlaps an input", fn);
     q4::RopeArgs a = {};
     if (q) {
-        a.in[0] = heads_arg(*q);
-        a.out = heads_arg(*q_out);
+        a.in[0] = heads_arg(*q, tokens, q_heads);
+        a.out = heads_arg(*q_out, tokens, q_heads);
         a.heads[0] = q_heads;
     }
-    a.in[1] = heads_arg(*k);
-    a.in[2] = heads_arg(*v);
+    a.in[1] = heads_arg(*k, tokens, cache->kv_heads);
+    a.in[2] = heads_arg(*v, tokens, cache->kv_heads);
     a.heads[1] = a.heads[2] = cache->kv_heads;
     a.paged = 1;
     a.cache = cache_arg(*cache);
@@ -306,7 +315,8 @@ q4_status q4_attention_paged(const q4_kv_cache* cache, const q4_kv_batch* batch,
     st = check_heads(fn, "out", out, tokens, q_heads, dim, true);
     if (st) return st;
     if (q->type != cache->type || out->type != cache->type) return fail(Q4_ERR_INVALID_ARG, "%s: q and out must have the cache's type", fn);
-    if (!aligned(q->data, 16) || !aligned(out->data, 16) || (q->token_stride | q->head_stride | out->token_stride | out->head_stride) % 8)
+    const q4::HeadsArg qa = heads_arg(*q, tokens, q_heads), oa = heads_arg(*out, tokens, q_heads);
+    if (!aligned(qa.data, 16) || !aligned(oa.data, 16) || (qa.token_stride | qa.head_stride | oa.token_stride | oa.head_stride) % 8)
         return fail(Q4_ERR_MISALIGNED, "%s: q and out must be 16-byte aligned with strides that are multiples of 8", fn);
     if (!aligned(lse, 4)) return fail(Q4_ERR_MISALIGNED, "%s: lse must be 4-byte aligned", fn);
     if (!(scale > 0.0f) || !std::isfinite(scale) || !std::isfinite(scale * 1.4426950408889634f))
@@ -332,8 +342,8 @@ q4_status q4_attention_paged(const q4_kv_cache* cache, const q4_kv_batch* batch,
                 return fail(Q4_ERR_INVALID_ARG, "%s: outputs and workspace must not overlap", fn);
     }
     q4::AttnArgs a = {};
-    a.q = heads_arg(*q);
-    a.out = heads_arg(*out);
+    a.q = qa;
+    a.out = oa;
     a.lse = lse;
     a.cache = c;
     a.batch = b;

@@ -107,6 +107,56 @@ def test_hints_do_not_change_what_is_computed(hint):
     check(q4, batch, q, k, v, max_query_len=hint)
 
 
+@pytest.mark.parametrize("hint", [1, 100, 10 ** 6])
+def test_a_wrong_longest_context_does_not_change_what_is_computed(hint):
+    q4 = lib()
+    for lens in ([(1, 3000), (1, 5)], [(40, 3000), (3, 70)]):
+        batch = kv_ref.Batch(lens, 16, seed=2)
+        q, k, v = make(batch, 4, 2, 64, torch.bfloat16)
+        want, _, bound, _ = kv_ref.attention(q, k, v, batch, 0.125, 0)
+        dev = q4.KVBatch(*batch.device(q4)._keep, max_context_len=hint)
+        out = q4.q4_attention_paged(q4.KVCache(on_gpu(k), on_gpu(v)), dev, q.cuda(), scale=0.125)
+        assert bool(((out.double().cpu() - want).abs() <= bound).all())
+
+
+def test_keys_and_values_of_one_tensor_and_queries_in_place():
+    """Keys and values side by side in one tensor, queries turned in their place in packed rows."""
+    q4 = lib()
+    page, hq, hk, dim, n = 16, 4, 2, 64, 21
+    g = torch.Generator().manual_seed(3)
+    both = torch.zeros(5, 2, hk, page, dim, dtype=torch.float16, device="cuda")
+    cache = q4.KVCache(both[:, 0], both[:, 1])
+    plain = q4.KVCache(torch.zeros(5, hk, page, dim, dtype=torch.float16, device="cuda"),
+                       torch.zeros(5, hk, page, dim, dtype=torch.float16, device="cuda"))
+    packed = torch.randn(n, (hq + 2 * hk) * dim, generator=g).half().cuda()
+    q, k, v = packed.view(n, -1, dim).split([hq, hk, hk], 1)
+    kv = packed[:, hq * dim:].clone()
+    batch = q4.KVBatch(torch.tensor([[3, 1]], dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                       torch.tensor([n], dtype=torch.int32, device="cuda"))
+    freq, _ = q4.rope_frequencies(dim)
+    want = q4.q4_attention_paged(plain, batch, q4.q4_kv_append(plain, batch, k, v, q=q, inv_freq=freq))
+    turned = q4.q4_kv_append(cache, batch, k, v, q=q, inv_freq=freq, q_out=q)
+    assert turned is q and torch.equal(packed[:, hq * dim:], kv)
+    assert torch.equal(q4.q4_attention_paged(cache, batch, q), want)
+    assert torch.equal(both[:, 0], plain.k) and torch.equal(both[:, 1], plain.v)
+
+
+def test_no_new_tokens_at_all():
+    """Sequences without new tokens: nothing is written, whatever rows the tensors have."""
+    q4 = lib()
+    batch = kv_ref.Batch([(0, 40), (0, 0), (0, 3000)], 16, pad_rows=3)
+    q, k, v = make(batch, 4, 2, 128, torch.float16)
+    out = torch.full(q.shape, 5.0, dtype=q.dtype, device="cuda")
+    kc, vc = on_gpu(k), on_gpu(v)
+    cache, dev = q4.KVCache(kc, vc), batch.device(q4)
+    before = kc.view(torch.int16).clone()
+    q4.q4_attention_paged(cache, dev, q.cuda(), out=out)
+    new = torch.ones(3, 2, 128, dtype=torch.float16, device="cuda")
+    q4.q4_kv_append(cache, dev, new, new, q=q.cuda(), q_out=out)
+    torch.cuda.synchronize()
+    assert bool((out == 5.0).all()) and torch.equal(kc.view(torch.int16), before)
+
+
 def test_pages_without_a_place_are_not_seen():
     """Pages given back (-1) or outside the cache, in the middle and at the ends; a sequence that holds none."""
     q4 = lib()

@@ -98,7 +98,7 @@ CACHE_REFUSALS = [
     (dict(q_out=heads(3 * GIB + 2)), -1, "q_out overlaps"), (dict(q_out=heads(GIB)), -1, "q_out overlaps"),
     (dict(q_out=heads(16 * GIB)), -1, "q_out overlaps"), (dict(q_out=heads(64 * GIB)), -1, "q_out overlaps"),
     (dict(k=heads(16 * GIB, 2)), -1, "overlaps an input"), (dict(v=heads(32 * GIB, 2)), -1, "overlaps an input"),
-    (dict(q=heads(32 * GIB)), -1, "q overlaps the cache"), (dict(pos=16 * GIB + BASE), -1, "overlaps an input"),
+    (dict(q=heads(32 * GIB)), -1, "q overlaps the cache"), (dict(cache=cache(v=BASE + 16 * GIB)), -1, "same memory"), (dict(pos=16 * GIB + BASE), -1, "overlaps an input"),
     (dict(rot=130), -1, "rot_dim"), (dict(freq=None), -1, "inv_freq"), (dict(layout=9), -1, "layout"),
     (dict(pos=POS + 1), -2, "positions"),
 ])
@@ -130,6 +130,16 @@ def test_attention_refusals(lib, over, want, text):
     st = lib.q4_attention_paged(ref(a["cache"]), ref(a["batch"]), ref(a["q"]), ref(a["out"]), a["lse"], a["q_heads"],
                                 a["tokens"], a["scale"], a["window"], BASE + 80 * GIB, GIB, None)
     refused(lib, st, want, text)
+
+
+def test_strides_of_single_tokens_do_not_count(lib):
+    """torch gives a dimension of one entry any stride: it is no misalignment (the call fails on the workspace only)."""
+    c, b = cache(), batch(table_pages=2000, table_stride=2000, max_context=32000)
+    odd = heads(GIB, token_stride=1025)
+    st = lib.q4_attention_paged(ref(c), ref(b), ref(odd), ref(heads(2 * GIB)), None, 8, 1, 0.1, 0, None, 0, None)
+    refused(lib, st, -3, "workspace")
+    st = lib.q4_attention_paged(ref(c), ref(b), ref(odd), ref(heads(2 * GIB)), None, 8, 2, 0.1, 0, None, 0, None)
+    refused(lib, st, -2, "multiples of 8")
 
 
 def test_attention_workspace(lib):
