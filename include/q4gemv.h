@@ -541,7 +541,7 @@ typedef struct q4_kv_cache {
 typedef struct q4_kv_batch {
     const int32_t* block_table;
     int64_t table_stride; /* int32 entries from one sequence's row to the next */
-    int table_pages;      /* entries of a row, >= 1 */
+    int table_pages;      /* entries of a row, >= 1, together at most 2^30 tokens */
     int seqs;             /* >= 1 */
     const int32_t* query_start;
     const int32_t* context_len;
@@ -584,7 +584,8 @@ Q4_API q4_status q4_rope(const q4_heads* x, const q4_heads* out, const int32_t* 
  *               the angles instead
  *   inv_freq  : NULL with rot_dim == 0 (no rotation), else as in q4_rope
  * Each element is rounded once to the cache's type.  Slots that no new token
- * has are left as they are; a slot that two tokens share holds one of them.
+ * has are left as they are; where two new tokens have one slot, each element
+ * of it is that of one of them, not of the same one for all.
  */
 Q4_API q4_status q4_kv_append(const q4_kv_cache* cache, const q4_kv_batch* batch, const q4_heads* k,
                               const q4_heads* v, const q4_heads* q, const q4_heads* q_out, int q_heads,
@@ -610,10 +611,11 @@ Q4_API size_t q4_attention_paged_workspace_bytes(const q4_kv_cache* cache, const
  *            the sum of exp(scale * q . k_j)
  *   scale  : finite, > 0;  window >= 0 (0: no window)
  *   workspace : q4_attention_paged_workspace_bytes(...) bytes of device memory
- *            (may be NULL when that is 0), 16-byte aligned; its contents on entry do not matter.  Calls that
- *            may overlap in time need one each.
+ *            (may be NULL when that is 0), 16-byte aligned; its contents on
+ *            entry do not matter.  Calls that may overlap in time need one each.
  *   head_dim 64, 96, 128 or 256; q_heads a multiple of kv_heads; the cache
- *   16-byte aligned with strides that are multiples of 8.
+ *   16-byte aligned with strides that are multiples of 8, its slots at most
+ *   2^26 elements apart; tokens * q_heads at most 2^30
  * A row that sees no key is 0 (lse -infinity).  Slots beyond a context, pages
  * without a place and keys a row does not see leave it unaffected whatever they
  * hold.  Scores, softmax statistics and sums are binary32; the probabilities

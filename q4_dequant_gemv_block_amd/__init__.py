@@ -639,15 +639,15 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     return torch.tensor(freq, dtype=torch.float64, device=device), mscale
 
 
-def _heads(t: torch.Tensor, name: str, device) -> Heads:
-    """Tokens x heads x head_dim with the elements of a head side by side; other strides are free."""
+def _heads(t: torch.Tensor, name: str, gpu: int) -> Heads:
+    """Tokens x heads x head_dim on that GPU, the elements of a head side by side; other strides are free."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     kind = _TYPES.get(t.dtype)
     if kind is None:
         raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, t.dtype))
-    if t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
+    if t.get_device() != gpu:
+        raise ValueError("%s must be on GPU %d, is on %s" % (name, gpu, t.device))
     if t.dim() != 3:
         raise ValueError("%s must be [tokens, heads, head_dim]" % name)
     st, sh, sd = t.stride()
@@ -656,13 +656,13 @@ def _heads(t: torch.Tensor, name: str, device) -> Heads:
     return Heads(t.data_ptr(), st, sh, kind)
 
 
-def _vector(t: torch.Tensor, dtype, name: str, n: int | None, device) -> int:
+def _vector(t: torch.Tensor, dtype, name: str, n: int | None, gpu: int) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
+    if t.get_device() != gpu:
+        raise ValueError("%s must be on GPU %d, is on %s" % (name, gpu, t.device))
     if t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_contiguous():
         raise ValueError("%s must be contiguous, %s" % (name, "[%d]" % n if n is not None else "of one dimension"))
     return t.data_ptr()
@@ -674,31 +674,20 @@ def _layout(layout: str) -> int:
     return _LAYOUTS[layout]
 
 
-def _on(device, stream):
-    """The context in which a call allocates and launches: the tensors' device and the given stream (so that what is
+def _on(gpu: int, stream):
+    """The context in which a call allocates and launches: the tensors' GPU and the given stream (so that what is
     allocated here belongs to the stream that uses it), or None where they are the current ones already."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
+        if stream.device.index != gpu:
+            raise ValueError("stream is on %s, the tensors are on GPU %d" % (stream.device, gpu))
         return torch.cuda.stream(stream)
-    if device.type == "cuda" and torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
+    if torch._C._cuda_getDevice() != gpu:
+        return torch.cuda.device(gpu)
     return None
 
 
-def _current_stream(device) -> int:
-    """The handle of the device's current stream (torch.cuda.current_stream makes an object of it, for 3 us a call)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _cuda(t, name: str):
-    """The GPU a tensor is on."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    device = t.device
-    if device.type != "cuda":
-        raise ValueError("%s must be on a GPU" % name)
-    return device
+# The handle of a GPU's current stream (torch.cuda.current_stream makes an object of it, for 3 us a call).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (a torch built without GPUs has none)
 
 
 def q4_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layout: str = "half",
@@ -708,7 +697,11 @@ def q4_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
     (int32 [T], float64 [r / 2]; rope_frequencies makes them), the others as they are.  Pairs are elements i and
     i + r/2 ("half") or 2i and 2i + 1 ("interleaved"), results times mscale.  out: like x in shape, of any of the
     types, and may be x itself.  Turning by -positions undoes it and is its gradient."""
-    dev = _cuda(x, "x")
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be on a GPU")
     on = _on(dev, stream)
     if on is not None:
         with on:
@@ -716,7 +709,7 @@ def q4_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
     hx = _heads(x, "x", dev)
     t, h, d = x.shape
     if out is None:
-        out = torch.empty((t, h, d), dtype=x.dtype, device=dev)
+        out = x.new_empty((t, h, d))
     elif out.shape != x.shape:
         raise ValueError("out must have x's shape")
     ho = _heads(out, "out", dev)
@@ -749,7 +742,7 @@ class KVCache:
         if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v must have one shape, type and device")
         self.k, self.v = k, v
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.dtype, self.gpu = k.device, k.dtype, k.get_device()
         self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.desc = CacheDesc(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
                               v.stride(0), v.stride(1), v.stride(2), self.pages, self.page_size, self.kv_heads,
@@ -772,17 +765,17 @@ class KVBatch:
         if block_table.dim() != 2 or (block_table.stride(1) != 1 and block_table.shape[1] != 1):
             raise ValueError("block_table must be [sequences, pages] with consecutive entries")
         b = block_table.shape[0]
-        self.device = block_table.device
+        self.device, self.gpu = block_table.device, block_table.get_device()
         self._keep = (block_table, query_start, context_lens)
         self.desc = BatchDesc(block_table.data_ptr(), block_table.stride(0), block_table.shape[1], b,
-                              _vector(query_start, torch.int32, "query_start", b + 1, self.device),
-                              _vector(context_lens, torch.int32, "context_lens", b, self.device),
+                              _vector(query_start, torch.int32, "query_start", b + 1, self.gpu),
+                              _vector(context_lens, torch.int32, "context_lens", b, self.gpu),
                               int(max_query_len or 0), int(max_context_len or 0))
         self._ref = ctypes.byref(self.desc)
 
 
 def _same_device(cache: KVCache, batch: KVBatch):
-    if batch.device != cache.device:
+    if batch.gpu != cache.gpu:
         raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
 
 
@@ -792,12 +785,12 @@ def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
     """Write the new tokens' keys and values (k, v [T, kv_heads, D], any of the three types) into the cache, the keys
     turned on the way as by q4_rope (inv_freq None: not turned) by their positions in the sequence, or by
     `positions` (int32 [T]).  With q [T, q_heads, D] also returns q turned, in the cache's type, in q_out if given."""
-    on = _on(cache.device, stream)
+    on = _on(cache.gpu, stream)
     if on is not None:
         with on:
             return q4_kv_append(cache, batch, k, v, q, inv_freq, layout, mscale, positions, q_out)
     _same_device(cache, batch)
-    dev = cache.device
+    dev = cache.gpu
     hk, hv = _heads(k, "k", dev), _heads(v, "v", dev)
     t = k.shape[0]
     if k.shape != v.shape or k.shape[1] != cache.kv_heads or k.shape[2] != cache.head_dim:
@@ -810,7 +803,7 @@ def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
         if q.shape[0] != t or q.shape[2] != cache.head_dim:
             raise ValueError("q must be [T=%d, heads, %d]" % (t, cache.head_dim))
         if q_out is None:
-            q_out = torch.empty((t, heads, cache.head_dim), dtype=cache.dtype, device=dev)
+            q_out = torch.empty((t, heads, cache.head_dim), dtype=cache.dtype, device=cache.device)
         elif q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
         ho = _heads(q_out, "q_out", dev)
@@ -847,32 +840,32 @@ def q4_attention_paged(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: f
     h / (q_heads / kv_heads).  scale: 1 / sqrt(D) if None.  Append the new tokens first (q4_kv_append).  out like q;
     lse (float32 [T, q_heads], optional) receives the log of the sum of exponentials; workspace (uint8) at least
     attention_workspace_bytes.  Rows that see nothing are 0."""
-    on = _on(cache.device, stream)
+    on = _on(cache.gpu, stream)
     if on is not None:
         with on:
             return q4_attention_paged(cache, batch, q, scale, window, out, lse, workspace)
     _same_device(cache, batch)
-    dev = cache.device
+    dev = cache.gpu
     hq = _heads(q, "q", dev)
     t, h, d = q.shape
     if d != cache.head_dim:
         raise ValueError("q must be [T, heads, %d]" % cache.head_dim)
     if out is None:
-        out = torch.empty((t, h, d), dtype=q.dtype, device=dev)
+        out = q.new_empty((t, h, d))
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
     ho = _heads(out, "out", dev)
     lp = None
     if lse is not None:
-        if tuple(lse.shape) != (t, h) or lse.device != dev:
-            raise ValueError("lse must be float32 [T, heads] on %s" % dev)
         lp = _ptr(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (t, h) or lse.get_device() != dev:
+            raise ValueError("lse must be float32 [T, heads] on %s" % cache.device)
     lib = _lib or load_library()
     wp, wb = None, 0
     if workspace is None:
         wb = lib.q4_attention_paged_workspace_bytes(cache._ref, batch._ref, h, t, window)
         if wb:
-            workspace = torch.empty(wb, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(wb, dtype=torch.uint8, device=cache.device)
             wp = workspace.data_ptr()
     else:
         wp, wb = _vector(workspace, torch.uint8, "workspace", None, dev), workspace.shape[0]
