@@ -38,6 +38,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 namespace q4 {
 
@@ -562,37 +563,57 @@ bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256
 
 // How a call is cut: the rows of an item, and whether items are taken whole or
 // in parts.  Parts cost a launch that waits for the first one (measured 5 to 7
-// us) and their way to memory and back; whole items cost what the longest of
-// them takes alone.  Both are estimated from the longest context and the most
-// new tokens of a sequence, as far as the caller knows them, and the cheapest
-// way is taken.  Measured (head_dim 128): a step of k_attn's waves (256 keys) takes
-// 1.7 us, a tile of k_attn_tile 1.1 us (64 rows) or 1.5 us (128) for a workgroup
-// alone on a CU and 1.3 or 1.9 us where two share it, the join of two waves 0.6 us.
+// us), their way to memory and back at about 4 TB/s, and in tiles the L2: whole
+// items of one kv head run side by side and read the same keys, ranges do not.
+// Whole items cost what the longest of them takes alone.  Both are estimated
+// from the longest context and the most new tokens of a sequence, as far as the
+// caller knows them, and the cheapest way is taken.
+//
+// Measured: a step of k_attn's waves (256 keys of head_dim 128) takes 1.7 us.  The
+// numbers of the tiles are a fit to 560 calls (head_dim 64 to 256, 64 to 4096 new
+// tokens of 1 to 30 sequences, equal and ragged, up to 30000 keys, windows) run in
+// each of the four ways: what it takes was within 5 % of the best of them in 540
+// and 22 % behind at most.
 AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
     const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
     const int64_t longest = max_query > 0 ? std::min<int64_t>(max_query, tokens) : tokens;  // new tokens of a sequence
     const int64_t most = longest * group;
     const int64_t seqs = std::min<int64_t>(b.seqs, tokens);
+    const int64_t context = max_context > 0 ? std::min<int64_t>(max_context, capacity) : capacity;
     const int cus = compute_units();
-    int64_t keys = max_context > 0 ? std::min<int64_t>(max_context, capacity) : capacity;
-    if (window) keys = std::min<int64_t>(keys, window + longest);
-    // A sequence's rows see its context less half of the new tokens on average.
-    const double seen = window ? 1.0 : 1.0 - 0.5 * longest / std::max<double>(keys, longest);
+    const double dim = c.head_dim / 128.0;
     AttnShape best = {};
     double best_us = 0;
-    auto consider = [&](int rows, int step, int slots, double alone, double shared) {  // us of a whole item
+    auto consider = [&](int rows) {
         AttnShape s = {};
         s.rows = rows;
-        s.step = step;
+        s.step = rows <= 32 ? kStep : 64;
         s.unit = 64;
         s.most_rows = (int)std::min<int64_t>(rows, most);
+        const int slots = rows <= 32 || c.head_dim > 128 ? cus : 2 * cus;
+        // keys of an item, the part of them that its sequence's items see on average, and all items
+        const int64_t keys = window ? std::min<int64_t>(context, (int64_t)window + (rows - 1) / group + 2) : context;
+        const int64_t past = std::max<int64_t>(context - longest, 0);
+        const double inside = (double)std::min(std::max<int64_t>(keys - past, 0), longest);  // tokens that see less
+        const double seen = std::min(1.0, (inside * past + inside * (inside + 1) / 2 + (longest - inside) * keys) / ((double)longest * keys));
         const double items = (double)c.kv_heads * (longest * seqs == tokens ? seqs * ((most + rows - 1) / rows) : (tokens * group + rows * seqs / 2) / rows);
-        const double us = items > cus ? shared : alone;
-        const double whole = items > slots ? us * seen * items / slots + 0.5 * us : us;
-        // ranges of equal units, of which an item counts as many as its sequence's longest
+        const double rounds = items / slots;
         const double parts = std::min<double>(slots, items * keys / s.unit);
-        const double join = 7.5 + parts * s.most_rows * c.head_dim * 8 / 4e6;  // written and read at about 4 TB/s
-        const double cut = shared * items / slots + join;
+        const double traffic = parts * s.most_rows * c.head_dim * 8 / 4e6;
+        double whole, cut;
+        if (rows <= 32) {
+            const double us = 1.7 * keys / 256 * dim;  // a whole item
+            whole = rounds > 1 ? us * (seen * rounds + 0.5) : us;
+            cut = us * rounds + 7.5 + traffic;
+        } else {
+            const double tiles = (double)((keys + 63) / 64);
+            const double shared = 0.55 + tiles * (c.head_dim > 128 ? (rows == 64 ? 2.25 : 2.8) : rows == 64 ? 0.4 + 0.75 * dim : 0.5 + dim);
+            const double alone = c.head_dim > 128 ? shared : shared * (rows == 64 ? 0.75 : 0.8);  // on its CU
+            const double work = seen * rounds;
+            // the last round's items end later than the work would, by 0.65 of what their round lacks
+            whole = items <= cus ? alone : rounds <= 1 ? shared : shared * std::max(1.0, work + 0.65 * std::min(1.0, std::ceil(rounds) - work));
+            cut = 1.15 * shared * rounds * (0.85 + 0.15 * seen) + 15 + traffic;
+        }
         const int64_t bound = item_bound(c, b, q_heads, tokens, rows);
         if (whole <= cut && bound < (int64_t(1) << 31)) {
             s.unit = 1 << 30;
@@ -609,15 +630,11 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
             best_us = std::min(whole, cut);
         }
     };
-    const double dim = c.head_dim / 128.0;
     if (most <= 32) {
-        const double us = 1.7 * keys / 256 * dim;
-        consider(most <= 16 ? 16 : 32, kStep, cus, us, us);
+        consider(most <= 16 ? 16 : 32);
     } else {
-        const double tiles = (keys + 63) / 64 * dim;
-        const int slots = c.head_dim <= 128 ? 2 * cus : cus;
-        consider(64, 64, slots, 1.1 * tiles + 0.6, 1.3 * tiles + 0.6);
-        consider(128, 64, slots, 1.5 * tiles, 1.9 * tiles);
+        consider(64);
+        consider(128);
     }
     return best;
 }
