@@ -569,11 +569,12 @@ bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256
 // from the longest context and the most new tokens of a sequence, as far as the
 // caller knows them, and the cheapest way is taken.
 //
-// Measured: a step of k_attn's waves (256 keys of head_dim 128) takes 1.7 us.  The
-// numbers of the tiles are a fit to 560 calls (head_dim 64 to 256, 64 to 4096 new
-// tokens of 1 to 30 sequences, equal and ragged, up to 30000 keys, windows) run in
-// each of the four ways: what it takes was within 5 % of the best of them in 540
-// and 22 % behind at most.
+// The numbers are fits to calls run in each way, head_dim 64 to 256, equal and
+// ragged, with and without windows.  Tiles: 560 calls of 64 to 4096 new tokens of 1
+// to 30 sequences, up to 30000 keys; what is taken was within 5 % of the best of the
+// four ways in 540 and 22 % behind at most.  k_attn: 264 calls of 1 to 4 new tokens
+// of 1 to 200 sequences, up to 20000 keys; 260 within 5 % of the better way, 27 %
+// behind at most.
 AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
     const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
     const int64_t longest = max_query > 0 ? std::min<int64_t>(max_query, tokens) : tokens;  // new tokens of a sequence
@@ -597,21 +598,20 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
         const double inside = (double)std::min(std::max<int64_t>(keys - past, 0), longest);  // tokens that see less
         const double seen = std::min(1.0, (inside * past + inside * (inside + 1) / 2 + (longest - inside) * keys) / ((double)longest * keys));
         const double items = (double)c.kv_heads * (longest * seqs == tokens ? seqs * ((most + rows - 1) / rows) : (tokens * group + rows * seqs / 2) / rows);
-        const double rounds = items / slots;
+        const double rounds = items / slots, work = seen * rounds;
+        const double late = std::min(1.0, std::ceil(rounds) - work);  // what the last round lacks
         const double parts = std::min<double>(slots, items * keys / s.unit);
         const double traffic = parts * s.most_rows * c.head_dim * 8 / 4e6;
         double whole, cut;
         if (rows <= 32) {
-            const double us = 1.7 * keys / 256 * dim;  // a whole item
-            whole = rounds > 1 ? us * (seen * rounds + 0.5) : us;
-            cut = us * rounds + 7.5 + traffic;
+            const double us = keys / 256.0 * (0.25 + 1.85 * dim);  // an item's steps
+            whole = (1.3 + us) * (rounds > 1 ? work + 1.2 * late : 1.0);
+            cut = us * rounds * (c.head_dim == 64 ? 1.4 : 1.0) + 6 + traffic;  // two whole items of 64 share a CU
         } else {
             const double tiles = (double)((keys + 63) / 64);
             const double shared = 0.55 + tiles * (c.head_dim > 128 ? (rows == 64 ? 2.25 : 2.8) : rows == 64 ? 0.4 + 0.75 * dim : 0.5 + dim);
             const double alone = c.head_dim > 128 ? shared : shared * (rows == 64 ? 0.75 : 0.8);  // on its CU
-            const double work = seen * rounds;
-            // the last round's items end later than the work would, by 0.65 of what their round lacks
-            whole = items <= cus ? alone : rounds <= 1 ? shared : shared * std::max(1.0, work + 0.65 * std::min(1.0, std::ceil(rounds) - work));
+            whole = items <= cus ? alone : rounds <= 1 ? shared : shared * std::max(1.0, work + 0.65 * late);
             cut = 1.15 * shared * rounds * (0.85 + 0.15 * seen) + 15 + traffic;
         }
         const int64_t bound = item_bound(c, b, q_heads, tokens, rows);
