@@ -574,7 +574,8 @@ bool attn_head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256
 // to 30 sequences, up to 30000 keys; what is taken was within 5 % of the best of the
 // four ways in 540 and 22 % behind at most.  k_attn: 264 calls of 1 to 4 new tokens
 // of 1 to 200 sequences, up to 20000 keys; 260 within 5 % of the better way, 27 %
-// behind at most.
+// behind at most; of 96 batches of 16 to 200 sequences, half of them with lengths from
+// 1/16 of the longest up, which the host cannot see, 79 and 47 %.
 AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
     const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
     const int64_t longest = max_query > 0 ? std::min<int64_t>(max_query, tokens) : tokens;  // new tokens of a sequence
