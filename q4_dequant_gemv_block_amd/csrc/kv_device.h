@@ -53,20 +53,31 @@ __device__ __forceinline__ void store_elems(char* p, const float (&x)[V]) {
     }
 }
 
+// The last j in [0, n) for which low(j) holds, where it holds for the first ones and
+// not for the others; -1 if for none.  Called by whole waves with n uniform: 64
+// places a step, counted with a ballot, so 64^k sequences take k loads one after
+// the other (a walk through all of them would make a batch's time grow with its
+// square, as every token and every item looks for its own).
+template <typename F>
+__device__ __forceinline__ int last_low(int n, F low) {
+    const int lane = (int)(threadIdx.x & 63);
+    int base = 0;
+    for (;;) {
+        const int step = (n + 63) >> 6;
+        const int at = lane * step;
+        const int count = __popcll(__ballot(at < n && low(base + at)));
+        if (step <= 1 || !count) return base + count - 1;
+        base += (count - 1) * step;
+        n = min(step, n - (count - 1) * step);
+    }
+}
+
 // The sequence whose new tokens hold row t: the last b with query_start[b] <= t
 // (sequences without new tokens share their start with the next one), -1 for a
-// row before the first or behind the last.  Called by whole waves with t
-// uniform: 64 starts a load, counted with a ballot.
+// row before the first or behind the last.  Called by whole waves with t uniform.
 __device__ __forceinline__ int sequence_of(const BatchArg& b, int64_t t) {
     if (t >= b.query_start[b.seqs]) return -1;
-    int count = 0;
-    for (int i = 0; i < b.seqs; i += 64) {
-        const int j = i + (int)(threadIdx.x & 63);
-        const uint64_t below = __ballot(j < b.seqs && b.query_start[j] <= t);
-        count += __popcll(below);
-        if (below != ~uint64_t(0)) break;
-    }
-    return count - 1;
+    return last_low(b.seqs, [&](int j) { return b.query_start[j] <= t; });
 }
 
 // Page that holds position p of the sequence with block-table row `row`, or -1
