@@ -83,7 +83,7 @@ struct Layout : LdsRow<D> {
     static __device__ __forceinline__ int swz_v(int r) { return R::chunks == 8 ? ((r >> 1) & 3) << 1 : (r & 7) << 1; }
 };
 
-template <typename T, int D, int NR>
+template <typename T, int D, int NR, typename WORK>
 __global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const AttnArgs a, const Cut cut) {
     typedef Layout<D, NR> L;
     constexpr int ROWS = 16 * NR, kWaves = L::waves;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const AttnArgs a, c
     extern __shared__ char sh[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, n16 = lane & 15;
-    Work work;
+    WORK work;
     if (!work.start(cut, a.batch)) return;
     const Seq& seq = work.seq;
     const Parts<D> parts(a.workspace, (int)gridDim.x, ROWS);
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const AttnArgs a, c
             for (int d = 0; d < DT; ++d) *reinterpret_cast<f4*>(&sh_o[at * L::lines + 16 * d + 4 * q]) = acc[r][d];
         }
         __syncthreads();
-        const bool whole = it.u0 == 0 && it.u1 == seq.units;
+        const bool whole = work.whole(it);
         const int64_t slot = (int64_t)2 * blockIdx.x + (it.u0 == 0);
         for (int u = threadIdx.x; u < rows * (D / 4); u += 64 * kWaves) {
             const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
@@ -492,9 +492,13 @@ int compute_units() {
     return n;
 }
 
-// Most items a call can have: a sequence's rows round up once.
-int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int rows) {
-    return (int64_t)c.kv_heads * (tokens * (q_heads / c.kv_heads) / rows + std::min<int64_t>(b.seqs, tokens));
+// Most items a call can have: the rows of a sequence with new tokens round up once,
+// or those of each token; and whether it is the second bound.
+int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int rows, int* per_token) {
+    const int group = q_heads / c.kv_heads, each = (group + rows - 1) / rows;
+    const int64_t by_rows = tokens * group / rows + std::min<int64_t>(b.seqs, tokens);
+    *per_token = tokens * each <= by_rows ? each : 0;
+    return c.kv_heads * (*per_token ? tokens * each : by_rows);
 }
 
 Cut make_cut(const AttnArgs& a, const AttnShape& s) {
@@ -503,6 +507,8 @@ Cut make_cut(const AttnArgs& a, const AttnShape& s) {
     c.unit_log2 = __builtin_ctz(s.unit);
     c.step = s.step;
     c.window = a.window;
+    c.places = (uint32_t)s.places;
+    c.per_token = s.per_token;
     c.group = FastDiv((uint32_t)a.group);
     c.kv_heads = FastDiv((uint32_t)a.cache.kv_heads);
     c.capacity = (int)((int64_t)a.batch.table_pages * a.cache.page_size.d);
@@ -510,14 +516,19 @@ Cut make_cut(const AttnArgs& a, const AttnShape& s) {
     return c;
 }
 
-template <typename T, int D, int NR>
-hipError_t launch(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
+template <typename T, int D, int NR, typename WORK>
+hipError_t launch_work(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
     constexpr size_t lds = Layout<D, NR>::total;
     static LdsLimit limit;
-    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn<T, D, NR>), lds);
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn<T, D, NR, WORK>), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn<T, D, NR>), dim3(shape.grid), dim3(64 * Layout<D, NR>::waves), lds, s, a, make_cut(a, shape));
+    hipLaunchKernelGGL((k_attn<T, D, NR, WORK>), dim3(shape.grid), dim3(64 * Layout<D, NR>::waves), lds, s, a, make_cut(a, shape));
     return hipGetLastError();
+}
+
+template <typename T, int D, int NR>
+hipError_t launch(const AttnArgs& a, const AttnShape& shape, hipStream_t s) {
+    return shape.places ? launch_work<T, D, NR, Places>(a, shape, s) : launch_work<T, D, NR, Work>(a, shape, s);
 }
 
 template <typename T, int D>
@@ -615,10 +626,10 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
             whole = items <= cus ? alone : rounds <= 1 ? shared : shared * std::max(1.0, work + 0.65 * late);
             cut = 1.15 * shared * rounds * (0.85 + 0.15 * seen) + 15 + traffic;
         }
-        const int64_t bound = item_bound(c, b, q_heads, tokens, rows);
+        const int64_t bound = item_bound(c, b, q_heads, tokens, rows, &s.per_token);
         if (whole <= cut && bound < (int64_t(1) << 31)) {
             s.unit = 1 << 30;
-            s.grid = (int)bound;
+            s.grid = s.places = (int)bound;
         } else {
             // larger units where this many would pass 31 bits
             while (s.unit < (1 << 30) && bound * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;

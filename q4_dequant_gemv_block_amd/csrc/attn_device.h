@@ -68,6 +68,8 @@ __device__ __forceinline__ void wave_lds_fence() {
 struct Cut {
     int rows_log2, unit_log2, step;  // an item's keys begin at a multiple of step
     int window, capacity;            // capacity: tokens a row of the block table holds
+    uint32_t places;                 // for items that are taken whole (Places)
+    int per_token;                   // places of a token and kv head; 0: by rows
     FastDiv group, kv_heads;
     int64_t tokens;
 };
@@ -114,9 +116,86 @@ __device__ __forceinline__ void place_item(const Cut& c, const Seq& seq, uint32_
     x->rows = min(1 << c.rows_log2, seq.n * (int)c.group.d - x->row0);
 }
 
-// The call's work as whole waves see it: each lane holds the lengths of one of
+// Positions of an item's rows and the keys of its units [u0, u1).
+__device__ __forceinline__ void place_keys(const Cut& c, const Seq& seq, Item* x) {
+    x->past = seq.ctx - seq.n;
+    x->p_first = x->past + (int)c.group.div(x->row0);
+    x->p_last = x->past + (int)c.group.div(x->row0 + x->rows - 1);
+    const int keys = max(0, min(min(seq.ctx, c.capacity), x->p_last + 1));
+    const int start = c.window ? (max(0, x->p_first - c.window + 1) & -c.step) : 0;
+    x->k_lo = (int)min((int64_t)keys, start + ((int64_t)x->u0 << c.unit_log2));
+    x->k_hi = (int)min((int64_t)keys, start + ((int64_t)x->u1 << c.unit_log2));
+}
+
+// Items taken whole, a workgroup each, which must not walk through the sequences
+// (a batch's time would grow with its square).  Place x of a kv head belongs to the
+// last sequence b with f(b) <= x, found by 64 probes a step, where f is
+//   floor(query_start[b] group / rows) + min(query_start[b], b), or
+//   query_start[b] ceil(group / rows),
+// whichever ends lower (the second for decode steps).  Over a sequence with new
+// tokens f grows by at least its items (floor(A + B) - floor(A) >= floor(B), and 1
+// more for what that leaves out), so each item has a place; what is left are empty
+// places.  f of the end is what item_bound() counts.
+struct Places {
+    Seq seq;
+    uint32_t at;  // the place to look at next
+
+    __device__ __forceinline__ bool start(const Cut& c, const BatchArg& batch) {
+        at = blockIdx.x;
+        return true;
+    }
+    // Picks the sequence of a place; false if the place is empty.
+    __device__ __forceinline__ bool find(const Cut& c, const BatchArg& batch, uint32_t place, uint32_t* item) {
+        const int64_t x = c.kv_heads.div(place);
+        auto first_place = [&](int start, int b) {
+            const int64_t s = max(start, 0);
+            return c.per_token ? s * c.per_token : (s * c.group.d >> c.rows_log2) + min(s, (int64_t)b);
+        };
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));  // made anew: addresses from it would be held through the kernel's loop
+        int b0 = 0, n = batch.seqs;
+        while (n > 64) {
+            const int step = (n + 63) >> 6, i = lane * step;
+            const int count = max(1, __popcll(__ballot(i < n && first_place(batch.query_start[b0 + i], b0 + i) <= x)));
+            b0 += (count - 1) * step;
+            n = min(step, n - (count - 1) * step);
+        }
+        int first = 0, last = 0, ctx = 0;
+        if (lane < n) {
+            first = batch.query_start[b0 + lane];
+            last = batch.query_start[b0 + lane + 1];
+            ctx = batch.context_len[b0 + lane];
+        }
+        const int64_t f = first_place(first, b0 + lane);
+        const int l = max(1, __popcll(__ballot(lane < n && f <= x))) - 1;
+        seq.b = b0 + l;
+        seq.row0 = __builtin_amdgcn_readlane(first, l);
+        const int end = __builtin_amdgcn_readlane(last, l);
+        seq.n = seq.row0 < 0 || end > c.tokens || end < seq.row0 ? 0 : end - seq.row0;
+        seq.ctx = __builtin_amdgcn_readlane(ctx, l);
+        cut_sequence(c, &seq);
+        *item = place - c.kv_heads.d * (uint32_t)__builtin_amdgcn_readlane((int)f, l);
+        return *item < c.kv_heads.d * seq.tiles;
+    }
+    __device__ __forceinline__ bool next(const Cut& c, const BatchArg& batch, Item* x) {
+        uint32_t item;
+        do {
+            if (at >= c.places) return false;
+            at += gridDim.x;
+        } while (!find(c, batch, at - gridDim.x, &item));
+        x->u0 = 0;
+        x->u1 = seq.units;
+        place_item(c, seq, item, x);
+        place_keys(c, seq, x);
+        return true;
+    }
+    __device__ __forceinline__ bool whole(const Item&) const { return true; }
+};
+
+// Ranges of units, as whole waves see them: each lane holds the lengths of one of
 // 64 sequences (read once where there are no more), a wave's scan finds the
-// sequence of a unit.
+// sequence of a unit.  A workgroup walks through the sequences twice, but there
+// are never more workgroups than the machine holds.
 struct Work {
     uint32_t total;  // units of all sequences
     uint32_t begin;  // first unit of seq
@@ -201,15 +280,10 @@ struct Work {
         x->u1 = (int)min((uint32_t)seq.units, x->u0 + (hi - lo));
         lo += x->u1 - x->u0;
         place_item(c, seq, item, x);
-        x->past = seq.ctx - seq.n;
-        x->p_first = x->past + (int)c.group.div(x->row0);
-        x->p_last = x->past + (int)c.group.div(x->row0 + x->rows - 1);
-        const int keys = max(0, min(min(seq.ctx, c.capacity), x->p_last + 1));
-        const int start = c.window ? (max(0, x->p_first - c.window + 1) & -c.step) : 0;
-        x->k_lo = (int)min((int64_t)keys, start + ((int64_t)x->u0 << c.unit_log2));
-        x->k_hi = (int)min((int64_t)keys, start + ((int64_t)x->u1 << c.unit_log2));
+        place_keys(c, seq, x);
         return true;
     }
+    __device__ __forceinline__ bool whole(const Item& x) const { return x.u0 == 0 && x.u1 == seq.units; }
 };
 
 // Parts in the workspace: every workgroup has at most two, one that begins its

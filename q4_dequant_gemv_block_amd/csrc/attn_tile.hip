@@ -64,7 +64,7 @@ struct Layout : LdsRow<D> {
     static __device__ __forceinline__ int swz_v(int r) { return R::chunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; }
 };
 
-template <typename T, int D, int U>
+template <typename T, int D, int U, typename WORK>
 __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const AttnArgs a, const Cut cut) {
     typedef Layout<D> L;
     constexpr int NW = kWaves, ROWS = 64 * U;
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
     const int first = U == 2 ? 0 : 32 * (wave >> 1);  // its first key of a tile
     const uint32_t sh0 = lds_address(sh);
 
-    Work work;
+    WORK work;
     if (!work.start(cut, a.batch)) return;
     const Seq& seq = work.seq;
     const Parts<D> parts(a.workspace, (int)gridDim.x, ROWS);
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
         int n = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
         asm volatile("" : "+v"(n), "+v"(h));
         if (32 * rows32 + n >= it.rows) continue;
-        if (it.u0 == 0 && it.u1 == seq.units) {
+        if (work.whole(it)) {
             const float f = row_scale(l);
             char* dst = a.out.data + ((int64_t)(seq.row0 + qi) * a.out.token_stride + (int64_t)qh * a.out.head_stride + 4 * h) * 2;
 #pragma unroll
@@ -446,14 +446,19 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
     }
 }
 
-template <typename T, int D, int U>
-hipError_t launch(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
+template <typename T, int D, int U, typename WORK>
+hipError_t launch_work(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
     constexpr size_t lds = (size_t)4 * Layout<D>::bytes + kWaves * sizeof(int);
     static LdsLimit limit;
-    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, U>), lds);
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, U, WORK>), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<T, D, U>), dim3(shape.grid), dim3(kThreads), lds, s, a, cut);
+    hipLaunchKernelGGL((k_attn_tile<T, D, U, WORK>), dim3(shape.grid), dim3(kThreads), lds, s, a, cut);
     return hipGetLastError();
+}
+
+template <typename T, int D, int U>
+hipError_t launch(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
+    return shape.places ? launch_work<T, D, U, Places>(a, cut, shape, s) : launch_work<T, D, U, Work>(a, cut, shape, s);
 }
 
 }  // namespace

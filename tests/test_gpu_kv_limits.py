@@ -43,3 +43,45 @@ def test_append_finds_its_sequence_among_many(seqs):
     torch.cuda.synchronize()
     assert torch.equal(kc, want)
     assert torch.equal(vc, torch.where(want == -1.0, want, -want))
+
+
+def uniform(q4, new, ctx, hq, hk, dim, **hints):
+    """Attention with queries of 0, all sequences in one page of 65536 slots: a row's output is the mean of the values
+    it sees, every weight alike and so exact.  Checks it, and returns the workspace that the call needs.
+
+    An output is off by its rounding, half a step, and by the 32-bit sum of at most 400 values below 8 in each of
+    which a rounding of 2^-24 of a partial sum is made: 400 * 2^-24 * 8 < 2^-12."""
+    rng = np.random.default_rng(len(new))
+    k, v = (torch.from_numpy(rng.normal(0, 1, (1, hk, 65536, dim)).clip(-7, 7)).half().cuda() for _ in range(2))
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    seq = np.repeat(np.arange(len(new)), new)
+    sees = ctx[seq] - new[seq] + np.arange(start[-1]) - start[seq] + 1
+    assert sees.max() <= 400
+    batch = on(q4, start, ctx.astype(np.int32), np.zeros((len(new), 1), dtype=np.int32), **hints)
+    t = int(start[-1])
+    out = torch.full((t + 3, hq, dim), 5.0, dtype=torch.float16, device="cuda")
+    cache = q4.KVCache(k, v)
+    q4.q4_attention_paged(cache, batch, torch.zeros_like(out), out=out)
+    torch.cuda.synchronize()
+    n = torch.from_numpy(sees).cuda()
+    mean = v[0, :, :400].double().cumsum(1) / torch.arange(1, 401, device="cuda")[:, None]
+    mean = torch.cat((torch.zeros_like(mean[:, :1]), mean), 1)  # none: 0
+    want = mean[:, n.clamp(min=0)].transpose(0, 1).repeat_interleave(hq // hk, 1)
+    assert bool(((out[:t].double() - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -12).all())
+    assert bool((out[t:] == 5.0).all())
+    return q4.attention_workspace_bytes(cache, batch, hq, t + 3)
+
+
+@pytest.mark.parametrize("seqs,most,hint,whole", [
+    (65, 2, 1000, True), (4097, 2, 1000, True), (20000, 1, 1000, True), (130, 40, 1000, True), (4200, 17, 1000, True),
+    (65, 2, 65536, False), (4097, 2, 100, False), (130, 40, 65536, False)])
+def test_items_of_many_sequences(seqs, most, hint, whole):
+    """Items find their sequence among many, most of the sequences' rows not a multiple of an item's."""
+    q4 = lib()
+    say("attention, sequences", seqs, most)
+    rng = np.random.default_rng(seqs)
+    new = rng.integers(0, most + 1, seqs)
+    new[[0, seqs // 2]] = 0
+    ctx = np.maximum(new + rng.integers(-2, 300, seqs), 0)
+    # the hint decides whether items are taken whole
+    assert (uniform(q4, new, ctx, 6, 2, 64, max_query_len=most, max_context_len=hint) == 0) == whole
