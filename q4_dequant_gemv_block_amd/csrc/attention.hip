@@ -629,7 +629,8 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
         const int64_t bound = item_bound(c, b, q_heads, tokens, rows, &s.per_token);
         if (whole <= cut && bound < (int64_t(1) << 31)) {
             s.unit = 1 << 30;
-            s.grid = s.places = (int)bound;
+            s.places = (int)bound;
+            s.grid = std::min(s.places, 1 << 22);  // fewer than 2^32 threads; a workgroup goes on to other places
         } else {
             // larger units where this many would pass 31 bits
             while (s.unit < (1 << 30) && bound * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs a, const RopeU
     __shared__ f2 turn[kTokens][kMaxPairs];
     __shared__ int64_t place_k[kTokens], place_v[kTokens];
     __shared__ int state[kTokens];  // bit 0: the row is a token, bit 1: it has a place in the cache
-    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+    const int64_t t0 = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * kTokens;
     {
         const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
         const int64_t t = t0 + w;
@@ -181,7 +181,9 @@ hipError_t launch(const RopeArgs& a, hipStream_t s) {
     // Few tokens: a token's units over several workgroups, one unit a thread.
     const int64_t want = (1024 + bx - 1) / bx;
     const int by = (int)std::max<int64_t>(1, std::min<int64_t>(want, (total + kThreads - 1) / kThreads));
-    hipLaunchKernelGGL((k_rope<IN, OUT, HALF, V>), dim3((unsigned)bx, (unsigned)by), dim3(kThreads), 0, s, a, n);
+    // a launch has fewer than 2^32 threads along each axis
+    const unsigned gx = (unsigned)std::min<int64_t>(bx, 1 << 22), gz = (unsigned)((bx + gx - 1) / gx);
+    hipLaunchKernelGGL((k_rope<IN, OUT, HALF, V>), dim3(gx, (unsigned)by, gz), dim3(kThreads), 0, s, a, n);
     return hipGetLastError();
 }
 

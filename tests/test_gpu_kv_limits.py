@@ -45,14 +45,14 @@ def test_append_finds_its_sequence_among_many(seqs):
     assert torch.equal(vc, torch.where(want == -1.0, want, -want))
 
 
-def uniform(q4, new, ctx, hq, hk, dim, **hints):
-    """Attention with queries of 0, all sequences in one page of 65536 slots: a row's output is the mean of the values
+def uniform(q4, new, ctx, hq, hk, dim, slots=65536, **hints):
+    """Attention with queries of 0, all sequences in one page: a row's output is the mean of the values
     it sees, every weight alike and so exact.  Checks it, and returns the workspace that the call needs.
 
     An output is off by its rounding, half a step, and by the 32-bit sum of at most 400 values below 8 in each of
     which a rounding of 2^-24 of a partial sum is made: 400 * 2^-24 * 8 < 2^-12."""
     rng = np.random.default_rng(len(new))
-    k, v = (torch.from_numpy(rng.normal(0, 1, (1, hk, 65536, dim)).clip(-7, 7)).half().cuda() for _ in range(2))
+    k, v = (torch.from_numpy(rng.normal(0, 1, (1, hk, slots, dim)).clip(-7, 7)).half().cuda() for _ in range(2))
     start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     seq = np.repeat(np.arange(len(new)), new)
     sees = ctx[seq] - new[seq] + np.arange(start[-1]) - start[seq] + 1
@@ -85,3 +85,27 @@ def test_items_of_many_sequences(seqs, most, hint, whole):
     ctx = np.maximum(new + rng.integers(-2, 300, seqs), 0)
     # the hint decides whether items are taken whole
     assert (uniform(q4, new, ctx, 6, 2, 64, max_query_len=most, max_context_len=hint) == 0) == whole
+
+
+def test_more_items_than_a_launch_has_workgroups():
+    """2^23 workgroups of 512 threads are one too many for a launch; with one item each this call has 200 more."""
+    q4 = lib()
+    seqs, hk = 131073, 64
+    new = np.ones(seqs, dtype=np.int64)
+    ctx = np.random.default_rng(5).integers(0, 60, seqs)
+    assert uniform(q4, new, ctx, hk, hk, 64, slots=1024, max_query_len=1, max_context_len=1024) == 0
+
+
+def test_more_tokens_than_a_launch_has_workgroups():
+    """2^24 workgroups of 256 threads, of 4 tokens each, are one too many for a launch."""
+    q4 = lib()
+    t, period = (1 << 26) + 5, 1 << 20
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(period, 1, 2, generator=g).half().cuda()
+    pos = torch.randint(0, 1 << 20, (period,), generator=g, dtype=torch.int32).cuda()
+    freq = torch.tensor([0.25], dtype=torch.float64, device="cuda")
+    want = q4.q4_rope(x, pos, freq)
+    got = q4.q4_rope(x.repeat(65, 1, 1)[:t], pos.repeat(65)[:t], freq)
+    torch.cuda.synchronize()
+    assert torch.equal(got[: 64 * period].view(64, period, 2), want.view(1, period, 2).expand(64, -1, -1))
+    assert torch.equal(got[64 * period :], want[:5])
