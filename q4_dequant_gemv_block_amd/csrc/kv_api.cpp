@@ -33,13 +33,23 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int type_bytes(int type) { return type == Q4_TYPE_F32 ? 4 : type == Q4_TYPE_F16 || type == Q4_TYPE_BF16 ? 2 : 0; }
 
-// Limits that keep every element offset inside int64 and every row, position
-// and unit index inside 32 bits.
+// Limits that keep every row, position and unit index inside 32 bits, and every
+// byte offset inside int64: strides alone do not, their products with the counts
+// are bounded by kMaxReach.
 constexpr int64_t kMaxTokens = int64_t(1) << 27;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxReach = int64_t(1) << 60;  // elements, of at most 4 bytes
 constexpr int kMaxHeads = 4096;
 constexpr int kMaxHeadDim = 1024;
 constexpr int kMaxPage = 65536;
+
+// Elements from the first to behind the last of `count` blocks of `block` elements
+// that are `stride` apart (kMaxReach where there are more).
+int64_t reach(int64_t block, int64_t count, int64_t stride) {
+    int64_t r;
+    if (__builtin_mul_overflow(count - 1, stride, &r) || __builtin_add_overflow(block, r, &r)) return kMaxReach;
+    return std::min(r, kMaxReach);
+}
 
 struct Span {
     uintptr_t lo, hi;  // [lo, hi) bytes
@@ -84,6 +94,8 @@ q4_status check_heads(const char* fn, const char* name, const q4_heads* x, int64
     if (!aligned(x->data, b)) return fail(Q4_ERR_MISALIGNED, "%s: %s must be aligned to its elements", fn, name);
     if (x->token_stride < 0 || x->token_stride > kMaxStride || x->head_stride < 0 || x->head_stride > kMaxStride)
         return fail(Q4_ERR_INVALID_ARG, "%s: a stride of %s is negative or too large", fn, name);
+    if (reach(reach(dim, heads, x->head_stride), tokens, x->token_stride) >= kMaxReach)
+        return fail(Q4_ERR_INVALID_ARG, "%s: the strides of %s reach too far", fn, name);
     if (output) {
         const int64_t ts = x->token_stride, hs = x->head_stride;
         const bool by_token = (heads == 1 || hs >= dim) && (tokens == 1 || ts >= (heads - 1) * hs + dim);
@@ -123,6 +135,9 @@ q4_status check_cache(const char* fn, const q4_kv_cache* c) {
         const int64_t count = i % 3 == 0 ? c->pages : i % 3 == 1 ? c->kv_heads : c->page_size;
         if (count > 1 && s[i] < c->head_dim) return fail(Q4_ERR_INVALID_ARG, "%s: the heads of the cache overlap each other", fn);
     }
+    for (int i = 0; i < 6; i += 3)
+        if (reach(reach(reach(c->head_dim, c->page_size, s[i + 2]), c->kv_heads, s[i + 1]), c->pages, s[i]) >= kMaxReach)
+            return fail(Q4_ERR_INVALID_ARG, "%s: the strides of the cache reach too far", fn);
     return Q4_OK;
 }
 
@@ -141,6 +156,8 @@ q4_status check_batch(const char* fn, const q4_kv_batch* b, const q4_kv_cache* c
         return fail(Q4_ERR_INVALID_ARG, "%s: a block table of %d pages: it must hold 1 page and at most 2^30 tokens", fn, b->table_pages);
     if (b->table_stride < 0 || b->table_stride > kMaxStride || (b->seqs > 1 && b->table_stride < b->table_pages))
         return fail(Q4_ERR_INVALID_ARG, "%s: the block table's stride is smaller than a row", fn);
+    if (reach(b->table_pages, b->seqs, b->table_stride) >= kMaxReach)
+        return fail(Q4_ERR_INVALID_ARG, "%s: the block table's stride reaches too far", fn);
     if (b->max_query < 0 || b->max_context < 0) return fail(Q4_ERR_INVALID_ARG, "%s: max_query and max_context must not be negative", fn);
     return Q4_OK;
 }

@@ -1,0 +1,44 @@
+"""Refusals that follow from where the tensors of the cache operators lie: strides whose products pass 64 bits, caches
+that overlap themselves or each other.  Every call here fails on the host, with made-up addresses."""
+import pytest
+
+import q4_dequant_gemv_block_amd as q4
+from test_kv_cpu import BASE, FREQ, GIB, POS, batch, cache, heads, lib, ref, refused  # noqa: F401 (lib: a fixture)
+
+FAR = 1 << 40  # the largest stride
+
+
+@pytest.mark.parametrize("which", ["x", "out"])
+def test_rope_strides_that_pass_64_bits(lib, which):
+    """2^24 tokens 2^40 elements apart: the span's end is in front of its beginning, and would overlap nothing."""
+    a = dict(x=heads(0), out=heads(GIB))
+    a[which] = heads(0, token_stride=FAR)
+    st = lib.q4_rope(ref(a["x"]), ref(a["out"]), POS, FREQ, 1 << 24, 8, 128, 128, 0, 1.0, None)
+    refused(lib, st, -1, "strides of %s reach too far" % which)
+
+
+def test_append_strides_that_pass_64_bits(lib):
+    def call(**over):
+        a = dict(cache=cache(), batch=batch(), k=heads(GIB, 2), v=heads(2 * GIB, 2), q=heads(3 * GIB), q_out=heads(4 * GIB))
+        a.update(over)
+        return lib.q4_kv_append(ref(a["cache"]), ref(a["batch"]), ref(a["k"]), ref(a["v"]), ref(a["q"]), ref(a["q_out"]), 8,
+                                1 << 24, None, FREQ, 128, 0, 1.0, None)
+    for name in ("k", "v", "q", "q_out"):
+        refused(lib, call(**{name: heads(3 * GIB, token_stride=FAR)}), -1, "strides of %s reach too far" % name)
+    for over in (dict(k_page_stride=FAR), dict(v_page_stride=FAR)):
+        refused(lib, call(cache=cache(pages=1 << 30, **over)), -1, "strides of the cache reach too far")
+    refused(lib, call(batch=batch(seqs=1 << 24, table_stride=FAR)), -1, "stride reaches too far")
+
+
+def test_attention_strides_that_pass_64_bits(lib):
+    def call(**over):
+        a = dict(cache=cache(), batch=batch(), q=heads(GIB), out=heads(2 * GIB))
+        a.update(over)
+        return lib.q4_attention_paged(ref(a["cache"]), ref(a["batch"]), ref(a["q"]), ref(a["out"]), None, 8, 1 << 24, 0.1, 0,
+                                      BASE + 80 * GIB, 8 * GIB, None)
+    for name in ("q", "out"):
+        refused(lib, call(**{name: heads(3 * GIB, token_stride=FAR)}), -1, "strides of %s reach too far" % name)
+    refused(lib, call(cache=cache(pages=1 << 30, v_page_stride=FAR)), -1, "strides of the cache reach too far")
+    refused(lib, call(batch=batch(seqs=1 << 24, table_stride=FAR)), -1, "stride reaches too far")
+    assert lib.q4_attention_paged_workspace_bytes(ref(cache(pages=1 << 30, k_page_stride=FAR)), ref(batch()), 8, 5, 0) == 0
+    assert "too far" in q4.last_error()
