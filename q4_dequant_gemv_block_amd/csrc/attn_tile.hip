@@ -138,8 +138,9 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                     const int r8 = x * L::per_load + lane / L::chunks;  // row of the group
                     const int r = 8 * group + r8;
                     const int c = (lane % L::chunks) ^ (values ? L::swz_v(r) : L::swz_k(r));
-                    if (D == 8 * L::chunks || c < D / 8)
-                        load_to_lds(src, r8 * (uint32_t)slot_stride * 2 + 16 * c, to + (8 * group + x * L::per_load) * L::row);
+                    // (heads of 96: the lanes behind a row's end load its last chunks again, for no use: masks for them would cost scalar registers)
+                    const int at = D == 8 * L::chunks || c < D / 8 ? c : c - (L::chunks - D / 8);
+                    load_to_lds(src, r8 * (uint32_t)slot_stride * 2 + 16 * at, to + (8 * group + x * L::per_load) * L::row);
                 }
             }
         };
