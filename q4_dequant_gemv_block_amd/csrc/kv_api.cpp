@@ -141,6 +141,31 @@ q4_status check_cache(const char* fn, const q4_kv_cache* c) {
     return Q4_OK;
 }
 
+// The axes of keys or values that have more than one entry, the largest stride first.
+struct Axis {
+    int64_t stride, count;
+};
+int cache_axes(const q4_kv_cache* c, bool values, Axis (&axis)[3]) {
+    const Axis all[3] = {{values ? c->v_page_stride : c->k_page_stride, c->pages},
+                         {values ? c->v_head_stride : c->k_head_stride, c->kv_heads},
+                         {values ? c->v_slot_stride : c->k_slot_stride, c->page_size}};
+    int n = 0;
+    for (const Axis& a : all)
+        if (a.count > 1) axis[n++] = a;
+    std::sort(axis, axis + n, [](const Axis& a, const Axis& b) { return a.stride > b.stride; });
+    return n;
+}
+
+// Each stride steps over all that the smaller ones reach: no two elements of a
+// cache that is written are the same memory.
+bool axes_nest(const Axis* axis, int n, int64_t dim) {
+    for (int i = n - 1; i >= 0; --i) {
+        if (axis[i].stride < dim) return false;
+        dim = reach(dim, axis[i].count, axis[i].stride);
+    }
+    return true;
+}
+
 Span cache_span(const q4_kv_cache* c, bool values) {
     const int64_t p = values ? c->v_page_stride : c->k_page_stride, h = values ? c->v_head_stride : c->k_head_stride,
                   s = values ? c->v_slot_stride : c->k_slot_stride;
@@ -270,6 +295,9 @@ q4_status q4_kv_append(const q4_kv_cache* cache, const q4_kv_batch* batch, const
     if (st) return st;
     st = check_heads(fn, "v", v, tokens, cache->kv_heads, dim, false);
     if (st) return st;
+    Axis ak[3], av[3];
+    if (!axes_nest(ak, cache_axes(cache, false, ak), dim) || !axes_nest(av, cache_axes(cache, true, av), dim))
+        return fail(Q4_ERR_INVALID_ARG, "%s: the heads of the cache overlap each other", fn);
     if (cache->k == cache->v) return fail(Q4_ERR_INVALID_ARG, "%s: the cache's keys and values are the same memory", fn);
     if (k->type != v->type || (q && q->type != k->type)) return fail(Q4_ERR_INVALID_ARG, "%s: q, k and v must have one type", fn);
     if (!q != !q_out) return fail(Q4_ERR_INVALID_ARG, "%s: q and q_out go together", fn);

@@ -42,3 +42,33 @@ def test_attention_strides_that_pass_64_bits(lib):
     refused(lib, call(batch=batch(seqs=1 << 24, table_stride=FAR)), -1, "stride reaches too far")
     assert lib.q4_attention_paged_workspace_bytes(ref(cache(pages=1 << 30, k_page_stride=FAR)), ref(batch()), 8, 5, 0) == 0
     assert "too far" in q4.last_error()
+
+
+def append(lib, c, **over):
+    """An append to that cache that is refused behind the checks of the cache (q without q_out) if those pass."""
+    dim = c.head_dim
+    k, v = heads(GIB, c.kv_heads, dim), heads(2 * GIB, c.kv_heads, dim)
+    return lib.q4_kv_append(ref(c), ref(batch()), ref(k), ref(v), ref(heads(3 * GIB, 8, dim)), None, 8, 5, None, FREQ, 64,
+                            0, 1.0, None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(k_head_stride=128),                                         # heads in each other's slots
+    dict(v_head_stride=128),
+    dict(k_page_stride=16 * 128),                                    # a page where the next head is
+    dict(v_page_stride=2 * 16 * 128 - 1),                            # one element too near
+    dict(k_page_stride=128, k_head_stride=10 * 128, k_slot_stride=19 * 128),  # pages innermost: 2 heads reach 20
+])
+def test_append_to_a_cache_that_overlaps_itself(lib, over):
+    refused(lib, append(lib, cache(**over)), -1, "heads of the cache overlap each other")
+
+
+@pytest.mark.parametrize("over", [
+    dict(k_page_stride=16 * 2 * 128, k_slot_stride=2 * 128, k_head_stride=128),  # slots outside heads
+    dict(v_page_stride=128, v_head_stride=10 * 128, v_slot_stride=20 * 128),     # pages innermost
+    dict(k_page_stride=1 << 20, k_head_stride=1 << 13, k_slot_stride=136),       # gaps
+    dict(kv_heads=1, k_head_stride=0, v_head_stride=5),                          # a stride that is never used
+    dict(pages=1, k_page_stride=0),
+])
+def test_append_to_any_layout(lib, over):
+    refused(lib, append(lib, cache(**over)), -1, "go together")
