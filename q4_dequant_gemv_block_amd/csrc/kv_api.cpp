@@ -166,6 +166,22 @@ bool axes_nest(const Axis* axis, int n, int64_t dim) {
     return true;
 }
 
+// Whether an element of the values, `delta` elements behind the keys, may be one of
+// the keys (nested axes, largest first).  With equal strides the outermost can
+// bring a block of the one near a block of the other in two ways only, rounding
+// delta / stride down and up; where the layouts differ the spans decide.
+bool blocks_meet(const Axis* k, int nk, const Axis* v, int nv, int64_t dim, int64_t delta) {
+    int64_t rk = dim, rv = dim;
+    for (int i = 0; i < nk; ++i) rk = reach(rk, k[i].count, k[i].stride);
+    for (int i = 0; i < nv; ++i) rv = reach(rv, v[i].count, v[i].stride);
+    if (delta >= rk || -delta >= rv) return false;
+    if (!nk || !nv || k->stride != v->stride || k->count != v->count) return true;
+    const int64_t down = delta / k->stride - (delta % k->stride < 0);
+    for (int64_t i = down; i <= down + 1; ++i)
+        if (i > -k->count && i < k->count && blocks_meet(k + 1, nk - 1, v + 1, nv - 1, dim, delta - i * k->stride)) return true;
+    return false;
+}
+
 Span cache_span(const q4_kv_cache* c, bool values) {
     const int64_t p = values ? c->v_page_stride : c->k_page_stride, h = values ? c->v_head_stride : c->k_head_stride,
                   s = values ? c->v_slot_stride : c->k_slot_stride;
@@ -296,9 +312,11 @@ q4_status q4_kv_append(const q4_kv_cache* cache, const q4_kv_batch* batch, const
     st = check_heads(fn, "v", v, tokens, cache->kv_heads, dim, false);
     if (st) return st;
     Axis ak[3], av[3];
-    if (!axes_nest(ak, cache_axes(cache, false, ak), dim) || !axes_nest(av, cache_axes(cache, true, av), dim))
+    const int nk = cache_axes(cache, false, ak), nv = cache_axes(cache, true, av);
+    if (!axes_nest(ak, nk, dim) || !axes_nest(av, nv, dim))
         return fail(Q4_ERR_INVALID_ARG, "%s: the heads of the cache overlap each other", fn);
-    if (cache->k == cache->v) return fail(Q4_ERR_INVALID_ARG, "%s: the cache's keys and values are the same memory", fn);
+    if (blocks_meet(ak, nk, av, nv, dim, (int64_t)((intptr_t)cache->v - (intptr_t)cache->k) / 2))
+        return fail(Q4_ERR_INVALID_ARG, "%s: the cache's keys and values are the same memory, or parts of them", fn);
     if (k->type != v->type || (q && q->type != k->type)) return fail(Q4_ERR_INVALID_ARG, "%s: q, k and v must have one type", fn);
     if (!q != !q_out) return fail(Q4_ERR_INVALID_ARG, "%s: q and q_out go together", fn);
     if (!aligned(positions, 4)) return fail(Q4_ERR_MISALIGNED, "%s: positions must be 4-byte aligned", fn);

@@ -72,3 +72,38 @@ def test_append_to_a_cache_that_overlaps_itself(lib, over):
 ])
 def test_append_to_any_layout(lib, over):
     refused(lib, append(lib, cache(**over)), -1, "go together")
+
+
+K = BASE + 16 * GIB
+PAGE = 2 * 16 * 128  # elements of a page of the keys: 2 heads of 16 slots
+
+
+@pytest.mark.parametrize("over", [
+    dict(v=K), dict(v=K + 2 * 128), dict(v=K + 2), dict(v=K + 2 * (10 * PAGE - 1)),  # behind the keys' beginning
+    dict(v=K - 2 * 128), dict(v=K - 2 * (10 * PAGE - 1)),                             # in front of it
+    # page by page, but one element, or one slot, too few between
+    dict(v=K + 2 * (PAGE - 1), k_page_stride=2 * PAGE, v_page_stride=2 * PAGE),
+    dict(v=K + 2 * PAGE, k_page_stride=2 * PAGE - 128, v_page_stride=2 * PAGE - 128),
+    # head by head (each head's values behind its keys), the values one slot early
+    dict(v=K + 2 * 15 * 128, k_head_stride=2 * 16 * 128, v_head_stride=2 * 16 * 128, k_page_stride=2 * PAGE, v_page_stride=2 * PAGE),
+    # slot by slot, half a head apart
+    dict(v=K + 2 * 64, k_slot_stride=256, v_slot_stride=256, k_head_stride=4096, v_head_stride=4096, k_page_stride=8192, v_page_stride=8192),
+])
+def test_append_to_keys_and_values_that_overlap(lib, over):
+    refused(lib, append(lib, cache(**dict(dict(k=K), **over))), -1, "same memory")
+
+
+@pytest.mark.parametrize("over", [
+    dict(v=K + 2 * 10 * PAGE), dict(v=K - 2 * 10 * PAGE),                                 # one behind the other
+    dict(v=K + 2 * PAGE, k_page_stride=2 * PAGE, v_page_stride=2 * PAGE),                  # page by page
+    dict(v=K - 2 * PAGE, k_page_stride=2 * PAGE, v_page_stride=2 * PAGE),
+    dict(v=K + 2 * 16 * 128, k_head_stride=2 * 16 * 128, v_head_stride=2 * 16 * 128, k_page_stride=2 * PAGE, v_page_stride=2 * PAGE),
+    dict(v=K + 2 * 128, k_slot_stride=256, v_slot_stride=256, k_head_stride=4096, v_head_stride=4096, k_page_stride=8192, v_page_stride=8192),
+    # a page's values in another order than its keys
+    dict(v=K + 2 * PAGE, k_page_stride=2 * PAGE, v_page_stride=2 * PAGE, v_slot_stride=256, v_head_stride=128),
+    # the layers of a model page by page, this one's keys and values 3 and 8 places in
+    dict(k=K + 2 * 3 * PAGE, v=K + 2 * 8 * PAGE, k_page_stride=20 * PAGE, v_page_stride=20 * PAGE),
+    dict(k=K + 2 * 8 * PAGE, v=K + 2 * 3 * PAGE, k_page_stride=20 * PAGE, v_page_stride=20 * PAGE),
+])
+def test_append_to_keys_and_values_beside_each_other(lib, over):
+    refused(lib, append(lib, cache(**dict(dict(k=K), **over))), -1, "go together")
