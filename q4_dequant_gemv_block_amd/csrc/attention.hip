@@ -24,9 +24,9 @@
 // the operand's layout (half lines of 16 rows a load), took 2.4 us for a step of 8
 // waves on a CU, this 1.6.
 // The loads are non-temporal: each 128-byte line is used once.
-// The running maximum is raised only when a score exceeds it by 2^8 (the
-// probabilities stay below 2^8, far inside both types), so most steps neither
-// reduce over lanes nor rescale.  Row sums are of the rounded probabilities, so
+// The reference m of a row's weights is raised only when a score exceeds the one it
+// was made from by 2^8 (kLift in attn_device.h), so most steps neither reduce over
+// lanes nor rescale.  Row sums are of the rounded probabilities, so
 // a rounding does not shift a row's weight.
 //
 // Bound by HBM.  Measured, 32 query heads over 8 of 128: 61 ragged sequences up to
@@ -244,10 +244,10 @@ __global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const AttnArgs a, c
 #pragma unroll
                 for (int j = 1; j < 8; ++j) top = fmaxf(top, s[r][j]);
                 top *= a.scale_log2;
-                if (__ballot(top > m[r] + kRaise)) {
+                if (__ballot(top > m[r] + kRaise<T>)) {
                     top = fmaxf(top, __shfl_xor(top, 16));
                     top = fmaxf(top, __shfl_xor(top, 32));
-                    const float raised = top > m[r] + kRaise ? top : m[r];  // each row by itself
+                    const float raised = top > m[r] + kRaise<T> ? top - kLift<T> : m[r];  // each row by itself
                     const float f = raised == kNone ? 1.0f : __builtin_amdgcn_exp2f(m[r] - raised);
                     m[r] = raised;
                     l[r] *= f;

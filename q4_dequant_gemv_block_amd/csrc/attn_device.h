@@ -20,9 +20,16 @@ struct Cut;
 template <typename T, int D>
 hipError_t launch_attn_tile(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s);
 
-// log2 by which a score may exceed the running maximum before that is raised:
-// probabilities stay below 2^8, far inside both types.
-constexpr float kRaise = 8.0f;
+// A row's weights are 2^(score - m).  m is set to kLift below the largest score, and
+// set anew when a score exceeds it by kRaise (each 2^8 of scores at the soonest).
+// In binary16 the largest weight is then between 2^7 and 2^15, so that weights keep
+// their 11 bits down to 2^-21 of it and come to 0 at 2^-32 (from 2^0 they would at
+// 2^-25, a part of the sum that counts where there are 10^5 of them).  bfloat16 has
+// the exponents: 2^0 to 2^8.
+template <typename T>
+constexpr float kLift = std::is_same<T, F16>::value ? 7.0f : 0.0f;
+template <typename T>
+constexpr float kRaise = kLift<T> + 8.0f;
 constexpr float kNone = -__builtin_inff();
 
 // Two floats rounded to T in one dword (first in the low half), and back.

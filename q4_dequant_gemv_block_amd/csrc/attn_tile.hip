@@ -19,7 +19,7 @@
 // LDS rows are as long as a head; the 16-byte chunk c of row r lies at c ^ f(r),
 // so that the 16 rows of a K read and the 4 rows x 64 bytes of a V read cover all 64
 // banks (f by row for K, by row % 4 in 64-byte blocks for V; measured without
-// conflicts).  The running maximum is raised as in k_attn.  A wave works on two
+// conflicts).  The weights' reference is raised as in k_attn.  A wave works on two
 // tiles at once: the products of the next tile's scores are issued between the
 // exponentials of this one's, so that neither unit waits for the other.
 //
@@ -275,9 +275,9 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                     }
             }
             top *= a.scale_log2;
-            if (__ballot(top > m + kRaise)) {
+            if (__ballot(top > m + kRaise<T>)) {
                 top = fmaxf(top, __shfl_xor(top, 32));
-                const float raised = top > m + kRaise ? top : m;  // each row by itself
+                const float raised = top > m + kRaise<T> ? top - kLift<T> : m;  // each row by itself
                 const float f = raised == kNone ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
                 m = raised;
                 l *= f;
