@@ -696,7 +696,7 @@ def q4_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
     with the leading 2 * len(inv_freq) elements of each head turned by the angles positions[t] * inv_freq[i]
     (int32 [T], float64 [r / 2]; rope_frequencies makes them), the others as they are.  Pairs are elements i and
     i + r/2 ("half") or 2i and 2i + 1 ("interleaved"), results times mscale.  out: like x in shape, of any of the
-    types, and may be x itself.  Turning by -positions undoes it and is its gradient."""
+    types, and may be x itself.  Turning by -positions undoes it and is its gradient.  No tokens: nothing to do."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     dev = x.get_device()
@@ -713,10 +713,11 @@ def q4_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
     elif out.shape != x.shape:
         raise ValueError("out must have x's shape")
     ho = _heads(out, "out", dev)
-    freq = _vector(inv_freq, torch.float64, "inv_freq", None, dev)
+    freq, pos, kind = _vector(inv_freq, torch.float64, "inv_freq", None, dev), _vector(positions, torch.int32, "positions", t, dev), _layout(layout)
+    if t == 0:
+        return out
     status = (_lib or load_library()).q4_rope(
-        ctypes.byref(hx), ctypes.byref(ho), _vector(positions, torch.int32, "positions", t, dev), freq, t, h, d,
-        2 * inv_freq.shape[0], _layout(layout), mscale, _current_stream(dev))
+        ctypes.byref(hx), ctypes.byref(ho), pos, freq, t, h, d, 2 * inv_freq.shape[0], kind, mscale, _current_stream(dev))
     if status:
         _check(status)
     return out
@@ -784,7 +785,8 @@ def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
                  positions: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None):
     """Write the new tokens' keys and values (k, v [T, kv_heads, D], any of the three types) into the cache, the keys
     turned on the way as by q4_rope (inv_freq None: not turned) by their positions in the sequence, or by
-    `positions` (int32 [T]).  With q [T, q_heads, D] also returns q turned, in the cache's type, in q_out if given."""
+    `positions` (int32 [T]).  With q [T, q_heads, D] also returns q turned, in the cache's type, in q_out if given.
+    No tokens (a step in which no sequence has new ones): nothing to do."""
     on = _on(cache.gpu, stream)
     if on is not None:
         with on:
@@ -814,10 +816,13 @@ def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
     if inv_freq is not None:
         freq = _vector(inv_freq, torch.float64, "inv_freq", None, dev)
         r = inv_freq.shape[0]
+    pos = None if positions is None else _vector(positions, torch.int32, "positions", t, dev)
+    kind = _layout(layout)
+    if t == 0:
+        return q_out
     status = (_lib or load_library()).q4_kv_append(
-        cache._ref, batch._ref, ctypes.byref(hk), ctypes.byref(hv), rq, ro, heads, t,
-        None if positions is None else _vector(positions, torch.int32, "positions", t, dev),
-        freq if r else None, 2 * r, _layout(layout), mscale, _current_stream(dev))
+        cache._ref, batch._ref, ctypes.byref(hk), ctypes.byref(hv), rq, ro, heads, t, pos, freq if r else None, 2 * r,
+        kind, mscale, _current_stream(dev))
     if status:
         _check(status)
     return q_out
@@ -825,6 +830,8 @@ def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
 
 def attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, tokens: int, window: int = 0) -> int:
     """Bytes of the workspace q4_attention_paged needs for these sizes (0: none)."""
+    if tokens == 0:
+        return 0
     with torch.cuda.device(cache.device):  # the work is cut for this device
         n = int(load_library().q4_attention_paged_workspace_bytes(cache._ref, batch._ref, q_heads, tokens, window))
     if n == 0 and last_error():
@@ -839,7 +846,7 @@ def q4_attention_paged(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: f
     their sequences up to their own positions, the last `window` of them if window > 0; query head h reads kv head
     h / (q_heads / kv_heads).  scale: 1 / sqrt(D) if None.  Append the new tokens first (q4_kv_append).  out like q;
     lse (float32 [T, q_heads], optional) receives the log of the sum of exponentials; workspace (uint8) at least
-    attention_workspace_bytes.  Rows that see nothing are 0."""
+    attention_workspace_bytes.  Rows that see nothing are 0.  No tokens: nothing to do."""
     on = _on(cache.gpu, stream)
     if on is not None:
         with on:
@@ -860,6 +867,8 @@ def q4_attention_paged(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: f
         lp = _ptr(lse, torch.float32, "lse")
         if tuple(lse.shape) != (t, h) or lse.get_device() != dev:
             raise ValueError("lse must be float32 [T, heads] on %s" % cache.device)
+    if t == 0:
+        return out
     lib = _lib or load_library()
     wp, wb = None, 0
     if workspace is None:

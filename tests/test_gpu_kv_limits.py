@@ -109,3 +109,30 @@ def test_more_tokens_than_a_launch_has_workgroups():
     torch.cuda.synchronize()
     assert torch.equal(got[: 64 * period].view(64, period, 2), want.view(1, period, 2).expand(64, -1, -1))
     assert torch.equal(got[64 * period :], want[:5])
+
+
+@pytest.mark.parametrize("seqs", [0, 3])
+def test_a_step_without_tokens(seqs):
+    """Token tensors without rows, of a batch with or without sequences: outputs without rows, the cache as it was."""
+    q4 = lib()
+    kc, vc = (torch.full((2, 2, 8, 64), 3.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    cache = q4.KVCache(kc, vc)
+    batch = on(q4, np.zeros(seqs + 1, dtype=np.int32), np.full(seqs, 5, dtype=np.int32), np.zeros((seqs, 1), dtype=np.int32))
+    freq, _ = q4.rope_frequencies(64)
+    kv = torch.empty((0, 2, 64), device="cuda")
+    q = torch.empty((0, 4, 64), device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert q4.q4_rope(q, none, freq).shape == (0, 4, 64)
+    assert q4.q4_kv_append(cache, batch, kv, kv, inv_freq=freq) is None
+    turned = q4.q4_kv_append(cache, batch, kv, kv, q=q, inv_freq=freq, positions=none)
+    assert turned.shape == (0, 4, 64) and turned.dtype == torch.float16
+    out = torch.empty_like(turned)
+    assert q4.attention_workspace_bytes(cache, batch, 4, 0) == 0
+    assert q4.q4_attention_paged(cache, batch, turned).shape == (0, 4, 64)
+    assert q4.q4_attention_paged(cache, batch, turned, out=out, lse=torch.empty((0, 4), device="cuda")) is out
+    torch.cuda.synchronize()
+    assert bool((kc == 3.0).all()) and bool((vc == 3.0).all())
+    with pytest.raises(ValueError):
+        q4.q4_rope(q, none, freq, layout="other")  # what is wrong stays wrong
+    with pytest.raises(ValueError):
+        q4.q4_kv_append(cache, batch, kv, kv, positions=torch.empty(1, dtype=torch.int32, device="cuda"))
