@@ -771,7 +771,7 @@ class KVBatch:
         self.desc = BatchDesc(block_table.data_ptr(), block_table.stride(0), block_table.shape[1], b,
                               _vector(query_start, torch.int32, "query_start", b + 1, self.gpu),
                               _vector(context_lens, torch.int32, "context_lens", b, self.gpu),
-                              int(max_query_len or 0), int(max_context_len or 0))
+                              *(min(int(n or 0), 2 ** 31 - 1) for n in (max_query_len, max_context_len)))
         self._ref = ctypes.byref(self.desc)
 
 

@@ -136,3 +136,20 @@ def test_a_step_without_tokens(seqs):
         q4.q4_rope(q, none, freq, layout="other")  # what is wrong stays wrong
     with pytest.raises(ValueError):
         q4.q4_kv_append(cache, batch, kv, kv, positions=torch.empty(1, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("hint", [2 ** 31, 2 ** 32 + 5, 2 ** 40])
+def test_hints_past_32_bits(hint):
+    """A longest context or query beyond what 32 bits hold is a hint as any other (its low bits would be negative, or
+    a few tokens)."""
+    q4 = lib()
+    start, ctx = np.array([0, 2, 3], dtype=np.int32), np.array([5, 7], dtype=np.int32)
+    table = np.array([[0], [1]], dtype=np.int32)
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(2, 1, 8, 64, generator=g).half().cuda() for _ in range(2))
+    q = torch.randn(3, 2, 64, generator=g).half().cuda()
+    cache = q4.KVCache(k, v)
+    want = q4.q4_attention_paged(cache, on(q4, start, ctx, table), q)
+    batch = on(q4, start, ctx, table, max_query_len=hint, max_context_len=hint)
+    assert batch.desc.max_query == batch.desc.max_context == 2 ** 31 - 1
+    assert torch.equal(q4.q4_attention_paged(cache, batch, q), want)
