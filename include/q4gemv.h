@@ -502,8 +502,9 @@ Q4_API q4_status q4_0_gemm_prefill_batch(const q4_prefill_plan* plan, void* stre
 #define Q4_ROPE_INTERLEAVED 1 /* 2i and 2i + 1 */
 
 /* Heads of a list of tokens: element d of head h of token t at
- * data[t * token_stride + h * head_stride + d] (strides in elements, >= 0), for
- * instance a part of the packed output of the q/k/v products. */
+ * data[t * token_stride + h * head_stride + d] (strides in elements, 0 to 2^40, the
+ * last element less than 2^60 behind the first), for instance a part of the
+ * packed output of the q/k/v products. */
 typedef struct q4_heads {
     void* data;
     int64_t token_stride;
@@ -513,8 +514,10 @@ typedef struct q4_heads {
 
 /* A paged key/value cache: element d of kv head h in slot s of page p at
  * k[p * k_page_stride + h * k_head_stride + s * k_slot_stride + d], v alike
- * (strides in elements; both may be parts of one tensor).  Which pages a
- * sequence holds is in its row of q4_kv_batch's block table. */
+ * (strides in elements, of the same limits; both may be parts of one tensor).
+ * q4_kv_append writes it: there each stride that is used steps over all that the
+ * smaller ones reach, and keys and values lie apart or beside each other in equal
+ * steps.  Which pages a sequence holds is in its row of q4_kv_batch's block table. */
 typedef struct q4_kv_cache {
     void* k;
     void* v;
@@ -542,7 +545,7 @@ typedef struct q4_kv_batch {
     const int32_t* block_table;
     int64_t table_stride; /* int32 entries from one sequence's row to the next */
     int table_pages;      /* entries of a row, >= 1, together at most 2^30 tokens */
-    int seqs;             /* >= 1 */
+    int seqs;             /* 1 .. 2^24 */
     const int32_t* query_start;
     const int32_t* context_len;
     /* Most new tokens of a sequence and longest context, 0 if not known: they
@@ -562,7 +565,8 @@ typedef struct q4_kv_batch {
  *               gradient), 4-byte aligned
  *   inv_freq  : rot_dim / 2 binary64 values, 8-byte aligned: the frequencies,
  *               with any scaling for long contexts in them
- *   tokens >= 1, heads >= 1, 2 <= rot_dim <= head_dim <= 1024, rot_dim even
+ *   1 <= tokens <= 2^27, 1 <= heads <= 4096 (of queries, keys and values alike in
+ *   the operators below), 2 <= rot_dim <= head_dim <= 1024, rot_dim even
  * Angles are reduced in binary64, so far positions keep their precision; the
  * rotation is in binary32 and each element is rounded once.  Any strides and
  * alignments of the elements' own size; 16-byte aligned heads with

@@ -15,7 +15,10 @@
 // A wave takes 32 keys at a time, straight from HBM into its own part of LDS
 // (global_load_lds, whole rows, 16 bytes a lane), so that waves never wait for each
 // other: while it works on V, the next step's K is on its way into the place that
-// K left, and the next V follows into V's.
+// K left, and the next V follows into V's.  (Before the scores the compiler waits
+// for the queries in every step, as it does not count on the wait before the loop;
+// loads return in order, so V is waited for there too, and only the K of the next
+// step is on its way beside work.)
 //   S^T = K Q^T on v_mfma_f32_16x16x32, 16 keys a tile: lane (q, n) gets the keys 4 q
 //     .. 4 q + 3 of both tiles for query row n, which is the B operand P^T of
 //   O^T = V^T P^T, whose A operand the transposing LDS reads give for the same keys.
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const AttnArgs a, c
         int t = k_lo + wave * kStep;
         Pages now = {}, next = {};
         if (t < k_hi) now = pages(t);
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // the queries: no wait for them in the loop
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // the queries
         if (t < k_hi) {
             fill_k(t, now);
             fill_v(t, now);

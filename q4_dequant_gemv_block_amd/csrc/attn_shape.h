@@ -27,7 +27,9 @@ inline int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int
 // from the longest context and the most new tokens of a sequence, as far as the
 // caller knows them, and the cheapest way is taken.
 //
-// The numbers are fits to calls run in each way, head_dim 64 to 256, equal and
+// The estimates are numbers to compare ways by, of the size of microseconds but no
+// forecast (a windowed call of 34 us is put at 18, a chunk of 490 at 385).  They are
+// fits to calls run in each way, head_dim 64 to 256, equal and
 // ragged, with and without windows.  Tiles: 560 calls of 64 to 4096 new tokens of 1
 // to 30 sequences, up to 30000 keys; what is taken was within 5 % of the best of the
 // four ways in 540 and 22 % behind at most.  k_attn: 264 calls of 1 to 4 new tokens
@@ -42,7 +44,7 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
     const int64_t context = max_context > 0 ? std::min<int64_t>(max_context, capacity) : capacity;
     const double dim = c.head_dim / 128.0;
     AttnShape best = {};
-    double best_us = 0;
+    double best_cost = 0;
     auto consider = [&](int rows) {
         AttnShape s = {};
         s.rows = rows;
@@ -84,9 +86,9 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
             s.few = items * 8 <= slots;
             s.bytes = (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + 2 * sizeof(float));
         }
-        if (!best.rows || std::min(whole, cut) < best_us) {
+        if (!best.rows || std::min(whole, cut) < best_cost) {
             best = s;
-            best_us = std::min(whole, cut);
+            best_cost = std::min(whole, cut);
         }
     };
     if (most <= 32) {

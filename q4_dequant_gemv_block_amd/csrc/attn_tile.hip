@@ -9,6 +9,10 @@
 // share a CU (8 waves of 256 rows that share the tiles were no faster: 606 us
 // against 578 for a prompt of 8192).  K and V go from HBM or L2 straight into LDS
 // (global_load_lds, 16 bytes a lane), two tiles of each deep, one barrier a tile.
+// (A tile begins with the loads of the next V and of the K behind it, then looks up
+// the pages of a later tile, and the compiler waits for that lookup at once; loads
+// return in order, so the tile's work starts when all of these have landed.  The
+// compiler's waits for the queries, in every other tile, come behind that.)
 // The products run on v_mfma_f32_32x32x16:
 //   S^T = K Q^T: A = 32 keys from LDS, B = Q^T, which stays in registers;
 //   O^T = V^T P^T: A = V^T by the transposing LDS read (ds_read_b64_tr_b16: 16
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             page0 = pages(t);
             page1 = pages(t + kTile);
             page2 = pages(t + 2 * kTile);
-            __builtin_amdgcn_s_waitcnt(0x0F70);  // with the queries: no wait for them, and so for tiles, in the loop
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // with the queries
             fill_k(t, page0, 0);
             fill_v(t, page0, 0);
             if (t + kTile < it.k_hi) {

@@ -16,10 +16,12 @@
 // block table, store), and then the units of a token are spread over several
 // workgroups.
 //
-// Measured: 8191 tokens of 32 heads of 128 in bf16 22.9 us (5.9 TB/s read and
-// written, a copy of that size reaches 4.7), 8192 tokens into a cache of 8 heads
-// with 32 query heads 37 us (4.4 TB/s); one token 3.7 to 4.1 us, as long
-// as an empty launch.
+// Measured with 12 sets of tensors in turn, more than the last-level cache holds:
+// 8191 tokens of 32 heads of 128, 64 of each rotated, in bf16 30.3 us (4.4 TB/s read
+// and written; a plain copy of the same heads 27.1), rotated whole in binary32 55.4
+// us (4.9 TB/s), 5 ragged prompts of 6,709 tokens together into a cache of 8 heads
+// with 32 query heads 39.5 us (4.2 TB/s); with one set, from that cache in part,
+// 23.1, 47.8 and 30.7 us.  One token 3.7 to 4.1 us, as long as an empty launch.
 #include "kv_device.h"
 #include "q4gemv.h"
 
