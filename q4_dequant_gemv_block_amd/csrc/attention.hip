@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const AttnArgs a, c
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, n16 = lane & 15;
     WORK work;
-    if (!work.start(cut, a.batch)) return;
+    Item it;
+    if (!work.start(cut, a.batch, &it)) return;
     const Seq& seq = work.seq;
     const Parts<D> parts(a.workspace, (int)gridDim.x, ROWS);
     // this wave's K and V, and where the lane reads in them
@@ -109,7 +110,6 @@ __global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const AttnArgs a, c
     const char* at_v = my + L::bytes + row_v * L::row + (n16 & 1) * 8;
     const int chunk_v = ((n16 & 3) >> 1) ^ L::swz_v(row_v);
     const bool one_page = a.cache.page_size.d % kStep == 0;  // a step's keys lie in one page
-    Item it;
     while (work.next(cut, a.batch, &it)) {
         const int head = it.head, row0 = it.row0, rows = it.rows, past = it.past;
         const int p_first = it.p_first, p_last = it.p_last, k_lo = it.k_lo, k_hi = it.k_hi;
@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const AttnArgs a, c
                 if (d == 0) parts.ml[slot * ROWS + row] = f2{top, sum};
             }
         }
+        if constexpr (WORK::once) break;
         __syncthreads();
     }
 }
@@ -502,7 +503,6 @@ Cut make_cut(const AttnArgs& a, const AttnShape& s) {
     c.unit_log2 = __builtin_ctz(s.unit);
     c.step = s.step;
     c.window = a.window;
-    c.places = (uint32_t)s.places;
     c.per_token = s.per_token;
     c.group = FastDiv((uint32_t)a.group);
     c.kv_heads = FastDiv((uint32_t)a.cache.kv_heads);
@@ -517,8 +517,9 @@ hipError_t launch_work(const AttnArgs& a, const AttnShape& shape, hipStream_t s)
     static LdsLimit limit;
     const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn<T, D, NR, WORK>), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn<T, D, NR, WORK>), dim3(shape.grid), dim3(64 * Layout<D, NR>::waves), lds, s, a, make_cut(a, shape));
-    return hipGetLastError();
+    return launch_shape(shape, make_cut(a, shape), [&](unsigned grid, const Cut& c) {
+        hipLaunchKernelGGL((k_attn<T, D, NR, WORK>), dim3(grid), dim3(64 * Layout<D, NR>::waves), lds, s, a, c);
+    });
 }
 
 template <typename T, int D, int NR>

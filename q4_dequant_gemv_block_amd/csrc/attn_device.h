@@ -4,6 +4,7 @@
 
 #include "kv_device.h"
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -75,11 +76,23 @@ __device__ __forceinline__ void wave_lds_fence() {
 struct Cut {
     int rows_log2, unit_log2, step;  // an item's keys begin at a multiple of step
     int window, capacity;            // capacity: tokens a row of the block table holds
-    uint32_t places;                 // for items that are taken whole (Places)
+    uint32_t place;                  // items taken whole (Places): the first workgroup's place
     int per_token;                   // places of a token and kv head; 0: by rows
     FastDiv group, kv_heads;
     int64_t tokens;
 };
+
+// Launches a call's workgroups with what they are told: those of whole items 2^22 at
+// a time (a launch has fewer than 2^32 threads along an axis).
+template <typename L>
+hipError_t launch_shape(const AttnShape& shape, Cut cut, L launch) {
+    if (!shape.places) launch((unsigned)shape.grid, cut);
+    for (int64_t at = 0; at < shape.places; at += 1 << 22) {
+        cut.place = (uint32_t)at;
+        launch((unsigned)std::min<int64_t>(shape.places - at, 1 << 22), cut);
+    }
+    return hipGetLastError();
+}
 
 // What one sequence asks for.
 struct Seq {
@@ -97,6 +110,16 @@ __device__ __forceinline__ void cut_sequence(const Cut& c, Seq* s) {
     }
     s->tiles = (int)(((int64_t)s->n * c.group.d + (1 << c.rows_log2) - 1) >> c.rows_log2);
     s->units = s->n ? max(1, (int)(((int64_t)span + (1 << c.unit_log2) - 1) >> c.unit_log2)) : 0;
+}
+
+// Sequence b.  One whose rows are not all among the call's has no new tokens.
+__device__ __forceinline__ void read_sequence(const Cut& c, const BatchArg& batch, int b, Seq* s) {
+    const int first = batch.query_start[b], last = batch.query_start[b + 1];
+    s->b = b;
+    s->ctx = batch.context_len[b];
+    s->row0 = first;
+    s->n = first < 0 || last > c.tokens || last < first ? 0 : last - first;
+    cut_sequence(c, s);
 }
 
 // First unit of range w of `grid`.
@@ -134,68 +157,80 @@ __device__ __forceinline__ void place_keys(const Cut& c, const Seq& seq, Item* x
     x->k_hi = (int)min((int64_t)keys, start + ((int64_t)x->u1 << c.unit_log2));
 }
 
-// Items taken whole, a workgroup each, which must not walk through the sequences
-// (a batch's time would grow with its square).  Place x of a kv head belongs to the
-// last sequence b with f(b) <= x, found by 64 probes a step, where f is
-//   floor(query_start[b] group / rows) + min(query_start[b], b), or
-//   query_start[b] ceil(group / rows),
-// whichever ends lower (the second for decode steps).  Over a sequence with new
-// tokens f grows by at least its items (floor(A + B) - floor(A) >= floor(B), and 1
-// more for what that leaves out), so each item has a place; what is left are empty
-// places.  f of the end is what item_bound() counts.
+// Items taken whole, a workgroup each, which must not walk through many sequences
+// (a batch's time would grow with its square).  The places of a kv head:
+//   up to 64 sequences: their items one after the other (a load and a scan);
+//   decode steps of more: ceil(group / rows) of each token, so those of sequence b
+//     begin at query_start[b] ceil(group / rows);
+//   others: a(b) = floor(query_start[b] group / rows) and on, a(b + 1) - a(b) items
+//     of sequence b, which has one more at most (floor(A + B) - floor(A) is B rounded
+//     down or up); behind all of those one place for each sequence's last item, at
+//     min(query_start[b], b), which grows by 1 over a sequence with new tokens.
+// The sequence of a place is the last that begins at it or in front, found as in
+// last_low.  Empty places are behind the items, or (the last items of sequences) few
+// among them: in their midst they would hold up workgroups with work (40 x 2 tokens
+// of 1500 keys, 8 heads a kv head: 15.6 us, with an empty place behind each item 23.7).
+// item_bound() counts them.
 struct Places {
+    static constexpr bool once = true;  // the kernel's loop over items is left after the first, and holds nothing for others
     Seq seq;
-    uint32_t at;  // the place to look at next
 
-    __device__ __forceinline__ bool start(const Cut& c, const BatchArg& batch) {
-        at = blockIdx.x;
-        return true;
-    }
     // Picks the sequence of a place; false if the place is empty.
     __device__ __forceinline__ bool find(const Cut& c, const BatchArg& batch, uint32_t place, uint32_t* item) {
-        const int64_t x = c.kv_heads.div(place);
-        auto first_place = [&](int start, int b) {
-            const int64_t s = max(start, 0);
-            return c.per_token ? s * c.per_token : (s * c.group.d >> c.rows_log2) + min(s, (int64_t)b);
-        };
-        int lane = threadIdx.x & 63;
-        asm volatile("" : "+v"(lane));  // made anew: addresses from it would be held through the kernel's loop
-        int b0 = 0, n = batch.seqs;
-        while (n > 64) {
-            const int step = (n + 63) >> 6, i = lane * step;
-            const int count = max(1, __popcll(__ballot(i < n && first_place(batch.query_start[b0 + i], b0 + i) <= x)));
-            b0 += (count - 1) * step;
-            n = min(step, n - (count - 1) * step);
+        const uint32_t x = c.kv_heads.div(place);
+        uint32_t up;  // item of the kv head
+        if (batch.seqs <= 64) {
+            const int lane = threadIdx.x & 63;
+            Seq s = {};
+            if (lane < batch.seqs) read_sequence(c, batch, lane, &s);
+            uint32_t sum = s.tiles;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const uint32_t t = (uint32_t)__shfl_up((int)sum, o);
+                if (lane >= o) sum += t;
+            }
+            const uint64_t past = __ballot(sum > x);
+            if (!past) return false;
+            const int l = __builtin_ctzll(past);
+            seq.b = l;
+            seq.row0 = __builtin_amdgcn_readlane(s.row0, l);
+            seq.n = __builtin_amdgcn_readlane(s.n, l);
+            seq.ctx = __builtin_amdgcn_readlane(s.ctx, l);
+            cut_sequence(c, &seq);
+            up = x - (uint32_t)__builtin_amdgcn_readlane((int)(sum - s.tiles), l);
+        } else {
+            auto start_of = [&](int b) { return (int64_t)max(batch.query_start[b], 0); };
+            auto full = [&](int b) { return start_of(b) * c.group.d >> c.rows_log2; };
+            const int64_t fulls = c.per_token ? 0 : full(batch.seqs);
+            int b;
+            if (c.per_token) {
+                b = last_low(batch.seqs, [&](int j) { return start_of(j) * c.per_token <= x; });
+                up = x - (uint32_t)(start_of(max(b, 0)) * c.per_token);
+            } else if (x < fulls) {
+                b = last_low(batch.seqs, [&](int j) { return full(j) <= x; });
+                up = x - (uint32_t)full(max(b, 0));
+            } else {
+                b = last_low(batch.seqs, [&](int j) { return min(start_of(j), (int64_t)j) <= x - fulls; });
+                up = (uint32_t)(full(max(b, 0) + 1) - full(max(b, 0)));
+                if (min(start_of(max(b, 0)), (int64_t)max(b, 0)) != x - fulls) return false;
+            }
+            if (b < 0) return false;
+            read_sequence(c, batch, b, &seq);
         }
-        int first = 0, last = 0, ctx = 0;
-        if (lane < n) {
-            first = batch.query_start[b0 + lane];
-            last = batch.query_start[b0 + lane + 1];
-            ctx = batch.context_len[b0 + lane];
-        }
-        const int64_t f = first_place(first, b0 + lane);
-        const int l = max(1, __popcll(__ballot(lane < n && f <= x))) - 1;
-        seq.b = b0 + l;
-        seq.row0 = __builtin_amdgcn_readlane(first, l);
-        const int end = __builtin_amdgcn_readlane(last, l);
-        seq.n = seq.row0 < 0 || end > c.tokens || end < seq.row0 ? 0 : end - seq.row0;
-        seq.ctx = __builtin_amdgcn_readlane(ctx, l);
-        cut_sequence(c, &seq);
-        *item = place - c.kv_heads.d * (uint32_t)__builtin_amdgcn_readlane((int)f, l);
-        return *item < c.kv_heads.d * seq.tiles;
+        *item = up * c.kv_heads.d + (place - x * c.kv_heads.d);
+        return up < (uint32_t)seq.tiles;
     }
-    __device__ __forceinline__ bool next(const Cut& c, const BatchArg& batch, Item* x) {
+    // This workgroup's item, the only one.
+    __device__ __forceinline__ bool start(const Cut& c, const BatchArg& batch, Item* x) {
         uint32_t item;
-        do {
-            if (at >= c.places) return false;
-            at += gridDim.x;
-        } while (!find(c, batch, at - gridDim.x, &item));
+        if (!find(c, batch, c.place + blockIdx.x, &item)) return false;
         x->u0 = 0;
         x->u1 = seq.units;
         place_item(c, seq, item, x);
         place_keys(c, seq, x);
         return true;
     }
+    __device__ __forceinline__ bool next(const Cut&, const BatchArg&, Item*) { return true; }
     __device__ __forceinline__ bool whole(const Item&) const { return true; }
 };
 
@@ -204,6 +239,7 @@ struct Places {
 // sequence of a unit.  A workgroup walks through the sequences twice, but there
 // are never more workgroups than the machine holds.
 struct Work {
+    static constexpr bool once = false;
     uint32_t total;  // units of all sequences
     uint32_t begin;  // first unit of seq
     Seq seq;
@@ -217,13 +253,7 @@ struct Work {
         const int lane = threadIdx.x & 63;
         base = b0;
         Seq s = {};
-        if (b0 + lane < batch.seqs) {
-            const int first = batch.query_start[b0 + lane], last = batch.query_start[b0 + lane + 1];
-            s.ctx = batch.context_len[b0 + lane];
-            s.row0 = first;
-            s.n = first < 0 || last > c.tokens || last < first ? 0 : last - first;
-        }
-        cut_sequence(c, &s);
+        if (b0 + lane < batch.seqs) read_sequence(c, batch, b0 + lane, &s);
         l_row0 = s.row0;
         l_n = s.n;
         l_ctx = s.ctx;
@@ -267,7 +297,7 @@ struct Work {
     }
 
     // This workgroup's range; next() goes through its items.
-    __device__ __forceinline__ bool start(const Cut& c, const BatchArg& batch) {
+    __device__ __forceinline__ bool start(const Cut& c, const BatchArg& batch, Item*) {
         sum(c, batch);
         const uint32_t grid = min((uint32_t)gridDim.x, total);  // no range is empty
         if (blockIdx.x >= grid) return false;

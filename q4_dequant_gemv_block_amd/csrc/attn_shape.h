@@ -10,8 +10,9 @@ namespace q4 {
 
 constexpr int kAttnStep = 32;  // keys a wave of k_attn takes at a time
 
-// Most items a call can have: the rows of a sequence with new tokens round up once,
-// or those of each token; and whether it is the second bound.
+// Places for the items of a call, the most that it can have: the rows of a sequence
+// with new tokens round up once, or those of each token; and whether it is the
+// second (Places in attn_device.h).
 inline int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int rows, int* per_token) {
     const int group = q_heads / c.kv_heads, each = (group + rows - 1) / rows;
     const int64_t by_rows = tokens * group / rows + std::min<int64_t>(b.seqs, tokens);
@@ -78,7 +79,6 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
         if (whole <= cut && bound < (int64_t(1) << 31)) {
             s.unit = 1 << 30;
             s.places = (int)bound;
-            s.grid = std::min(s.places, 1 << 22);  // fewer than 2^32 threads; a workgroup goes on to other places
         } else {
             // larger units where this many would pass 31 bits
             while (s.unit < (1 << 30) && bound * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;

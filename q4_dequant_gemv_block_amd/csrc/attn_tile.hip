@@ -88,10 +88,10 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
     const uint32_t sh0 = lds_address(sh);
 
     WORK work;
-    if (!work.start(cut, a.batch)) return;
+    Item it;
+    if (!work.start(cut, a.batch, &it)) return;
     const Seq& seq = work.seq;
     const Parts<D> parts(a.workspace, (int)gridDim.x, ROWS);
-    Item it;
 
     // where this lane reads in a tile: chunks 2 s + h of K's rows, 64-byte block d of V's
     int at_k0 = (first + n) * L::row + ((h ^ L::swz_k(n)) * 16), at_v0;
@@ -422,13 +422,19 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                     }
             }
             __syncthreads();
-            if (first) continue;
+            if (first) {
+                if constexpr (WORK::once) break;
+                continue;
+            }
         }
         l += __shfl_xor(l, 32);
         // (lane numbers anew: addresses made from them would be held through the loop)
         int n = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
         asm volatile("" : "+v"(n), "+v"(h));
-        if (32 * rows32 + n >= it.rows) continue;
+        if (32 * rows32 + n >= it.rows) {
+            if constexpr (WORK::once) break;
+            continue;
+        }
         if (work.whole(it)) {
             const float f = row_scale(l);
             char* dst = a.out.data + ((int64_t)(seq.row0 + qi) * a.out.token_stride + (int64_t)qh * a.out.head_stride + 4 * h) * 2;
@@ -449,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                     *reinterpret_cast<f4*>(&parts.o[slot * D + 32 * d + 2 * i + 4 * h]) = f4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]};
             if (h == 0) parts.ml[slot] = f2{m, l};
         }
+        if constexpr (WORK::once) break;
     }
 }
 
@@ -458,8 +465,9 @@ hipError_t launch_work(const AttnArgs& a, const Cut& cut, const AttnShape& shape
     static LdsLimit limit;
     const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, U, WORK>), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<T, D, U, WORK>), dim3(shape.grid), dim3(kThreads), lds, s, a, cut);
-    return hipGetLastError();
+    return launch_shape(shape, cut, [&](unsigned grid, const Cut& c) {
+        hipLaunchKernelGGL((k_attn_tile<T, D, U, WORK>), dim3(grid), dim3(kThreads), lds, s, a, c);
+    });
 }
 
 template <typename T, int D, int U>

@@ -83,8 +83,8 @@ struct AttnShape {
     int most_rows; // rows that an item has, as far as the caller knows
     int unit;      // keys of one unit of work
     int step;      // keys a kernel takes at a time
-    int grid;      // workgroups
-    int places;    // places of items that are taken whole, 0: ranges of units
+    int grid;      // workgroups of ranges of units
+    int places;    // workgroups of items that are taken whole, 0: ranges of units
     int per_token; // places of a token and kv head, 0: by rows
     bool few;      // far fewer items than workgroups
     size_t bytes;  // workspace, 0 where every item is taken whole
