@@ -119,7 +119,6 @@ __device__ __forceinline__ void read_sequence(const Cut& c, const BatchArg& batc
     s->ctx = batch.context_len[b];
     s->row0 = first;
     s->n = first < 0 || last > c.tokens || last < first ? 0 : last - first;
-    cut_sequence(c, s);
 }
 
 // First unit of range w of `grid`.
@@ -183,6 +182,7 @@ struct Places {
             const int lane = threadIdx.x & 63;
             Seq s = {};
             if (lane < batch.seqs) read_sequence(c, batch, lane, &s);
+            cut_sequence(c, &s);
             uint32_t sum = s.tiles;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
@@ -216,6 +216,7 @@ struct Places {
             }
             if (b < 0) return false;
             read_sequence(c, batch, b, &seq);
+            cut_sequence(c, &seq);
         }
         *item = up * c.kv_heads.d + (place - x * c.kv_heads.d);
         return up < (uint32_t)seq.tiles;
@@ -254,6 +255,7 @@ struct Work {
         base = b0;
         Seq s = {};
         if (b0 + lane < batch.seqs) read_sequence(c, batch, b0 + lane, &s);
+        cut_sequence(c, &s);
         l_row0 = s.row0;
         l_n = s.n;
         l_ctx = s.ctx;
