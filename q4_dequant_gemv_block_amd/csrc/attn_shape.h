@@ -30,13 +30,15 @@ inline int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int
 //
 // The estimates are numbers to compare ways by, of the size of microseconds but no
 // forecast (a windowed call of 34 us is put at 18, a chunk of 490 at 385).  They are
-// fits to calls run in each way, head_dim 64 to 256, equal and
-// ragged, with and without windows.  Tiles: 560 calls of 64 to 4096 new tokens of 1
-// to 30 sequences, up to 30000 keys; what is taken was within 5 % of the best of the
-// four ways in 540 and 22 % behind at most.  k_attn: 264 calls of 1 to 4 new tokens
-// of 1 to 200 sequences, up to 20000 keys; 260 within 5 % of the better way, 27 %
-// behind at most; of 96 batches of 16 to 200 sequences, half of them with lengths from
-// 1/16 of the longest up, which the host cannot see, 79 and 47 %.
+// fits to calls run in each way, head_dim 64 to 256, equal and ragged, with and
+// without windows, made when whole items took up to 1.5 us longer to start.  As the
+// kernels are now: tiles, 560 calls of 64 to 4096 new tokens of 1 to 30 sequences, up
+// to 30000 keys: what is taken is within 5 % of the best of the four ways in 524 and
+// 19 % behind at most.  k_attn, 264 calls of 1 to 4 new tokens of 1 to 200 sequences,
+// up to 20000 keys: 251 within 5 % of the better way, 38 % behind at most; of 96
+// batches of 16 to 200 sequences, half of them with lengths from 1/16 of the longest
+// up, which the host cannot see, 80, and 64 % behind at most (many short items of a
+// range, each of which starts with nothing on its way).
 inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
     const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
     const int64_t longest = max_query > 0 ? std::min<int64_t>(max_query, tokens) : tokens;  // new tokens of a sequence
