@@ -33,9 +33,9 @@
 // a rounding does not shift a row's weight.
 //
 // Bound by HBM.  Measured, 32 query heads over 8 of 128: 61 ragged sequences up to
-// 8192 keys 178 us and 5 for the join (6.4 TB/s; a read alone reaches 7.2 on this
+// 8192 keys 180 us and 5 for the join (6.4 TB/s; a read alone reaches 7.2 on this
 // card), one token over 131067 keys 84 and 5 (6.4 TB/s); one token over 515 keys of
-// 40 heads 9.4, the latency of 3 steps.
+// 40 heads 8.7, the latency of 3 steps.
 #include "attn_device.h"
 #include "attn_shape.h"
 #include "q4gemv.h"

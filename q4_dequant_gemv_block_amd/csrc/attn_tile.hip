@@ -28,9 +28,9 @@
 // exponentials of this one's, so that neither unit waits for the other.
 //
 // Bound by the matrix cores' issue beside the exponentials.  Measured, heads of 128:
-// 2048 tokens over 16384 keys 492 to 519 us (993 to 1,047 TFLOP/s with the card's
+// 2048 tokens over 16384 keys 482 to 514 us (1,002 to 1,069 TFLOP/s with the card's
 // clock and the cache; a large library product reaches 1,087 to 1,145), a prompt of
-// 8192 567 to 603 (912 to 970), one of 169 tokens 10 us (latency).
+// 8192 551 to 573 (960 to 998), one of 169 tokens 9.1 (latency).
 #include "attn_device.h"
 #include "q4gemv.h"
 
