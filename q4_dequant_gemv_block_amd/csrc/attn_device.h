@@ -171,7 +171,9 @@ __device__ __forceinline__ void place_keys(const Cut& c, const Seq& seq, Item* x
 // of 1500 keys, 8 heads a kv head: 15.6 us, with an empty place behind each item 23.7).
 // item_bound() counts them.
 struct Places {
-    static constexpr bool once = true;  // the kernel's loop over items is left after the first, and holds nothing for others
+    // The kernel's loop over items is left after the first one and holds nothing for
+    // others: no scalar registers are spilled for them (50 to 110 are for ranges).
+    static constexpr bool once = true;
     Seq seq;
 
     // Picks the sequence of a place; false if the place is empty.
