@@ -54,8 +54,8 @@ KERNEL_SOURCE = {"sweep": ["gemv.hip"], "gemv": ["gemv.hip"], "lmhead": ["gemv.h
                  "handoff": ["gemv.hip"], "q8": ["gemv.hip", "q8.hip"],
                  "smallm": ["smallm.hip"],
                  "prefill": ["prefill.hip"], "verify": ["smallm.hip", "gemv.hip", "verify.hip"],
-                 "attention": ["rope.hip", "attention.hip", "attn_tile.hip", "attn_device.h", "attn_shape.h", "kv_device.h",
-                               "kv_launch.h", "kv_api.cpp"]}
+                 "attention": ["rope.hip", "attention.hip", "attn_tile.hip", "attn_rows.h", "attn_tile.h", "attn_device.h",
+                               "attn_shape.h", "kv_device.h", "kv_launch.h", "kv_checks.h", "kv_api.cpp"]}
 
 
 def kernel_source_hash(workload: str) -> str:

@@ -631,6 +631,225 @@ Q4_API q4_status q4_attention_paged(const q4_kv_cache* cache, const q4_kv_batch*
                                     const q4_heads* out, float* lse, int q_heads, int64_t tokens, float scale,
                                     int64_t window, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The operators below are those of a decode step whose drafts are trees: each new
+ * token of a sequence names another one as its parent, the first is the last token
+ * that was chosen, and one pass of the trunk verifies all of them.
+ *
+ *   q4_kv_assign       block tables, slots, positions and masks from the lengths
+ *   q4_kv_append_norm  (q4_kv_append with norms of queries and keys) into the cache
+ *   q4_attention_tree  each new token over the cached ones and its ancestors
+ *   q4_logits_argmax   the pick behind each node under penalties and grammars
+ *   q4_tree_accept     the path that the drafts share with the picks
+ *   q4_kv_move         the path's keys and values side by side in the cache
+ *
+ * Lengths, tables and paths stay in device memory, so the step can be one captured
+ * graph.  A sequence is at most 1024 drafted tokens deep in a mask (16 words).
+ */
+
+/* A step's tables.  All tensors are int32 unless noted, in DEVICE memory, 4-byte
+ * aligned (slots, mask: 8). */
+typedef struct q4_kv_step {
+    /* read */
+    const int32_t* table_in;    /* seqs rows: pages each sequence holds, in order */
+    int64_t table_in_stride;    /* entries from one row to the next, >= table_pages */
+    const int32_t* held_in;     /* seqs: how many of them (the entries behind are free to be anything) */
+    const int32_t* past_len;    /* seqs: tokens in the cache */
+    const int32_t* new_len;     /* seqs: tokens of this step */
+    const int32_t* free_pages;  /* free_capacity: pages nobody holds, the first *free_count of them */
+    int64_t free_capacity;      /* 0 .. 2^31 - 1 */
+    const int32_t* free_count;  /* 1 */
+    const int32_t* parents;     /* NULL, or tokens: index of a token's parent among its sequence's new tokens, less
+                                   than its own; others (-1) are none */
+    /* written */
+    int32_t* table;             /* seqs rows; may be table_in itself, with its stride */
+    int64_t table_stride;
+    int32_t* held;              /* seqs */
+    int32_t* query_start;       /* seqs + 1 */
+    int32_t* context_len;       /* seqs */
+    int32_t* missing;           /* seqs: pages a sequence lacks, 0 if it was served */
+    int32_t* free_left;         /* 1: the pages that are left are the first ones of free_pages */
+    int32_t* positions;         /* tokens */
+    int64_t* slots;             /* tokens, int64: page * page_size + place in it, -1 for a token without a place */
+    uint64_t* mask;             /* NULL, or tokens x mask_words */
+    int mask_words;             /* 0 without mask, else 1 .. 16 */
+    int seqs;                   /* 1 .. 65536 */
+    int table_pages;            /* entries of a row that count, >= 1, together at most 2^30 tokens */
+    int page_size;              /* a multiple of 8, 8 .. 65536 */
+    int64_t tokens;             /* rows of positions, slots, mask and parents, 1 .. 2^27 */
+} q4_kv_step;
+
+/*
+ * The tables of a step from its lengths: query_start (sums of new_len), context_len
+ * = past_len + new_len, and a page for every place that a sequence needs and does
+ * not hold.  Pages are taken from the end of the free list, in the order of the
+ * sequences and of their places.  A sequence whose pages do not fit into what is
+ * left gets none of them (and so does every later one that needs any): missing says
+ * how many it lacks, its held and entries stay as they were.  Entries behind the
+ * pages a sequence holds are copied as they are.
+ *   slots     : of new token i, place past_len + i in the cache
+ *   positions : past_len + i; with parents past_len + the number of its ancestors
+ *   mask      : bit j of a row (bit j % 64 of word j / 64): j is the token itself or
+ *               an ancestor of it; without parents each token follows the one before.
+ *               With parents, new tokens from the 64 mask_words-th on (the 1024th
+ *               without mask) have no bits and no ancestors.
+ * Rows behind the last sequence's are left as they are, rows behind `tokens` are not
+ * written.  Lengths below 0 count as 0, those above 2^30 as 2^30, held_in is taken
+ * as at most table_pages.  Nothing that is written overlaps anything else here,
+ * except the table in place.  Deterministic.
+ */
+Q4_API q4_status q4_kv_assign(const q4_kv_step* step, void* stream);
+
+/*
+ * q4_rope behind a norm of each head:
+ *   y = x * gain / sqrt(mean over the head of x^2 + eps),
+ * then y's pairs turn as in q4_rope (and y's elements from rot_dim on are written
+ * as they are).
+ *   gain     : NULL (ones), or head_dim values of gain_type, aligned to their size
+ *   eps      : finite, >= 0
+ *   positions, inv_freq : as in q4_rope; may be NULL with rot_dim == 0 (no rotation)
+ * The norm's sum, y and the rotation are binary32, and each element is rounded once;
+ * the sum of squares of a head must be finite in binary32.  A head of zeros with eps
+ * == 0 gives NaN.  Sizes, strides and the fast path as in q4_rope.
+ */
+Q4_API q4_status q4_norm_rope(const q4_heads* x, const q4_heads* out, const void* gain, int gain_type, float eps,
+                              const int32_t* positions, const double* inv_freq, int64_t tokens, int heads,
+                              int head_dim, int rot_dim, int layout, float mscale, void* stream);
+
+/*
+ * q4_kv_append with the norm of q4_norm_rope on the keys' heads (and the queries',
+ * if given) before they turn; values are appended as they are.
+ *   q_gain, k_gain : NULL (ones), or head_dim values each, both of gain_type
+ * With positions the angles are theirs (a tree's depths), the places in the cache
+ * those of the batch.  Everything else as in q4_kv_append.
+ */
+Q4_API q4_status q4_kv_append_norm(const q4_kv_cache* cache, const q4_kv_batch* batch, const q4_heads* k,
+                                   const q4_heads* v, const q4_heads* q, const q4_heads* q_out, int q_heads,
+                                   int64_t tokens, const void* q_gain, const void* k_gain, int gain_type, float eps,
+                                   const int32_t* positions, const double* inv_freq, int rot_dim, int layout,
+                                   float mscale, void* stream);
+
+/* As q4_attention_paged_workspace_bytes, for q4_attention_tree. */
+Q4_API size_t q4_attention_tree_workspace_bytes(const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads,
+                                                int64_t tokens, int64_t window);
+
+/*
+ * q4_attention_paged where the new tokens of a sequence are a tree (q4_kv_batch's
+ * query_start and context_len as there; new token j lies at place past + j of its
+ * sequence, past = context_len - new tokens): a row sees every key at a place below
+ * past and the new tokens j whose bit is set in its mask.
+ *   mask   : tokens x mask_words uint64, 8-byte aligned: bit j % 64 of word j / 64;
+ *            1 <= mask_words <= 16.  New tokens from 64 mask_words on, and bits from
+ *            the number of new tokens on, count as not set.  Any bits will do, a
+ *            row's own among them or not.
+ *   window : with window > 0 the keys below past are seen from past + depth - window
+ *            + 1 on, depth being the number of new tokens that the row sees beside
+ *            itself: the place a token of a path has.  The mask alone decides about
+ *            new tokens.
+ * Everything else, workspace and limits included, as in q4_attention_paged.  With the
+ * mask of a chain the rows see what they see there.
+ */
+Q4_API q4_status q4_attention_tree(const q4_kv_cache* cache, const q4_kv_batch* batch, const q4_heads* q,
+                                   const q4_heads* out, const uint64_t* mask, int mask_words, float* lse, int q_heads,
+                                   int64_t tokens, float scale, int64_t window, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* Rules on the logits of a step's rows.  All pointers are DEVICE memory or NULL
+ * (that rule is not there); int32 and binary32, 4-byte aligned, mask 8. */
+typedef struct q4_logit_rules {
+    int seqs;                   /* 1 .. 2^24 */
+    const int32_t* query_start; /* seqs + 1: rows of each sequence, not falling; NULL: row t is sequence t */
+    /* what a sequence has behind it: its tokens in order, history_len[b] of them, the first prompt_len[b] its prompt
+     * (prompt_len NULL: none), the others its answer */
+    const int32_t* history;     /* seqs rows of history_tokens entries */
+    int64_t history_stride;
+    int history_tokens;         /* >= 1 with history; what history_len has above it does not count */
+    const int32_t* history_len; /* goes with history */
+    const int32_t* prompt_len;
+    /* drafted tokens, one a row: part of the answer for the rows that see them */
+    const int32_t* draft;       /* rows */
+    const uint64_t* mask;       /* rows x mask_words: bit j: the row sees its sequence's j-th; NULL: those up to its own */
+    int mask_words;             /* 1 .. 16 with mask, else 0 */
+    const float* repetition;    /* seqs each, > 0 */
+    const float* presence;
+    const float* frequency;
+    const int32_t* bias_start;  /* seqs + 1: a sequence's part of the lists, not falling */
+    const int32_t* bias_tokens; /* biases; of equal tokens in a sequence's part the last counts */
+    const float* bias_values;   /* biases */
+    int64_t biases;             /* 0 .. 2^31 - 1 */
+    const uint32_t* allowed;    /* allowed_rows rows of ceil(vocab / 32) words: bit v % 32 of word v / 32: v may be picked */
+    int64_t allowed_stride;
+    int64_t allowed_rows;
+    const int32_t* allowed_row; /* rows: the row of `allowed` that holds for a row of logits, one outside it: all are
+                                   allowed; NULL: its own number */
+} q4_logit_rules;
+
+/* Bytes of device workspace q4_logits_argmax needs (0: none, or sizes that are not valid). */
+Q4_API size_t q4_logits_argmax_workspace_bytes(int64_t rows, int64_t vocab);
+
+/*
+ * For row t and token v, with c the number of times v is in the answer and "seen" if
+ * it is in the prompt or the answer:
+ *   x = seen ? (x > 0 ? x / repetition : x * repetition) : x
+ *   x = x - frequency * c;  if c > 0: x = x - presence;  x = x + bias[v];
+ *   x = -infinity if v is not allowed
+ * each step rounded to binary32; tokens[t] = lowest v with the largest x.  NaN and
+ * -infinity are never picked: where nothing else is there, tokens[t] = -1.
+ *   logits : rows x vocab of `type`, rows row_stride elements apart
+ *   out    : NULL, or rows x vocab binary32 (written), may be logits itself (binary32,
+ *            the same stride)
+ *   tokens : rows int32 (written)
+ *   rules  : NULL: the bare pick
+ *   workspace : q4_logits_argmax_workspace_bytes(rows, vocab) bytes, 8-byte aligned
+ *            (NULL if 0); its contents on entry do not matter.  Calls that may overlap
+ *            in time need one each.
+ *   1 <= rows <= 2^24, 1 <= vocab <= 2^24; without query_start rows <= seqs
+ * Tokens outside [0, vocab) in any list do not count.  Rows outside [query_start[0],
+ * query_start[seqs]) are left as they are.  Deterministic.
+ */
+Q4_API q4_status q4_logits_argmax(const void* logits, int type, int64_t row_stride, int64_t rows, int64_t vocab,
+                                  const q4_logit_rules* rules, float* out, int64_t out_stride, int32_t* tokens,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The path through each sequence's drafted tree that the trunk agrees with: from the
+ * sequence's first new token on, the lowest child whose draft is what was chosen
+ * behind the node.  Rows are those of query_start and context_len as in q4_kv_batch;
+ * a sequence whose rows are not all among the call's has none.
+ *   choice  : tokens int32, the trunk's token behind each node (one below 0 ends the path)
+ *   draft   : tokens int32, each node's own token
+ *   parents : as in q4_kv_step, NULL: each node is the child of the one before
+ *   accepted: seqs (written): nodes of the path, the first one included; 0 without new tokens
+ *   next    : seqs (written): choice behind the last of them, -1 without new tokens
+ *   path    : tokens (written): the path's nodes (indices among the sequence's new
+ *             tokens) in the sequence's first rows, -1 in its others; rows of no sequence
+ *             are left as they are
+ *   lens    : seqs (written): context_len without the nodes that were not taken
+ *   history : NULL, or seqs rows of history_tokens entries, history_stride apart
+ *             (written): the path's drafts, from entry context_len - new tokens on,
+ *             as far as there are entries
+ *   1 <= seqs <= 2^24, 1 <= tokens <= 2^27.  No output overlaps anything else.
+ */
+Q4_API q4_status q4_tree_accept(const int32_t* query_start, const int32_t* context_len, int seqs,
+                                const int32_t* choice, const int32_t* draft, const int32_t* parents, int64_t tokens,
+                                int32_t* accepted, int32_t* next, int32_t* path, int32_t* lens, int32_t* history,
+                                int64_t history_stride, int history_tokens, void* stream);
+
+/*
+ * The keys and values of a path's nodes to the places behind each other that the path
+ * has: for j < accepted[b], what lies at place past + path[j] moves to past + j (past
+ * = context_len - new tokens), in the caches of all layers at once.
+ *   caches : 1 <= layers <= 512 descriptors (host memory) with the same sizes, strides and type;
+ *            no two keys or values may be the same memory
+ *   path   : tokens int32, accepted: seqs int32, as q4_tree_accept writes them; an entry
+ *            that is not above its own index j, or not below the number of new tokens,
+ *            moves nothing
+ * Slots that no path's node moves to are left as they are; places without a page are
+ * neither read nor written.  The pages of a sequence's new tokens must be its own.
+ */
+Q4_API q4_status q4_kv_move(const q4_kv_cache* caches, int layers, const q4_kv_batch* batch, const int32_t* path,
+                            const int32_t* accepted, int64_t tokens, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -46,6 +46,8 @@ EXPORTS = (
     "q4_0_gemm_prefill_batch_plan_bytes", "q4_0_gemm_prefill_batch_plan", "q4_0_gemm_prefill_batch",
     "q4_0_gemv_batch", "q4_0_gemv_batch_handoff",
     "q4_rope", "q4_kv_append", "q4_attention_paged_workspace_bytes", "q4_attention_paged",
+    "q4_kv_assign", "q4_norm_rope", "q4_kv_append_norm", "q4_attention_tree_workspace_bytes", "q4_attention_tree",
+    "q4_logits_argmax_workspace_bytes", "q4_logits_argmax", "q4_tree_accept", "q4_kv_move",
 )
 
 Q4_TYPE_F16 = 0
@@ -96,6 +98,27 @@ class BatchDesc(ctypes.Structure):
     _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_pages", ctypes.c_int),
                 ("seqs", ctypes.c_int), ("query_start", ctypes.c_void_p), ("context_len", ctypes.c_void_p),
                 ("max_query", ctypes.c_int), ("max_context", ctypes.c_int)]
+
+
+class StepDesc(ctypes.Structure):
+    _fields_ = [("table_in", ctypes.c_void_p), ("table_in_stride", ctypes.c_int64), ("held_in", ctypes.c_void_p),
+                ("past_len", ctypes.c_void_p), ("new_len", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("free_capacity", ctypes.c_int64), ("free_count", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("held", ctypes.c_void_p),
+                ("query_start", ctypes.c_void_p), ("context_len", ctypes.c_void_p), ("missing", ctypes.c_void_p),
+                ("free_left", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("mask_words", ctypes.c_int), ("seqs", ctypes.c_int),
+                ("table_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("tokens", ctypes.c_int64)]
+
+
+class RulesDesc(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int), ("query_start", ctypes.c_void_p), ("history", ctypes.c_void_p),
+                ("history_stride", ctypes.c_int64), ("history_tokens", ctypes.c_int), ("history_len", ctypes.c_void_p),
+                ("prompt_len", ctypes.c_void_p), ("draft", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("mask_words", ctypes.c_int), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("bias_start", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p),
+                ("bias_values", ctypes.c_void_p), ("biases", ctypes.c_int64), ("allowed", ctypes.c_void_p),
+                ("allowed_stride", ctypes.c_int64), ("allowed_rows", ctypes.c_int64), ("allowed_row", ctypes.c_void_p)]
 
 
 _lib = None
@@ -174,6 +197,25 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.q4_attention_paged_workspace_bytes.argtypes = [vp, vp, i32, i64, i64]
     lib.q4_attention_paged.restype = st
     lib.q4_attention_paged.argtypes = [vp, vp, vp, vp, vp, i32, i64, f32, i64, vp, ctypes.c_size_t, vp]
+    size = ctypes.c_size_t
+    lib.q4_kv_assign.restype = st
+    lib.q4_kv_assign.argtypes = [vp, vp]
+    lib.q4_norm_rope.restype = st
+    lib.q4_norm_rope.argtypes = [vp, vp, vp, i32, f32, vp, vp, i64, i32, i32, i32, i32, f32, vp]
+    lib.q4_kv_append_norm.restype = st
+    lib.q4_kv_append_norm.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, vp, vp, i32, f32, vp, vp, i32, i32, f32, vp]
+    lib.q4_attention_tree_workspace_bytes.restype = size
+    lib.q4_attention_tree_workspace_bytes.argtypes = [vp, vp, i32, i64, i64]
+    lib.q4_attention_tree.restype = st
+    lib.q4_attention_tree.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i64, f32, i64, vp, size, vp]
+    lib.q4_logits_argmax_workspace_bytes.restype = size
+    lib.q4_logits_argmax_workspace_bytes.argtypes = [i64, i64]
+    lib.q4_logits_argmax.restype = st
+    lib.q4_logits_argmax.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, size, vp]
+    lib.q4_tree_accept.restype = st
+    lib.q4_tree_accept.argtypes = [vp, vp, i32, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i32, vp]
+    lib.q4_kv_move.restype = st
+    lib.q4_kv_move.argtypes = [vp, i32, vp, vp, vp, i64, vp]
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -768,6 +810,7 @@ class KVBatch:
         b = block_table.shape[0]
         self.device, self.gpu = block_table.device, block_table.get_device()
         self._keep = (block_table, query_start, context_lens)
+        self.seqs = b
         self.desc = BatchDesc(block_table.data_ptr(), block_table.stride(0), block_table.shape[1], b,
                               _vector(query_start, torch.int32, "query_start", b + 1, self.gpu),
                               _vector(context_lens, torch.int32, "context_lens", b, self.gpu),
@@ -885,6 +928,480 @@ def q4_attention_paged(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: f
     return out
 
 
+class KVStep:
+    """The tables of a step, which q4_kv_assign writes: block_table [B, P], held [B], query_start [B + 1],
+    context_lens [B], missing [B], free_count [1] and positions [T], int32, slots [T] and, with mask_words > 0, mask
+    [T, mask_words], int64; and `batch`, the KVBatch of them.  The last step's tables (block_table, held, free_count)
+    are the next one's inputs, so a program keeps two of these and takes them in turn.  table: a tensor [B, P] to
+    write the block table to instead of one of its own (say the one it is read from)."""
+
+    def __init__(self, seqs: int, table_pages: int, page_size: int, tokens: int, mask_words: int = 0,
+                 max_query_len: int | None = None, max_context_len: int | None = None,
+                 table: torch.Tensor | None = None, device="cuda"):
+        for n, name in ((seqs, "seqs"), (table_pages, "table_pages"), (tokens, "tokens")):
+            if n < 1:
+                raise ValueError("%s must be at least 1" % name)
+        if mask_words < 0:
+            raise ValueError("mask_words must not be negative")
+
+        if table is not None and tuple(table.shape) != (seqs, table_pages):
+            raise ValueError("table must be int32 [%d, %d]" % (seqs, table_pages))
+        # the small tensors are parts of one, 64 bytes apart
+        sizes = [seqs, seqs + 1, seqs, seqs, 1, tokens]
+        starts = [0]
+        for n in sizes:
+            starts.append(starts[-1] + -(-n // 16) * 16)
+        whole = torch.zeros(starts[-1], dtype=torch.int32, device=device)
+        self.held, self.query_start, self.context_lens, self.missing, self.free_count, self.positions = (
+            whole[at : at + n] for at, n in zip(starts, sizes))
+        self.block_table = table if table is not None else torch.zeros((seqs, table_pages), dtype=torch.int32, device=device)
+        longs = torch.zeros((tokens, 1 + mask_words), dtype=torch.int64, device=device).view(-1)
+        self.slots = longs[:tokens]
+        self.mask = longs[tokens:].view(tokens, mask_words) if mask_words else None
+        self.seqs, self.table_pages, self.page_size, self.tokens, self.mask_words = seqs, table_pages, page_size, tokens, mask_words
+        self.batch = KVBatch(self.block_table, self.query_start, self.context_lens, max_query_len, max_context_len)
+        self.device, self.gpu = self.batch.device, self.batch.gpu
+        d = StepDesc()
+        d.table, d.table_stride = self.block_table.data_ptr(), self.block_table.stride(0)
+        d.held, d.query_start, d.context_len = self.held.data_ptr(), self.query_start.data_ptr(), self.context_lens.data_ptr()
+        d.missing, d.free_left, d.positions = self.missing.data_ptr(), self.free_count.data_ptr(), self.positions.data_ptr()
+        d.slots, d.mask = self.slots.data_ptr(), self.mask.data_ptr() if mask_words else None
+        d.mask_words, d.seqs, d.table_pages, d.page_size, d.tokens = mask_words, seqs, table_pages, page_size, tokens
+        self._desc = bytes(d)
+
+
+def q4_kv_assign(step: KVStep, block_table: torch.Tensor, held: torch.Tensor, past_lens: torch.Tensor,
+                 new_lens: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                 parents: torch.Tensor | None = None, stream=None) -> KVStep:
+    """Write `step`'s tables from the lengths past_lens and new_lens [B]: a page for each place a sequence needs and
+    does not hold (its first held[b] entries of block_table [B, P]), taken from the end of the first free_count[0] of
+    free_pages; a sequence whose pages do not fit gets none, and step.missing says how many it lacks.  parents [T]:
+    the tree of each sequence's new tokens (a parent's index among them, -1 for none): positions are depths then, and
+    the masks the ancestors; without it each token follows the one before.  All int32 on the GPU.  held, past_lens and
+    free_count must not be step's own tensors; block_table may be."""
+    on = _on(step.gpu, stream)
+    if on is not None:
+        with on:
+            return q4_kv_assign(step, block_table, held, past_lens, new_lens, free_pages, free_count, parents)
+    dev = step.gpu
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32:
+        raise TypeError("block_table must be an int32 tensor")
+    if block_table.get_device() != dev:
+        raise ValueError("block_table must be on GPU %d, is on %s" % (dev, block_table.device))
+    if tuple(block_table.shape) != (step.seqs, step.table_pages) or (block_table.stride(1) != 1 and step.table_pages != 1):
+        raise ValueError("block_table must be [%d, %d] with consecutive entries" % (step.seqs, step.table_pages))
+    b, i32 = step.seqs, torch.int32
+    d = StepDesc.from_buffer_copy(step._desc)
+    d.table_in, d.table_in_stride = block_table.data_ptr(), block_table.stride(0)
+    d.held_in, d.past_len = _vector(held, i32, "held", b, dev), _vector(past_lens, i32, "past_lens", b, dev)
+    d.new_len, d.free_pages = _vector(new_lens, i32, "new_lens", b, dev), _vector(free_pages, i32, "free_pages", None, dev)
+    d.free_capacity, d.free_count = free_pages.shape[0], _vector(free_count, i32, "free_count", 1, dev)
+    if parents is not None:
+        d.parents = _vector(parents, i32, "parents", step.tokens, dev)
+    status = (_lib or load_library()).q4_kv_assign(ctypes.byref(d), _current_stream(dev))
+    if status:
+        _check(status)
+    return step
+
+
+def _gain(t, name: str, n: int, gpu: int):
+    if t is None:
+        return None, 0
+    kind = _TYPES.get(getattr(t, "dtype", None))
+    if kind is None:
+        raise TypeError("%s must be a float16, bfloat16 or float32 tensor" % name)
+    return _vector(t, t.dtype, name, n, gpu), kind
+
+
+def q4_norm_rope(x: torch.Tensor, gain: torch.Tensor | None, eps: float = 1e-6, positions: torch.Tensor | None = None,
+                 inv_freq: torch.Tensor | None = None, layout: str = "half", mscale: float = 1.0,
+                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q4_rope behind a norm of each head: x [T, H, D] * gain [D] / sqrt(mean(x^2) + eps) (gain None: ones; float16,
+    bfloat16 or float32), then turned as by q4_rope; without inv_freq the norm alone.  Statistics and rotation in 32
+    bits, rounded once.  out: like x in shape, of any of the types, and may be x itself.  No tokens: nothing to do."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be on a GPU")
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return q4_norm_rope(x, gain, eps, positions, inv_freq, layout, mscale, out)
+    hx = _heads(x, "x", dev)
+    t, h, d = x.shape
+    if out is None:
+        out = x.new_empty((t, h, d))
+    elif out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    ho = _heads(out, "out", dev)
+    gp, gk = _gain(gain, "gain", d, dev)
+    r, freq, pos = 0, None, None
+    if inv_freq is not None:
+        freq, r = _vector(inv_freq, torch.float64, "inv_freq", None, dev), inv_freq.shape[0]
+    if positions is not None:
+        pos = _vector(positions, torch.int32, "positions", t, dev)
+    elif r:
+        raise ValueError("inv_freq without positions")
+    kind = _layout(layout)
+    if t == 0:
+        return out
+    status = (_lib or load_library()).q4_norm_rope(
+        ctypes.byref(hx), ctypes.byref(ho), gp, gk, eps, pos, freq if r else None, t, h, d, 2 * r, kind, mscale, _current_stream(dev))
+    if status:
+        _check(status)
+    return out
+
+
+def q4_kv_append_norm(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
+                      k_gain: torch.Tensor | None = None, q_gain: torch.Tensor | None = None, eps: float = 1e-6,
+                      inv_freq: torch.Tensor | None = None, layout: str = "half", mscale: float = 1.0,
+                      positions: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None):
+    """q4_kv_append with the norm of q4_norm_rope on the heads of k (and of q) before they turn; k_gain and q_gain [D],
+    both of one type, None: ones.  positions (int32 [T]) give the angles, as the depths of a tree's tokens do
+    (KVStep.positions); the places in the cache are the batch's."""
+    on = _on(cache.gpu, stream)
+    if on is not None:
+        with on:
+            return q4_kv_append_norm(cache, batch, k, v, q, k_gain, q_gain, eps, inv_freq, layout, mscale, positions, q_out)
+    _same_device(cache, batch)
+    dev = cache.gpu
+    hk, hv = _heads(k, "k", dev), _heads(v, "v", dev)
+    t = k.shape[0]
+    if k.shape != v.shape or k.shape[1] != cache.kv_heads or k.shape[2] != cache.head_dim:
+        raise ValueError("k and v must be [T, %d, %d]" % (cache.kv_heads, cache.head_dim))
+    rq = ro = None
+    heads = 0
+    if q is not None:
+        hq = _heads(q, "q", dev)
+        heads = q.shape[1]
+        if q.shape[0] != t or q.shape[2] != cache.head_dim:
+            raise ValueError("q must be [T=%d, heads, %d]" % (t, cache.head_dim))
+        if q_out is None:
+            q_out = torch.empty((t, heads, cache.head_dim), dtype=cache.dtype, device=cache.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        ho = _heads(q_out, "q_out", dev)
+        rq, ro = ctypes.byref(hq), ctypes.byref(ho)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    (gq, kind_q), (gk, kind_k) = _gain(q_gain, "q_gain", cache.head_dim, dev), _gain(k_gain, "k_gain", cache.head_dim, dev)
+    if q_gain is not None and k_gain is not None and kind_q != kind_k:
+        raise TypeError("q_gain and k_gain must have one type")
+    r, freq = 0, None
+    if inv_freq is not None:
+        freq = _vector(inv_freq, torch.float64, "inv_freq", None, dev)
+        r = inv_freq.shape[0]
+    pos = None if positions is None else _vector(positions, torch.int32, "positions", t, dev)
+    kind = _layout(layout)
+    if t == 0:
+        return q_out
+    status = (_lib or load_library()).q4_kv_append_norm(
+        cache._ref, batch._ref, ctypes.byref(hk), ctypes.byref(hv), rq, ro, heads, t, gq, gk, kind_q if q_gain is not None else kind_k,
+        eps, pos, freq if r else None, 2 * r, kind, mscale, _current_stream(dev))
+    if status:
+        _check(status)
+    return q_out
+
+
+def _mask(mask: torch.Tensor, rows: int, gpu: int) -> int:
+    """Address of masks int64 [rows, words], side by side."""
+    if not isinstance(mask, torch.Tensor):
+        raise TypeError("mask must be a torch.Tensor")
+    if mask.dtype is not torch.int64:
+        raise TypeError("mask must be int64, got %s" % mask.dtype)
+    if mask.get_device() != gpu:
+        raise ValueError("mask must be on GPU %d, is on %s" % (gpu, mask.device))
+    if mask.dim() != 2 or mask.shape[0] != rows or not mask.is_contiguous():
+        raise ValueError("mask must be contiguous, [%d, words]" % rows)
+    return mask.data_ptr()
+
+
+def attention_tree_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, tokens: int, window: int = 0) -> int:
+    """Bytes of the workspace q4_attention_tree needs for these sizes (0: none)."""
+    if tokens == 0:
+        return 0
+    with torch.cuda.device(cache.device):  # the work is cut for this device
+        n = int(load_library().q4_attention_tree_workspace_bytes(cache._ref, batch._ref, q_heads, tokens, window))
+    if n == 0 and last_error():
+        raise Q4Error(Q4_ERR_INVALID_ARG, last_error())
+    return n
+
+
+def q4_attention_tree(cache: KVCache, batch: KVBatch, q: torch.Tensor, mask: torch.Tensor, scale: float | None = None,
+                      window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q4_attention_paged for drafted trees: each new token sees the cached keys before its sequence's new ones (with
+    window > 0 those from past + depth - window + 1 on, depth: the new tokens it sees beside itself) and the new tokens
+    whose bits its mask has (int64 [T, words], bit j % 64 of word j / 64: the sequence's j-th; KVStep.mask).  Append
+    the new tokens first.  out, lse, workspace as there (attention_tree_workspace_bytes)."""
+    on = _on(cache.gpu, stream)
+    if on is not None:
+        with on:
+            return q4_attention_tree(cache, batch, q, mask, scale, window, out, lse, workspace)
+    _same_device(cache, batch)
+    dev = cache.gpu
+    hq = _heads(q, "q", dev)
+    t, h, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError("q must be [T, heads, %d]" % cache.head_dim)
+    mp = _mask(mask, t, dev)
+    if out is None:
+        out = q.new_empty((t, h, d))
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ho = _heads(out, "out", dev)
+    lp = None
+    if lse is not None:
+        lp = _ptr(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (t, h) or lse.get_device() != dev:
+            raise ValueError("lse must be float32 [T, heads] on %s" % cache.device)
+    if t == 0:
+        return out
+    lib = _lib or load_library()
+    wp, wb = None, 0
+    if workspace is None:
+        wb = lib.q4_attention_tree_workspace_bytes(cache._ref, batch._ref, h, t, window)
+        if wb:
+            workspace = torch.empty(wb, dtype=torch.uint8, device=cache.device)
+            wp = workspace.data_ptr()
+    else:
+        wp, wb = _vector(workspace, torch.uint8, "workspace", None, dev), workspace.shape[0]
+    status = lib.q4_attention_tree(cache._ref, batch._ref, ctypes.byref(hq), ctypes.byref(ho), mp, mask.shape[1], lp, h, t,
+                                   scale if scale is not None else d ** -0.5, window, wp, wb, _current_stream(dev))
+    if status:
+        _check(status)
+    return out
+
+
+class LogitRules:
+    """What q4_logits_argmax does to a step's logits; every part may be left out.  Tensors on the GPU, int32 unless
+    noted, which the kernel reads when it runs: their contents may change between calls and replays of a graph.
+
+      query_start [B + 1]      rows of each sequence; left out: row t is sequence t of `seqs` (any tensor by sequence
+                               says how many)
+      history [B, L], history_lens [B], prompt_lens [B]
+                               the tokens behind a sequence, the first prompt_lens of them its prompt, the others its answer
+      draft [T], mask [T, words] (int64)
+                               drafted tokens: each row's answer goes on with those of its sequence that its mask names
+                               (KVStep.mask); without mask with those up to its own
+      repetition, presence, frequency [B], float32
+                               logits of tokens seen are divided (above 0) or multiplied by repetition; those of the
+                               answer's tokens lose presence, and frequency for each time
+      bias_start [B + 1], bias_tokens [N], bias_values [N] (float32)
+                               added to the logits of these tokens; of equal tokens the last counts
+      allowed [R, ceil(V / 32)], allowed_rows [T]
+                               bit v % 32 of word v / 32: v may be picked, by row of logits or by the row that allowed_rows
+                               names (-1: all may)"""
+
+    def __init__(self, query_start=None, history=None, history_lens=None, prompt_lens=None, draft=None, mask=None,
+                 repetition=None, presence=None, frequency=None, bias_start=None, bias_tokens=None, bias_values=None,
+                 allowed=None, allowed_rows=None, seqs: int | None = None):
+        i32, f32 = torch.int32, torch.float32
+        named = dict(query_start=query_start, history=history, history_lens=history_lens, prompt_lens=prompt_lens, draft=draft,
+                     mask=mask, repetition=repetition, presence=presence, frequency=frequency, bias_start=bias_start,
+                     bias_tokens=bias_tokens, bias_values=bias_values, allowed=allowed, allowed_rows=allowed_rows)
+        given = [t for t in named.values() if t is not None]
+        for name, t in named.items():
+            if t is not None and not isinstance(t, torch.Tensor):
+                raise TypeError("%s must be a torch.Tensor" % name)
+        if given and given[0].get_device() < 0:
+            raise ValueError("the rules must be on a GPU")
+        self.gpu = dev = given[0].get_device() if given else None
+        self._keep = given
+        d = self.desc = RulesDesc()
+        sizes = [t.shape[0] - n for t, n in ((query_start, 1), (history, 0), (repetition, 0), (presence, 0), (frequency, 0),
+                                             (bias_start, 1)) if t is not None]
+        b = seqs if seqs is not None else sizes[0] if sizes else 0
+        self.seqs = b
+
+        def vector(t, dtype, name, n):
+            return None if t is None else _vector(t, dtype, name, n, dev)
+
+        def table(t, name, dtype=i32):
+            if t.dtype is not dtype:
+                raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+            if t.get_device() != dev:
+                raise ValueError("%s must be on GPU %d, is on %s" % (name, dev, t.device))
+            if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+                raise ValueError("%s must have two dimensions with consecutive entries" % name)
+            return t.data_ptr()
+
+        if (history is None) != (history_lens is None) or (prompt_lens is not None and history is None):
+            raise ValueError("history goes with history_lens, prompt_lens with both")
+        if mask is not None and draft is None:
+            raise ValueError("a mask without draft")
+        if len({bias_start is None, bias_tokens is None, bias_values is None}) > 1:
+            raise ValueError("bias_start, bias_tokens and bias_values go together")
+        if allowed_rows is not None and allowed is None:
+            raise ValueError("allowed_rows without allowed")
+        d.query_start = vector(query_start, i32, "query_start", b + 1)
+        if history is not None:
+            d.history, d.history_stride, d.history_tokens = table(history, "history"), history.stride(0), history.shape[1]
+            if history.shape[0] != b:
+                raise ValueError("history must have %d rows" % b)
+        d.history_len, d.prompt_len = vector(history_lens, i32, "history_lens", b), vector(prompt_lens, i32, "prompt_lens", b)
+        self.rows = None  # of the tensors by row of logits
+        if draft is not None:
+            d.draft, self.rows = vector(draft, i32, "draft", None), draft.shape[0]
+        if mask is not None:
+            d.mask, d.mask_words = _mask(mask, self.rows, dev), mask.shape[1]
+        d.repetition, d.presence, d.frequency = (vector(t, f32, n, b) for t, n in (
+            (repetition, "repetition"), (presence, "presence"), (frequency, "frequency")))
+        if bias_start is not None:
+            d.bias_start, d.biases = vector(bias_start, i32, "bias_start", b + 1), bias_tokens.shape[0]
+            d.bias_tokens, d.bias_values = vector(bias_tokens, i32, "bias_tokens", None), vector(bias_values, f32, "bias_values", d.biases)
+        self.words = None
+        if allowed is not None:
+            d.allowed, d.allowed_stride, d.allowed_rows = table(allowed, "allowed"), allowed.stride(0), allowed.shape[0]
+            self.words = allowed.shape[1]
+        if allowed_rows is not None:
+            if self.rows is None:
+                self.rows = allowed_rows.shape[0]
+            d.allowed_row = vector(allowed_rows, i32, "allowed_rows", self.rows)
+        d.seqs = b
+        self._ref = ctypes.byref(d)
+
+
+def logits_argmax_workspace_bytes(rows: int, vocab: int) -> int:
+    """Bytes of the workspace q4_logits_argmax needs (0: none)."""
+    return int(load_library().q4_logits_argmax_workspace_bytes(rows, vocab))
+
+
+def q4_logits_argmax(logits: torch.Tensor, rules: LogitRules | None = None, out: torch.Tensor | None = None,
+                     tokens: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The greedy pick (int32 [T]) of logits [T, V] (float32, float16 or bfloat16, rows may lie apart) under `rules`:
+    the lowest index of the largest, -1 for a row in which nothing above -infinity is left.  out (float32 [T, V], may
+    be the logits themselves) receives the logits under the rules; workspace (uint8) at least
+    logits_argmax_workspace_bytes.  No rows: nothing to do."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    dev = logits.get_device()
+    if dev < 0:
+        raise ValueError("logits must be on a GPU")
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return q4_logits_argmax(logits, rules, out, tokens, workspace)
+    kind = _TYPES.get(logits.dtype)
+    if kind is None:
+        raise TypeError("logits must be float16, bfloat16 or float32, got %s" % logits.dtype)
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] != 1):
+        raise ValueError("logits must be [rows, vocabulary] with consecutive entries")
+    t, v = logits.shape
+    rp = None
+    if rules is not None:
+        if rules.gpu is not None and rules.gpu != dev:
+            raise ValueError("the rules are on GPU %d, the logits on %s" % (rules.gpu, logits.device))
+        if rules.rows is not None and rules.rows != t:
+            raise ValueError("draft and allowed_rows must have %d rows" % t)
+        if rules.words is not None and rules.words != (v + 31) // 32:
+            raise ValueError("allowed must have %d words a row" % ((v + 31) // 32))
+        if rules.desc.seqs:
+            rp = rules._ref
+        elif rules.gpu is not None:  # nothing by sequence: as many as there are rows
+            d = RulesDesc.from_buffer_copy(rules.desc)
+            d.seqs = max(t, 1)
+            rp = ctypes.byref(d)
+    op, os_ = None, 0
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.dtype is not torch.float32:
+            raise TypeError("out must be a float32 tensor")
+        if out.shape != logits.shape or out.get_device() != dev or (out.stride(1) != 1 and v != 1):
+            raise ValueError("out must be [%d, %d] on GPU %d with consecutive entries" % (t, v, dev))
+        op, os_ = out.data_ptr(), out.stride(0)
+    if tokens is None:
+        tokens = torch.empty(t, dtype=torch.int32, device=logits.device)
+    tp = _vector(tokens, torch.int32, "tokens", t, dev)
+    if t == 0:
+        return tokens
+    lib = _lib or load_library()
+    wp, wb = None, 0
+    if workspace is None:
+        wb = lib.q4_logits_argmax_workspace_bytes(t, v)
+        if wb:
+            workspace = torch.empty(wb, dtype=torch.uint8, device=logits.device)
+            wp = workspace.data_ptr()
+    else:
+        wp, wb = _vector(workspace, torch.uint8, "workspace", None, dev), workspace.shape[0]
+    status = lib.q4_logits_argmax(logits.data_ptr(), kind, logits.stride(0), t, v, rp, op, os_, tp, wp, wb, _current_stream(dev))
+    if status:
+        _check(status)
+    return tokens
+
+
+def q4_tree_accept(batch: KVBatch, choice: torch.Tensor, draft: torch.Tensor, parents: torch.Tensor | None = None,
+                   history: torch.Tensor | None = None, out=None, stream=None):
+    """(accepted [B], next_tokens [B], path [T], lens [B]), int32, of the trunk's choice behind each drafted token and
+    the tokens themselves (int32 [T]): from each sequence's first new token the lowest child (parents as in
+    q4_kv_assign; None: a chain) drafted as what was chosen, and so on.  accepted counts the path's tokens, the first
+    included; next_tokens is the choice behind its last; path has their indices in the sequence's first rows, then -1;
+    lens the context with them alone.  history (int32 [B, L]) receives the path's tokens at the places they have.
+    out: the four tensors to write.  Rows of no sequence are left as they are (in a new path: -1)."""
+    on = _on(batch.gpu, stream)
+    if on is not None:
+        with on:
+            return q4_tree_accept(batch, choice, draft, parents, history, out)
+    dev, b, i32 = batch.gpu, batch.seqs, torch.int32
+    cp = _vector(choice, i32, "choice", None, dev)
+    t = choice.shape[0]
+    dp = _vector(draft, i32, "draft", t, dev)
+    pp = None if parents is None else _vector(parents, i32, "parents", t, dev)
+    hp, hs, hn = None, 0, 0
+    if history is not None:
+        if not isinstance(history, torch.Tensor) or history.dtype is not i32:
+            raise TypeError("history must be an int32 tensor")
+        if history.dim() != 2 or history.shape[0] != b or history.get_device() != dev or (history.stride(1) != 1 and history.shape[1] != 1):
+            raise ValueError("history must be [%d, entries] on GPU %d with consecutive entries" % (b, dev))
+        hp, hs, hn = history.data_ptr(), history.stride(0), history.shape[1]
+    if out is None:
+        rest = torch.empty((3, b), dtype=i32, device=batch.device)
+        out = rest[0], rest[1], torch.full((t,), -1, dtype=i32, device=batch.device), rest[2]
+    accepted, following, path, lens = out
+    ap, np_, lp = _vector(accepted, i32, "accepted", b, dev), _vector(following, i32, "next_tokens", b, dev), _vector(lens, i32, "lens", b, dev)
+    rp = _vector(path, i32, "path", t, dev)
+    if t == 0:
+        raise ValueError("no tokens")
+    query_start, context_lens = batch._keep[1:]
+    status = (_lib or load_library()).q4_tree_accept(
+        query_start.data_ptr(), context_lens.data_ptr(), b, cp, dp, pp, t, ap, np_, rp, lp, hp, hs, hn, _current_stream(dev))
+    if status:
+        _check(status)
+    return out
+
+
+class KVLayers:
+    """The caches of a model's layers, alike in sizes and strides, for q4_kv_move."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not self.caches:
+            raise ValueError("no caches")
+        self.gpu, self.device = self.caches[0].gpu, self.caches[0].device
+        if any(c.gpu != self.gpu for c in self.caches):
+            raise ValueError("the caches must be on one GPU")
+        self.desc = (CacheDesc * len(self.caches))(*(c.desc for c in self.caches))
+
+
+def q4_kv_move(layers, batch: KVBatch, path: torch.Tensor, accepted: torch.Tensor, stream=None) -> None:
+    """Move the keys and values of each sequence's path (path [T], accepted [B], int32, of q4_tree_accept) to the places
+    behind each other that its tokens have, in the caches of all layers (a KVLayers, or one KVCache)."""
+    if isinstance(layers, KVCache):
+        layers = KVLayers([layers])
+    on = _on(layers.gpu, stream)
+    if on is not None:
+        with on:
+            return q4_kv_move(layers, batch, path, accepted)
+    _same_device(layers, batch)
+    dev = layers.gpu
+    pp, ap = _vector(path, torch.int32, "path", None, dev), _vector(accepted, torch.int32, "accepted", batch.seqs, dev)
+    if path.shape[0] == 0:
+        return
+    status = (_lib or load_library()).q4_kv_move(layers.desc, len(layers.caches), batch._ref, pp, ap, path.shape[0], _current_stream(dev))
+    if status:
+        _check(status)
+
+
 # Short names.
 gemv = q4_0_gemv
 gemm_smallm = q4_0_gemm_smallm
@@ -892,3 +1409,10 @@ gemm_prefill = q4_0_gemm_prefill
 rope = q4_rope
 kv_append = q4_kv_append
 attention_paged = q4_attention_paged
+kv_assign = q4_kv_assign
+norm_rope = q4_norm_rope
+kv_append_norm = q4_kv_append_norm
+attention_tree = q4_attention_tree
+logits_argmax = q4_logits_argmax
+tree_accept = q4_tree_accept
+kv_move = q4_kv_move

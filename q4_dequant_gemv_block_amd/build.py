@@ -4,6 +4,7 @@
 
 Every call compiles: a stale library never survives a source change.
 """
+import concurrent.futures
 import os
 import re
 import subprocess
@@ -16,8 +17,8 @@ LIB = os.path.join(HERE, "libq4gemv.so")
 # the read-bandwidth probe the benchmark quotes the GEMV against (not part of the GEMV library)
 STREAM_SRC = "stream.hip"
 STREAM_LIB = os.path.join(HERE, "libq4stream.so")
-SOURCES = ["gemv.hip", "smallm.hip", "prefill.hip", "verify.hip", "q8.hip", "rope.hip", "attention.hip", "attn_tile.hip", "api.cpp",
-           "kv_api.cpp"]
+SOURCES = ["gemv.hip", "smallm.hip", "prefill.hip", "verify.hip", "q8.hip", "rope.hip", "attention.hip", "attn_tile.hip",
+           "norm_rope.hip", "attn_tree.hip", "attn_tree_tile.hip", "logits.hip", "step.hip", "api.cpp", "kv_api.cpp", "step_api.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [
@@ -74,30 +75,35 @@ def hipcc():
     return "hipcc"
 
 
+def compile_source(src: str, build_dir: str, defines, verbose: bool) -> str:
+    """Compile one source; the object's path."""
+    obj = os.path.join(build_dir, src + ".o")
+    cmd = [hipcc()] + FLAGS + ["-D" + d for d in defines] + ["-c", os.path.join(CSRC, src), "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, stderr=subprocess.PIPE, text=True)
+    diag = "\n".join(l for l in r.stderr.splitlines()
+                     if "kernel-resource-usage" not in l and "packed-fp32-ops" not in l
+                     and not l.startswith("In file included from") and not re.match(r"^\s*\d*\s*\|", l))
+    if diag.strip():
+        print(diag, file=sys.stderr, flush=True)
+    if r.returncode != 0:
+        raise subprocess.CalledProcessError(r.returncode, cmd)
+    if src.endswith(".hip"):
+        for k in check_resources(r.stderr, src):
+            if verbose:
+                print("  %-100s vgpr %s agpr %s sgpr-spill %s" % (k["name"][:100], k.get("VGPRs"), k.get("AGPRs"),
+                                                                 k.get("SGPRs Spill")), flush=True)
+    return obj
+
+
 def build(verbose: bool = False, defines=()) -> str:
-    """Compile every source and link libq4gemv.so; `defines` are extra -D flags."""
-    objs = []
+    """Compile every source, a few at a time, and link libq4gemv.so; `defines` are extra -D flags."""
     build_dir = os.path.join(HERE, "_build")
     os.makedirs(build_dir, exist_ok=True)
-    for src in SOURCES:
-        obj = os.path.join(build_dir, src + ".o")
-        cmd = [hipcc()] + FLAGS + ["-D" + d for d in defines] + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, stderr=subprocess.PIPE, text=True)
-        diag = "\n".join(l for l in r.stderr.splitlines()
-                         if "kernel-resource-usage" not in l and "packed-fp32-ops" not in l
-                         and not re.match(r"^\s*\d*\s*\|", l))
-        if diag.strip():
-            print(diag, file=sys.stderr, flush=True)
-        if r.returncode != 0:
-            raise subprocess.CalledProcessError(r.returncode, cmd)
-        if src.endswith(".hip"):
-            for k in check_resources(r.stderr, src):
-                if verbose:
-                    print("  %-100s vgpr %s agpr %s sgpr-spill %s" % (k["name"][:100], k.get("VGPRs"), k.get("AGPRs"),
-                                                                     k.get("SGPRs Spill")), flush=True)
-        objs.append(obj)
+    workers = max(1, min(8, len(os.sched_getaffinity(0))))
+    with concurrent.futures.ThreadPoolExecutor(workers) as pool:
+        objs = list(pool.map(lambda src: compile_source(src, build_dir, defines, verbose), SOURCES))
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:

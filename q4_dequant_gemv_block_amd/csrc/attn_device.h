@@ -20,6 +20,9 @@ struct Cut;
 // The kernel for many query rows of a sequence (attn_tile.hip).
 template <typename T, int D>
 hipError_t launch_attn_tile(const AttnArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s);
+// The same over trees of new tokens (attn_tree_tile.hip).
+template <typename T, int D>
+hipError_t launch_attn_tile(const TreeArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s);
 
 // A row's weights are 2^(score - m).  m is set to kLift below the largest score, and
 // set anew when a score exceeds it by kRaise (each 2^8 of scores at the soonest).
@@ -101,11 +104,14 @@ struct Seq {
 };
 
 // Items of a kv head and units of an item (the most that any of the sequence's
-// items has: a unit behind an item's last visible key holds no work).
+// items has: a unit behind an item's last visible key holds no work).  TREE, here and
+// below: the new tokens' masks say which of them a row sees, so each row may see the
+// last key, and its window ends anywhere among them.
+template <bool TREE>
 __device__ __forceinline__ void cut_sequence(const Cut& c, Seq* s) {
     int span = max(0, min(s->ctx, c.capacity));
     if (c.window) {
-        const int64_t most = (int64_t)c.window + (int)c.group.div((1u << c.rows_log2) - 1) + 1 + c.step;
+        const int64_t most = (int64_t)c.window + (TREE ? s->n : (int)c.group.div((1u << c.rows_log2) - 1)) + 1 + c.step;
         span = (int)min((int64_t)span, most);
     }
     s->tiles = (int)(((int64_t)s->n * c.group.d + (1 << c.rows_log2) - 1) >> c.rows_log2);
@@ -146,10 +152,11 @@ __device__ __forceinline__ void place_item(const Cut& c, const Seq& seq, uint32_
 }
 
 // Positions of an item's rows and the keys of its units [u0, u1).
+template <bool TREE>
 __device__ __forceinline__ void place_keys(const Cut& c, const Seq& seq, Item* x) {
     x->past = seq.ctx - seq.n;
-    x->p_first = x->past + (int)c.group.div(x->row0);
-    x->p_last = x->past + (int)c.group.div(x->row0 + x->rows - 1);
+    x->p_first = x->past + (TREE ? 0 : (int)c.group.div(x->row0));
+    x->p_last = TREE ? seq.ctx - 1 : x->past + (int)c.group.div(x->row0 + x->rows - 1);
     const int keys = max(0, min(min(seq.ctx, c.capacity), x->p_last + 1));
     const int start = c.window ? (max(0, x->p_first - c.window + 1) & -c.step) : 0;
     x->k_lo = (int)min((int64_t)keys, start + ((int64_t)x->u0 << c.unit_log2));
@@ -170,7 +177,8 @@ __device__ __forceinline__ void place_keys(const Cut& c, const Seq& seq, Item* x
 // among them: in their midst they would hold up workgroups with work (40 x 2 tokens
 // of 1500 keys, 8 heads a kv head: 15.6 us, with an empty place behind each item 23.7).
 // item_bound() counts them.
-struct Places {
+template <bool TREE>
+struct PlacesOf {
     // The kernel's loop over items is left after the first one and holds nothing for
     // others: no scalar registers are spilled for them (50 to 110 are for ranges).
     static constexpr bool once = true;
@@ -184,7 +192,7 @@ struct Places {
             const int lane = threadIdx.x & 63;
             Seq s = {};
             if (lane < batch.seqs) read_sequence(c, batch, lane, &s);
-            cut_sequence(c, &s);
+            cut_sequence<TREE>(c, &s);
             uint32_t sum = s.tiles;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
@@ -198,7 +206,7 @@ struct Places {
             seq.row0 = __builtin_amdgcn_readlane(s.row0, l);
             seq.n = __builtin_amdgcn_readlane(s.n, l);
             seq.ctx = __builtin_amdgcn_readlane(s.ctx, l);
-            cut_sequence(c, &seq);
+            cut_sequence<TREE>(c, &seq);
             up = x - (uint32_t)__builtin_amdgcn_readlane((int)(sum - s.tiles), l);
         } else {
             auto start_of = [&](int b) { return (int64_t)max(batch.query_start[b], 0); };
@@ -218,7 +226,7 @@ struct Places {
             }
             if (b < 0) return false;
             read_sequence(c, batch, b, &seq);
-            cut_sequence(c, &seq);
+            cut_sequence<TREE>(c, &seq);
         }
         *item = up * c.kv_heads.d + (place - x * c.kv_heads.d);
         return up < (uint32_t)seq.tiles;
@@ -230,7 +238,7 @@ struct Places {
         x->u0 = 0;
         x->u1 = seq.units;
         place_item(c, seq, item, x);
-        place_keys(c, seq, x);
+        place_keys<TREE>(c, seq, x);
         return true;
     }
     __device__ __forceinline__ bool next(const Cut&, const BatchArg&, Item*) { return true; }
@@ -241,7 +249,8 @@ struct Places {
 // 64 sequences (read once where there are no more), a wave's scan finds the
 // sequence of a unit.  A workgroup walks through the sequences twice, but there
 // are never more workgroups than the machine holds.
-struct Work {
+template <bool TREE>
+struct WorkOf {
     static constexpr bool once = false;
     uint32_t total;  // units of all sequences
     uint32_t begin;  // first unit of seq
@@ -257,7 +266,7 @@ struct Work {
         base = b0;
         Seq s = {};
         if (b0 + lane < batch.seqs) read_sequence(c, batch, b0 + lane, &s);
-        cut_sequence(c, &s);
+        cut_sequence<TREE>(c, &s);
         l_row0 = s.row0;
         l_n = s.n;
         l_ctx = s.ctx;
@@ -274,7 +283,7 @@ struct Work {
         seq.row0 = __builtin_amdgcn_readlane(l_row0, b - base);
         seq.n = __builtin_amdgcn_readlane(l_n, b - base);
         seq.ctx = __builtin_amdgcn_readlane(l_ctx, b - base);
-        cut_sequence(c, &seq);
+        cut_sequence<TREE>(c, &seq);
     }
     __device__ __forceinline__ void sum(const Cut& c, const BatchArg& batch) {
         total = 0;
@@ -321,11 +330,43 @@ struct Work {
         x->u1 = (int)min((uint32_t)seq.units, x->u0 + (hi - lo));
         lo += x->u1 - x->u0;
         place_item(c, seq, item, x);
-        place_keys(c, seq, x);
+        place_keys<TREE>(c, seq, x);
         return true;
     }
     __device__ __forceinline__ bool whole(const Item& x) const { return x.u0 == 0 && x.u1 == seq.units; }
 };
+
+typedef PlacesOf<false> Places;
+typedef WorkOf<false> Work;
+
+// A row's mask of new tokens (TREE): bit j says whether it sees the sequence's j-th.
+// How many others of them it sees, for windows.
+__device__ __forceinline__ int tree_depth(const TreeArgs& a, const Seq& seq, int i) {
+    int depth = 0;
+    if (a.window) {
+        const uint64_t* words = a.mask + (int64_t)(seq.row0 + i) * a.mask_words;
+        for (int w = 0; w < a.mask_words && 64 * w < seq.n; ++w) {
+            const int left = seq.n - 64 * w;
+            depth += __popcll(words[w] & (left >= 64 ? ~uint64_t(0) : (uint64_t(1) << left) - 1));
+        }
+        if (i < 64 * a.mask_words) depth -= (int)((words[i >> 6] >> (i & 63)) & 1);
+    }
+    return depth;
+}
+// Which of the keys t .. t + 63 it sees, those behind the context aside: in the cache
+// from the window on, then by the mask.
+__device__ __forceinline__ uint64_t tree_seen(const TreeArgs& a, const Seq& seq, int i, int depth, int t, int past) {
+    const uint64_t* words = a.mask + (int64_t)(seq.row0 + i) * a.mask_words;
+    const int at = t - past;
+    if (at >= 0) {
+        const int w = at >> 6, s = at & 63;
+        const uint64_t low = w < a.mask_words ? words[w] : 0, high = w + 1 < a.mask_words ? words[w + 1] : 0;
+        return (low >> s) | (high << 1 << (63 - s));
+    }
+    const uint64_t cached = at <= -64 ? ~uint64_t(0) : (uint64_t(1) << -at) - 1;
+    const int from = a.window ? past + depth - a.window + 1 - t : 0;
+    return (at <= -64 ? 0 : words[0] << -at) | (cached & (from <= 0 ? ~uint64_t(0) : from >= 64 ? 0 : ~uint64_t(0) << from));
+}
 
 // Parts in the workspace: every workgroup has at most two, one that begins its
 // range (slot 0) and one whose item begins inside it and ends behind it (slot 1).

@@ -39,7 +39,7 @@ inline int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int
 // batches of 16 to 200 sequences, half of them with lengths from 1/16 of the longest
 // up, which the host cannot see, 80, and 64 % behind at most (many short items of a
 // range, each of which starts with nothing on its way).
-inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context) {
+inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context, bool tree = false) {
     const int64_t group = q_heads / c.kv_heads, capacity = (int64_t)b.table_pages * c.page_size.d;
     const int64_t longest = max_query > 0 ? std::min<int64_t>(max_query, tokens) : tokens;  // new tokens of a sequence
     const int64_t most = longest * group;
@@ -56,7 +56,7 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
         s.most_rows = (int)std::min<int64_t>(rows, most);
         const int slots = rows <= 32 || c.head_dim > 128 ? cus : 2 * cus;
         // keys of an item, the part of them that its sequence's items see on average, and all items
-        const int64_t keys = window ? std::min<int64_t>(context, (int64_t)window + (rows - 1) / group + 2) : context;
+        const int64_t keys = window ? std::min<int64_t>(context, (int64_t)window + (tree ? longest : (rows - 1) / group) + 2) : context;
         const int64_t past = std::max<int64_t>(context - longest, 0);
         const double inside = (double)std::min(std::max<int64_t>(keys - past, 0), longest);  // tokens that see less
         const double seen = std::min(1.0, (inside * past + inside * (inside + 1) / 2 + (longest - inside) * keys) / ((double)longest * keys));

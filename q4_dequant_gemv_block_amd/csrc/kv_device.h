@@ -53,6 +53,19 @@ __device__ __forceinline__ void store_elems(char* p, const float (&x)[V]) {
     }
 }
 
+// Cosine and sine of position * inv_freq, times mscale: the angle as turns in
+// binary64, reduced to [-1/2, 1/2] there, and what its rounding to binary32 leaves
+// out added to first order.
+__device__ __forceinline__ f2 turn_of(int position, double inv_freq, float mscale) {
+    double turns = (double)position * inv_freq * 0.15915494309189533577;  // / (2 pi)
+    turns -= __builtin_rint(turns);
+    const float near = (float)turns;
+    const float rest = 6.2831853071795864769f * (float)(turns - near);  // below 2^-22
+    float s, c;
+    sincospif(2.0f * near, &s, &c);
+    return f2{(c - rest * s) * mscale, (s + rest * c) * mscale};
+}
+
 // The last j in [0, n) for which low(j) holds, where it holds for the first ones and
 // not for the others; -1 if for none.  Called by whole waves with n uniform: 64
 // places a step, counted with a ballot, so 64^k sequences take k loads one after

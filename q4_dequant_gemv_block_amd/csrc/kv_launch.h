@@ -65,6 +65,33 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a, int in_type, int out_type, int layout, hipStream_t s);
 
+// The same with a norm of each turned head first.
+struct NormRopeArgs {
+    RopeArgs rope;
+    const char* gain[2];  // of the queries (or x), of the keys; null: ones
+    int gain_type;
+    float eps;
+};
+hipError_t launch_norm_rope(const NormRopeArgs& a, int in_type, int out_type, int layout, hipStream_t s);
+
+// Whether every head can be read and written in 16-byte pieces of 8 elements that
+// hold whole pairs, or whole runs of them (half layout).
+inline bool rope_vectors(const RopeArgs& a, int in_bytes, int out_bytes, bool half) {
+    auto heads_aligned = [](const HeadsArg& h, int bytes) {
+        return ((uintptr_t)h.data & 15) == 0 && h.token_stride * bytes % 16 == 0 && h.head_stride * bytes % 16 == 0;
+    };
+    bool vec = a.head_dim % 8 == 0 && a.rot_dim % (half ? 16 : 8) == 0;
+    for (int i = 0; i < 3; ++i)
+        if (a.heads[i]) vec = vec && heads_aligned(a.in[i], in_bytes);
+    if (a.heads[0]) vec = vec && heads_aligned(a.out, out_bytes);
+    if (a.paged) {
+        const CacheArg& c = a.cache;
+        vec = vec && (((uintptr_t)c.k | (uintptr_t)c.v) & 15) == 0;
+        vec = vec && (c.k_page | c.k_head | c.k_slot | c.v_page | c.v_head | c.v_slot) % 8 == 0;
+    }
+    return vec;
+}
+
 struct AttnArgs {
     HeadsArg q, out;
     float* lse;
@@ -75,6 +102,11 @@ struct AttnArgs {
     float scale_log2;       // scale * log2(e)
     int window;             // 0: none
     void* workspace;
+};
+// The same where each new token sees those of its sequence that its mask names.
+struct TreeArgs : AttnArgs {
+    const uint64_t* mask;  // [tokens][mask_words]
+    int mask_words;
 };
 // How a call is cut: a rule on sizes alone, the same for the workspace's size
 // and the launch.
@@ -90,7 +122,8 @@ struct AttnShape {
     size_t bytes;  // workspace, 0 where every item is taken whole
 };
 bool attn_head_dim_ok(int head_dim);
-AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context);
+AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context, bool tree = false);
+hipError_t launch_attention_tree(const TreeArgs& a, const AttnShape& shape, int type, hipStream_t s);
 hipError_t launch_attention(const AttnArgs& a, const AttnShape& shape, int type, hipStream_t s);
 
 }  // namespace q4

@@ -78,13 +78,7 @@ __global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs a, const RopeU
         if (lane == 0) state[w] = st;
         if (st) {
             for (int i = lane; i < a.rot_dim / 2; i += 64) {
-                double turns = (double)p * a.inv_freq[i] * 0.15915494309189533577;  // / (2 pi)
-                turns -= __builtin_rint(turns);
-                const float near = (float)turns;
-                const float rest = 6.2831853071795864769f * (float)(turns - near);  // below 2^-22
-                float s, c;
-                sincospif(2.0f * near, &s, &c);
-                turn[w][i] = f2{(c - rest * s) * a.mscale, (s + rest * c) * a.mscale};
+                turn[w][i] = turn_of(p, a.inv_freq[i], a.mscale);
             }
         }
     }
@@ -167,10 +161,6 @@ __global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs a, const RopeU
     }
 }
 
-bool heads_aligned(const HeadsArg& h, int bytes) {
-    return ((uintptr_t)h.data & 15) == 0 && h.token_stride * bytes % 16 == 0 && h.head_stride * bytes % 16 == 0;
-}
-
 template <typename IN, typename OUT, bool HALF, int V>
 hipError_t launch(const RopeArgs& a, hipStream_t s) {
     constexpr int W = HALF ? V : (V < 2 ? 2 : V);
@@ -195,16 +185,7 @@ hipError_t launch(const RopeArgs& a, hipStream_t s) {
 
 template <typename IN, typename OUT>
 hipError_t launch_types(const RopeArgs& a, int layout, hipStream_t s) {
-    const bool half = layout == Q4_ROPE_HALF;
-    bool vec = a.head_dim % 8 == 0 && a.rot_dim % (half ? 16 : 8) == 0;
-    for (int i = 0; i < 3; ++i)
-        if (a.heads[i]) vec = vec && heads_aligned(a.in[i], IN::bytes);
-    if (a.heads[0]) vec = vec && heads_aligned(a.out, OUT::bytes);
-    if (a.paged) {
-        const CacheArg& c = a.cache;
-        vec = vec && (((uintptr_t)c.k | (uintptr_t)c.v) & 15) == 0;
-        vec = vec && (c.k_page | c.k_head | c.k_slot | c.v_page | c.v_head | c.v_slot) % 8 == 0;
-    }
+    const bool half = layout == Q4_ROPE_HALF, vec = rope_vectors(a, IN::bytes, OUT::bytes, half);
     if (half) return vec ? launch<IN, OUT, true, 8>(a, s) : launch<IN, OUT, true, 1>(a, s);
     return vec ? launch<IN, OUT, false, 8>(a, s) : launch<IN, OUT, false, 1>(a, s);
 }
