@@ -278,6 +278,11 @@ struct WorkOf {
         }
     }
     __device__ __forceinline__ void pick(const Cut& c, const BatchArg& batch, int b) {
+        if constexpr (TREE) {  // (read again: what the lanes have would be held through the loops)
+            read_sequence(c, batch, b, &seq);
+            cut_sequence<TREE>(c, &seq);
+            return;
+        }
         if (b - base >= 64) load(c, batch, b);
         seq.b = b;
         seq.row0 = __builtin_amdgcn_readlane(l_row0, b - base);

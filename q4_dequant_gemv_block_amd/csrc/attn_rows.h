@@ -373,26 +373,82 @@ __global__ void __launch_bounds__(attn_waves(D) * 64) k_attn(const ARGS a, const
     }
 }
 
+// Item `ordinal` of a call in the order of its units: its sequence, its number there,
+// its first unit, and the units of the whole call; false if there are fewer items.
+template <bool TREE>
+__device__ __forceinline__ bool find_item(const Cut& c, const BatchArg& batch, uint32_t ordinal, Seq* seq, uint32_t* item, uint32_t* first, uint32_t* total) {
+    const int lane = threadIdx.x & 63;
+    uint32_t items = 0;  // of the sequences in front
+    bool found = false;
+    *total = 0;
+    for (int b0 = 0; b0 < batch.seqs; b0 += 64) {
+        Seq s = {};
+        if (b0 + lane < batch.seqs) read_sequence(c, batch, b0 + lane, &s);
+        cut_sequence<TREE>(c, &s);
+        const uint32_t mine = c.kv_heads.d * s.tiles;
+        uint32_t sum = mine, units = mine * s.units;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t x = (uint32_t)__shfl_up((int)sum, o), y = (uint32_t)__shfl_up((int)units, o);
+            if (lane >= o) {
+                sum += x;
+                units += y;
+            }
+        }
+        const uint64_t past = __ballot(items + sum > ordinal);
+        if (past && !found) {
+            found = true;
+            const int l = __builtin_ctzll(past);
+            seq->b = b0 + l;
+            seq->row0 = __builtin_amdgcn_readlane(s.row0, l);
+            seq->n = __builtin_amdgcn_readlane(s.n, l);
+            seq->ctx = __builtin_amdgcn_readlane(s.ctx, l);
+            cut_sequence<TREE>(c, seq);
+            const uint32_t before = (uint32_t)__builtin_amdgcn_readlane((int)(sum - mine), l);
+            *item = ordinal - items - before;
+            *first = *total + (uint32_t)__builtin_amdgcn_readlane((int)(units - mine * s.units), l) + *item * seq->units;
+        }
+        items += (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
+        *total += (uint32_t)__builtin_amdgcn_readlane((int)units, 63);
+    }
+    return found;
+}
+
 // Joins the parts of the items that several ranges share.  Workgroup (w, y)
 // takes the item that begins in range w and does not end there, if there is
 // one, and every gridDim.y-th batch of its rows: one SG-lane group a row where
 // the parts are few, all groups on one row where they are many.
+// Trees: with `by_item` workgroup (i, y) takes item i instead: calls of a few long items with many rows
+// have more ranges than items, and each empty workgroup costs its look at the lengths.
 template <typename T, int D, bool TREE>
-__global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, const Cut cut, uint32_t slots) {
+__global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, const Cut cut, uint32_t slots, int by_item) {
     constexpr int SG = D <= 64 ? 16 : D <= 128 ? 32 : 64;  // lanes of a row
     constexpr int NSG = kThreads / SG;
+    constexpr int AHEAD = TREE ? 8 : 4;                    // parts of a row at once
     __shared__ f4 sh_o[NSG][SG];
     __shared__ float sh_s[NSG];
-    WorkOf<TREE> work;
-    work.sum(cut, a.batch);
-    const uint32_t total = work.total, grid = min(slots, total), w0 = blockIdx.x;
-    if (w0 + 1 >= grid) return;
-    const uint32_t border = range_begin(total, w0 + 1, grid);
-    if (!work.find(cut, a.batch, border)) return;
-    const Seq& seq = work.seq;
-    const uint32_t item = (border - work.begin) / (uint32_t)seq.units;
-    const uint32_t first = work.begin + item * seq.units, last = first + seq.units - 1;
-    if (first == border || first < range_begin(total, w0, grid) || last >= total) return;
+    Seq seq;
+    uint32_t total, grid, w0, item, first, last;
+    if (TREE && by_item) {
+        if (!find_item<TREE>(cut, a.batch, blockIdx.x, &seq, &item, &first, &total)) return;
+        grid = min(slots, total);
+        last = first + seq.units - 1;
+        w0 = (uint32_t)((uint64_t)first * grid / total);  // the range that holds `first`
+        while (range_begin(total, w0 + 1, grid) <= first) ++w0;
+        while (range_begin(total, w0, grid) > first) --w0;
+        if (w0 + 1 >= grid || range_begin(total, w0 + 1, grid) > last) return;
+    } else {
+        WorkOf<TREE> work;
+        work.sum(cut, a.batch);
+        total = work.total, grid = min(slots, total), w0 = blockIdx.x;
+        if (w0 + 1 >= grid) return;
+        const uint32_t border = range_begin(total, w0 + 1, grid);
+        if (!work.find(cut, a.batch, border)) return;
+        seq = work.seq;
+        item = (border - work.begin) / (uint32_t)seq.units;
+        first = work.begin + item * seq.units, last = first + seq.units - 1;
+        if (first == border || first < range_begin(total, w0, grid) || last >= total) return;
+    }
     uint32_t w1 = (uint32_t)((uint64_t)last * grid / total);  // the range that holds `last`
     while (range_begin(total, w1 + 1, grid) <= last) ++w1;
     while (range_begin(total, w1, grid) > last) --w1;
@@ -401,7 +457,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, const 
     const int R = 1 << cut.rows_log2;
     const Parts<D> parts(a.workspace, (int)slots, R);
     const int g = threadIdx.x / SG, lane = threadIdx.x & (SG - 1), d = lane * 4;
-    const bool many = w1 - w0 >= NSG;
+    // (trees have many rows: a group a row up to more parts)
+    const bool many = w1 - w0 >= (TREE ? 8 * NSG : NSG);
     const int stride = many ? 1 : NSG;
     for (int row = blockIdx.y * stride + (many ? 0 : g); row < it.rows; row += gridDim.y * stride) {
         // part of range w: slot 2 w + 1 in the item's first range, else 2 w
@@ -409,23 +466,25 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const AttnArgs a, const 
         const uint32_t from = w0 + (many ? g : 0), by = many ? NSG : 1;
         float top = kNone, sum = 0.0f;
         f4 o = {0, 0, 0, 0};
-        for (uint32_t w = from; w <= w1; w += 4 * by) {
-            f2 ml[4];
-            f4 po[4];
+        for (uint32_t w = from; w <= w1; w += AHEAD * by) {
+            f2 ml[AHEAD];
+            f4 po[AHEAD];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < AHEAD; ++k) {
                 const bool in = w + k * by <= w1;
                 ml[k] = in ? parts.ml[slot_of(w + k * by)] : f2{kNone, 0.0f};
                 po[k] = in && d < D ? *reinterpret_cast<const f4*>(&parts.o[slot_of(w + k * by) * D + d]) : f4{0, 0, 0, 0};
             }
-            const float raised = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+            float raised = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+#pragma unroll
+            for (int k = 4; k < AHEAD; ++k) raised = fmaxf(raised, ml[k].x);
             const float ref = raised == kNone ? 0.0f : raised;
             const float keep = __builtin_amdgcn_exp2f(top - ref);
             sum *= keep;
             o *= keep;
             top = raised;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < AHEAD; ++k) {
                 const float f = __builtin_amdgcn_exp2f(ml[k].x - ref);
                 sum += f * ml[k].y;
                 o += f * po[k];
@@ -507,8 +566,12 @@ hipError_t launch_dim(const ARGS& a, const AttnShape& shape, hipStream_t s) {
         e = launch<T, D, 2>(a, shape, s);
     if (e != hipSuccess || !shape.bytes || shape.grid < 2) return e;
     // Few items have many parts each: a workgroup a row; else one for eight rows.
-    const int by = std::min(16, shape.few ? shape.most_rows : (shape.most_rows + 7) / 8);
-    hipLaunchKernelGGL((k_attn_join<T, D, std::is_same<ARGS, TreeArgs>::value>), dim3((unsigned)shape.grid - 1, by), dim3(kThreads), 0, s, a, make_cut(a, shape), (uint32_t)shape.grid);
+    constexpr bool TREE = std::is_same<ARGS, TreeArgs>::value;
+    const int by = TREE ? (shape.most_rows + 7) / 8 : std::min(16, shape.few ? shape.most_rows : (shape.most_rows + 7) / 8);
+    int per_token;
+    const int64_t items = TREE ? item_bound(a.cache, a.batch, a.q_heads, a.tokens, shape.rows, &per_token) : shape.grid;
+    const bool by_item = items < shape.grid;
+    hipLaunchKernelGGL((k_attn_join<T, D, TREE>), dim3((unsigned)(by_item ? items : shape.grid - 1), by), dim3(kThreads), 0, s, a, make_cut(a, shape), (uint32_t)shape.grid, by_item);
     return hipGetLastError();
 }
 

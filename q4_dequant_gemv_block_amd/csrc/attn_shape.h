@@ -20,6 +20,32 @@ inline int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int
     return c.kv_heads * (*per_token ? tokens * each : by_rows);
 }
 
+// Trees have few rows over long contexts, their tiles wait less (attn_tile.h) and
+// their parts are joined by item, so they have numbers of their own, and more ways:
+// up to 128 rows in items of 32 (many workgroups of little each: 16 tokens of 4 heads
+// a kv head over 515 keys 11.7 us, in one item of 64 rows 14.9), more than 128 of heads
+// of 96 or 128 in items of 256 (8 waves that share the keys' tiles) where the keys and
+// values are more than the last-level cache keeps, so that items of 128 rows would read
+// them twice from HBM (3 sequences of 64 tokens over 32768 keys, 32/8 heads of 128, 141
+// us, with items of 128 161).
+// Fitted to 320 calls; of 648 (2 to 200 tokens of 1 to 96 sequences over up to 40000
+// keys, heads of 64 to 256, with and without windows), each run in every way, what is
+// taken is within 5 % of the best in 587, 1.5 % behind in the mean and 35 % at most (by
+// the numbers for prompts and decode steps 4.6 % in the mean).
+struct TreeCost {
+    double start, each;     // us of an item, of 256 keys (items of 16 and 32 rows) or a tile
+    double late;            // of what the last round lacks
+    double parts, range, traffic;  // the join's launch, units in ranges, the parts' way to memory and back
+};
+inline TreeCost tree_cost(int rows, int head_dim) {
+    const double dim = head_dim / 128.0;
+    if (rows <= 32) return {1.4, (0.213 + 2.18 * dim) * (rows == 32 ? 1.05 : 1.0), 1.24, 10.4, 1.0, 0.71};
+    const double tile = head_dim > 128 ? (rows == 64 ? 1.82 : 2.14)
+                        : rows == 64   ? 0.47 + 0.75 * dim
+                                       : (0.515 + 0.77 * dim) * (rows == 256 ? 0.95 : 1.0);
+    return {0.38, tile, 0.16, 10.1, 1.17, 0.87};
+}
+
 // How a call is cut: the rows of an item, and whether items are taken whole or
 // in parts.  Parts cost a launch that waits for the first one (measured 5 to 7
 // us), their way to memory and back at about 4 TB/s, and in tiles the L2: whole
@@ -54,7 +80,7 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
         s.step = rows <= 32 ? kAttnStep : 64;
         s.unit = 64;
         s.most_rows = (int)std::min<int64_t>(rows, most);
-        const int slots = rows <= 32 || c.head_dim > 128 ? cus : 2 * cus;
+        const int slots = rows <= 32 || rows == 256 || c.head_dim > 128 ? cus : 2 * cus;
         // keys of an item, the part of them that its sequence's items see on average, and all items
         const int64_t keys = window ? std::min<int64_t>(context, (int64_t)window + (tree ? longest : (rows - 1) / group) + 2) : context;
         const int64_t past = std::max<int64_t>(context - longest, 0);
@@ -66,7 +92,14 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
         const double parts = std::min<double>(slots, items * keys / s.unit);
         const double traffic = parts * s.most_rows * c.head_dim * 8 / 4e6;
         double whole, cut;
-        if (rows <= 32) {
+        if (tree) {
+            const TreeCost cost = tree_cost(rows, c.head_dim);
+            const double us = cost.each * (rows <= 32 ? keys / 256.0 : (double)((keys + 63) / 64));
+            whole = rows <= 32 ? cost.start + us * (rounds > 1 ? rounds + cost.late * std::min(1.0, std::ceil(rounds) - rounds) : 1.0)
+                    : items <= cus ? 0.95 * (cost.start + us)  // each on its CU
+                                   : cost.start + us * std::max(1.0, rounds + cost.late * std::min(1.0, std::ceil(rounds) - rounds));
+            cut = cost.parts + cost.range * us * rounds + cost.traffic * traffic;
+        } else if (rows <= 32) {
             const double us = keys / 256.0 * (0.25 + 1.85 * dim);  // an item's steps
             whole = (1.3 + us) * (rounds > 1 ? work + 1.2 * late : 1.0);
             cut = us * rounds * (c.head_dim == 64 ? 1.4 : 1.0) + 6 + traffic;  // two whole items of 64 share a CU
@@ -78,7 +111,7 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
             cut = 1.15 * shared * rounds * (0.85 + 0.15 * seen) + 15 + traffic;
         }
         const int64_t bound = item_bound(c, b, q_heads, tokens, rows, &s.per_token);
-        if (whole <= cut && bound < (int64_t(1) << 31)) {
+        if (whole <= cut && bound < (int64_t(1) << 31) && rows <= 128) {
             s.unit = 1 << 30;
             s.places = (int)bound;
         } else {
@@ -88,16 +121,20 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
             s.few = items * 8 <= slots;
             s.bytes = (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + 2 * sizeof(float));
         }
-        if (!best.rows || std::min(whole, cut) < best_cost) {
+        const double taken = rows <= 128 ? std::min(whole, cut) : cut;  // items of 256 are not taken whole
+        if (!best.rows || taken < best_cost) {
             best = s;
-            best_cost = std::min(whole, cut);
+            best_cost = taken;
         }
     };
     if (most <= 32) {
         consider(most <= 16 ? 16 : 32);
     } else {
+        if (tree && most <= 128) consider(32);
         consider(64);
         consider(128);
+        const double bytes = 4.0 * c.kv_heads * c.head_dim * seqs * (window ? std::min<int64_t>(context, (int64_t)window + longest) : context);
+        if (tree && most > 128 && (c.head_dim == 96 || c.head_dim == 128) && bytes > 128e6) consider(256);
     }
     return best;
 }

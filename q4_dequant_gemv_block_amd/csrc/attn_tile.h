@@ -31,7 +31,8 @@ struct Mma32<BF16> {
 };
 
 constexpr int kTile = 64;  // keys of a tile
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kPageTiles = 32;  // tiles whose pages are looked up at once (trees)
+constexpr int kWaves = 4;  // of a workgroup, two of which share a CU; trees have one of 8, too
 
 // Places in LDS (rows and their swizzles as described above).
 template <int D>
@@ -41,11 +42,11 @@ struct Layout : LdsRow<D> {
     static __device__ __forceinline__ int swz_v(int r) { return R::chunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; }
 };
 
-template <typename T, int D, int U, typename WORK, typename ARGS>
-__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const ARGS a, const Cut cut) {
+template <typename T, int D, int U, typename WORK, typename ARGS, int NW>
+__global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) k_attn_tile(const ARGS a, const Cut cut) {
     constexpr bool TREE = std::is_same<ARGS, TreeArgs>::value;
     typedef Layout<D> L;
-    constexpr int NW = kWaves, ROWS = 64 * U;
+    constexpr int ROWS = 16 * NW * U, kThreads = 64 * NW;
     constexpr int PAIRS = 8 * U;                       // pairs of scores of a tile a lane has
     constexpr int KS = D / 16;                         // k-steps of the first product
     constexpr int DT = D / 32;                         // 32-element tiles of the output
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
     constexpr int LOADS = kTile / L::per_load / NW;    // loads of a wave for K, and for V, of a tile
     constexpr int GROUPS = 8 / NW;                     // groups of 8 keys they cover
     constexpr int PER_GROUP = LOADS / GROUPS;
-    extern __shared__ char sh[];  // K [2][64][row], V [2][64][row], then a flag of each wave, and a depth of each row (TREE)
+    extern __shared__ char sh[];  // K [2][64][row], V [2][64][row], then a flag of each wave; TREE: a depth of each row, pages
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int h = lane >> 5, n = lane & 31;
     const int rows32 = U == 2 ? wave : wave & 1;      // the wave's 32 rows of the item's
@@ -103,8 +104,22 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
         float m = kNone, l = 0.0f;
 
-        // page of this lane's group (lane % 8) of the tile at key t
-        auto pages = [&](int t) { return page_of(a.cache, a.batch, table, t + 8 * (lane & 7)); };
+        // Page of this lane's group (lane % 8) of the tile at key t.  TREE: out of LDS, where
+        // the pages of kPageTiles tiles lie: a wait for memory here would be one for the tiles
+        // in flight.
+        int* ahead = reinterpret_cast<int*>(sh + 4 * L::bytes) + NW + ROWS;
+        int ahead_at = it.k_lo;
+        auto look_ahead = [&](int t) {
+            ahead_at = t;
+            const int u = threadIdx.x & (8 * kPageTiles - 1);  // (8 waves: each of them twice)
+            ahead[u] = page_of(a.cache, a.batch, table, t + 8 * u);
+        };
+        auto pages = [&](int t) {
+            if constexpr (TREE)
+                return ahead[((t - ahead_at) >> 3) + (lane & 7)];
+            else
+                return page_of(a.cache, a.batch, table, t + 8 * (lane & 7));
+        };
         // K (or V) of the tile at key t into one of its two places
         auto fill = [&](int t, int page8, const char* base, int64_t page_stride, int64_t slot_stride, uint32_t to, bool values) {
 #pragma unroll
@@ -163,6 +178,13 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
         };
         f16v even[U], odds[U];  // scores of this tile and of the next one, in turn
 
+        if constexpr (TREE) {
+            look_ahead(it.k_lo);
+            __builtin_amdgcn_s_waitcnt(0x0F70);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) asm volatile("" : "+v"(qf[s]));  // the queries are there: no wait for them in the loop
+            __syncthreads();
+        }
         if (it.k_lo < it.k_hi) {
             const int t = it.k_lo;
             page0 = pages(t);
@@ -178,7 +200,11 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             } else {
                 asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LOADS) : "memory");
             }
-            scores(even);
+            if constexpr (TREE) {
+                if (w_rows > 0) scores(even);
+            } else {
+                scores(even);
+            }
         }
         // One tile: its scores are in `now`, the next one's will be in `next`.
         int stage = 0;
@@ -191,7 +217,18 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
             if (t + 2 * kTile < it.k_hi) fill_k(t + 2 * kTile, page2, stage);
             page0 = page1;
             page1 = page2;
-            page2 = pages(t + 3 * kTile);
+            if constexpr (TREE) {
+                if (t + 3 * kTile < it.k_hi) {
+                    if (t + 3 * kTile >= ahead_at + kPageTiles * kTile) {
+                        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // all have read the last ones
+                        look_ahead(t + 3 * kTile);
+                        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    }
+                    page2 = pages(t + 3 * kTile);
+                }
+            } else {
+                page2 = pages(t + 3 * kTile);
+            }
             const uint32_t valid = (uint32_t)__ballot(page8 >= 0) & 0xFF;  // groups with a place
 
             // Tiles that not all of the workgroup's rows see whole: values of
@@ -233,6 +270,13 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // LDS alone: the next tiles stay in flight
 #pragma unroll
                 for (int w = 0; w < NW; ++w) odd |= flags[w] != 0;
+            }
+            if constexpr (TREE) {
+                if (w_rows <= 0) {  // a wave without rows has done its loads
+                    stage ^= 1;
+                    at_v ^= L::bytes;
+                    return;
+                }
             }
 #pragma unroll
             for (int i = 0; i < kAheadK; ++i) read_k(i);
@@ -443,21 +487,24 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const 
     }
 }
 
-template <typename T, int D, int U, typename WORK, typename ARGS>
+template <typename T, int D, int U, typename WORK, typename ARGS, int NW>
 hipError_t launch_work(const ARGS& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
-    constexpr size_t lds = (size_t)4 * Layout<D>::bytes + (kWaves + (std::is_same<ARGS, TreeArgs>::value ? 64 * U : 0)) * sizeof(int);
+    constexpr size_t lds = (size_t)4 * Layout<D>::bytes + (NW + (std::is_same<ARGS, TreeArgs>::value ? 16 * NW * U + 8 * kPageTiles : 0)) * sizeof(int);
     static LdsLimit limit;
-    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, U, WORK, ARGS>), lds);
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, U, WORK, ARGS, NW>), lds);
     if (e != hipSuccess) return e;
     return launch_shape(shape, cut, [&](unsigned grid, const Cut& c) {
-        hipLaunchKernelGGL((k_attn_tile<T, D, U, WORK, ARGS>), dim3(grid), dim3(kThreads), lds, s, a, c);
+        hipLaunchKernelGGL((k_attn_tile<T, D, U, WORK, ARGS, NW>), dim3(grid), dim3(64 * NW), lds, s, a, c);
     });
 }
 
-template <typename T, int D, int U, typename ARGS>
+template <typename T, int D, int U, typename ARGS, int NW = kWaves>
 hipError_t launch(const ARGS& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
     constexpr bool TREE = std::is_same<ARGS, TreeArgs>::value;
-    return shape.places ? launch_work<T, D, U, PlacesOf<TREE>>(a, cut, shape, s) : launch_work<T, D, U, WorkOf<TREE>>(a, cut, shape, s);
+    if constexpr (NW == 8)  // (items of 256 rows are never taken whole)
+        return launch_work<T, D, U, WorkOf<TREE>, ARGS, NW>(a, cut, shape, s);
+    else
+        return shape.places ? launch_work<T, D, U, PlacesOf<TREE>, ARGS, NW>(a, cut, shape, s) : launch_work<T, D, U, WorkOf<TREE>, ARGS, NW>(a, cut, shape, s);
 }
 
 }  // namespace

@@ -8,6 +8,7 @@ import torch
 import attention_cuts
 import kv_ref
 import step_ref
+import tree_cuts
 from gpu_util import lib, say
 
 pytestmark = pytest.mark.gpu
@@ -43,10 +44,10 @@ def check(q4, batch, q, k, v, mask, window=0, hint=None, scale=None, exact=None)
 
 
 @pytest.mark.parametrize("dtype", BOTH)
-@pytest.mark.parametrize("case", attention_cuts.cases(), ids=repr)
+@pytest.mark.parametrize("case", tree_cuts.cases(), ids=repr)
 def test_every_kernel(case, dtype):
-    """Items of 16 to 128 rows, whole and cut, every head_dim, with and without a window (the calls of attention_cuts, whose
-    rows are trees here)."""
+    """Items of 16 to 128 rows, whole and cut, every head_dim, with and without a window (a CPU test checks that these calls are cut
+    like that)."""
     q4 = lib()
     say("tree", case, dtype)
     batch = case.batch(3)
@@ -112,13 +113,12 @@ def test_windows(window):
 
 
 def test_a_chain_is_causal():
-    """With the mask of a chain, with and without a window, as q4_attention_paged, within both bounds; bit for bit where
-    the call is cut alike (no window)."""
+    """With the mask of a chain, with and without a window, what attention over causal rows is (which the bounds are
+    those of, too)."""
     q4 = lib()
     for lens, hq in (([(5, 700), (1, 33)], 4), ([(60, 900), (64, 64)], 8)):
         batch, q, k, v, mask = setup(lens, 16, hq, 2, 128, torch.float16, 1, 2, kind="chain")
-        cache, dev, dq = q4.KVCache(k.cuda(), v.cuda()), batch.device(q4), q.cuda()
-        assert torch.equal(q4.q4_attention_tree(cache, dev, dq, mask.cuda()), q4.q4_attention_paged(cache, dev, dq))
+        check(q4, batch, q, k, v, mask, exact=attention_cuts.Exact(q, k, v, batch, 128 ** -0.5, 0))
         exact = attention_cuts.Exact(q, k, v, batch, 128 ** -0.5, 50)
         # a window reaches into the chain: its first tokens are out of sight of the last
         inside = step_ref.mask_rows([step_ref.tree(n, None, "chain") for n in batch.new], 1)
