@@ -763,7 +763,7 @@ typedef struct q4_logit_rules {
      * (prompt_len NULL: none), the others its answer */
     const int32_t* history;     /* seqs rows of history_tokens entries */
     int64_t history_stride;
-    int history_tokens;         /* >= 1 with history; what history_len has above it does not count */
+    int history_tokens;         /* 1 .. 2^29 with history; what history_len has above it does not count */
     const int32_t* history_len; /* goes with history */
     const int32_t* prompt_len;
     /* drafted tokens, one a row: part of the answer for the rows that see them */
@@ -776,7 +776,7 @@ typedef struct q4_logit_rules {
     const int32_t* bias_start;  /* seqs + 1: a sequence's part of the lists, not falling */
     const int32_t* bias_tokens; /* biases; of equal tokens in a sequence's part the last counts */
     const float* bias_values;   /* biases */
-    int64_t biases;             /* 0 .. 2^31 - 1 */
+    int64_t biases;             /* 0 .. 2^29 */
     const uint32_t* allowed;    /* allowed_rows rows of ceil(vocab / 32) words: bit v % 32 of word v / 32: v may be picked */
     int64_t allowed_stride;
     int64_t allowed_rows;

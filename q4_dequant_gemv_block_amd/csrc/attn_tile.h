@@ -32,7 +32,7 @@ struct Mma32<BF16> {
 
 constexpr int kTile = 64;  // keys of a tile
 constexpr int kPageTiles = 32;  // tiles whose pages are looked up at once (trees)
-constexpr int kWaves = 4;  // of a workgroup, two of which share a CU; trees have one of 8, too
+constexpr int kWaves = 4;  // of a workgroup, two of which share a CU; for trees also one of 8 that has it alone
 
 // Places in LDS (rows and their swizzles as described above).
 template <int D>

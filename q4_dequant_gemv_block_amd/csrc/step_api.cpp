@@ -148,14 +148,14 @@ q4_status q4_logits_argmax(const void* logits, int type, int64_t row_stride, int
         if (r->seqs < 1 || r->seqs > kMaxRows) return fail(Q4_ERR_INVALID_ARG, "%s: seqs = %d outside [1, 2^24]", fn, r->seqs);
         if (!r->query_start && n > r->seqs) return fail(Q4_ERR_INVALID_ARG, "%s: %lld rows of %d sequences without query_start", fn, (long long)n, r->seqs);
         if (!r->history != !r->history_len) return fail(Q4_ERR_INVALID_ARG, "%s: history and history_len go together", fn);
-        if (r->history && (r->history_tokens < 1 || r->history_stride < 0 || r->history_stride > kMaxStride ||
+        if (r->history && (r->history_tokens < 1 || r->history_tokens > (1 << 29) || r->history_stride < 0 || r->history_stride > kMaxStride ||
                            (r->seqs > 1 && r->history_stride < r->history_tokens)))
-            return fail(Q4_ERR_INVALID_ARG, "%s: history_tokens = %d must be at least 1 and history_stride no smaller", fn, r->history_tokens);
+            return fail(Q4_ERR_INVALID_ARG, "%s: history_tokens = %d must be in [1, 2^29] and history_stride no smaller", fn, r->history_tokens);
         if (r->prompt_len && !r->history) return fail(Q4_ERR_INVALID_ARG, "%s: prompt_len without history", fn);
         if (r->mask && !r->draft) return fail(Q4_ERR_INVALID_ARG, "%s: a mask without draft", fn);
         if (r->mask ? r->mask_words < 1 || r->mask_words > kMaxWords : r->mask_words != 0)
             return fail(Q4_ERR_INVALID_ARG, "%s: mask_words = %d must be in [1, %d] with a mask and 0 without", fn, r->mask_words, kMaxWords);
-        if (r->biases < 0 || r->biases > 0x7fffffff) return fail(Q4_ERR_INVALID_ARG, "%s: biases outside [0, 2^31)", fn);
+        if (r->biases < 0 || r->biases > (1 << 29)) return fail(Q4_ERR_INVALID_ARG, "%s: biases outside [0, 2^29]", fn);
         if (r->bias_start ? r->biases && (!r->bias_tokens || !r->bias_values) : r->bias_tokens || r->bias_values || r->biases)
             return fail(Q4_ERR_INVALID_ARG, "%s: bias_start, bias_tokens and bias_values go together", fn);
         const int64_t words = (vocab + 31) / 32;

@@ -102,7 +102,7 @@ def test_attention_tree_refusals(lib, over, want, text):
 
 RULES = dict(seqs=3, query_start=20, history=21, history_stride=100, history_tokens=100, history_len=22, prompt_len=23, draft=24, mask=25,
              mask_words=1, repetition=26, presence=27, frequency=28, bias_start=29, bias_tokens=30, bias_values=31, biases=4, allowed=32,
-             allowed_stride=40, allowed_rows=5, allowed_row=33)
+             allowed_stride=300, allowed_rows=5, allowed_row=33)
 RULE_POINTERS = [n for n, t in q4.RulesDesc._fields_ if t is ctypes.c_void_p]
 
 
@@ -114,10 +114,10 @@ def rules(**over):
 
 @pytest.mark.parametrize("over,want,text", [
     (dict(rows=0), -1, "rows"), (dict(rows=1 << 25), -1, "rows"), (dict(vocab=0), -1, "vocab"), (dict(vocab=1 << 25), -1, "vocab"),
-    (dict(type=3), -1, "type"), (dict(stride=-1), -1, "stride"), (dict(out_stride=1000), -1, "overlap each other"),
+    (dict(type=3), -1, "type"), (dict(stride=-1), -1, "stride"), (dict(out_stride=8000), -1, "overlap each other"),
     (dict(logits=None), -1, "logits"), (dict(tokens=None), -1, "tokens"), (dict(logits=BASE + 2), -2, "logits"), (dict(out=BASE + GIB + 1), -2, "out"),
     (dict(tokens=BASE + 2 * GIB + 2), -2, "tokens"), (dict(workspace=None), -3, "workspace"), (dict(bytes=7), -3, "workspace"),
-    (dict(workspace=BASE + 3 * GIB + 4), -2, "workspace"), (dict(out=BASE + 4), -1, "out overlaps logits"), (dict(out=BASE, out_stride=1300), -1, "out overlaps logits"),
+    (dict(workspace=BASE + 3 * GIB + 4), -2, "workspace"), (dict(out=BASE + 4), -1, "out overlaps logits"), (dict(out=BASE, out_stride=9100), -1, "out overlaps logits"),
     (dict(tokens=BASE + 16), -1, "tokens overlaps logits"), (dict(workspace=BASE + GIB), -1, "out overlaps workspace"),
     (dict(rules=rules(seqs=0)), -1, "seqs"), (dict(rules=rules(query_start=None)), -1, "without query_start"),
     (dict(rules=rules(history_len=None)), -1, "go together"), (dict(rules=rules(history=None)), -1, "go together"),
@@ -132,7 +132,7 @@ def rules(**over):
   + [(dict(rules=rules(**{n: BASE + GIB})), -1, "out overlaps " + n) for n in RULE_POINTERS]
   + [(dict(rules=rules(**{n: BASE + 2 * GIB})), -1, "tokens overlaps " + n) for n in RULE_POINTERS])
 def test_logits_refusals(lib, over, want, text):
-    a = dict(logits=BASE, type=2, stride=1200, rows=5, vocab=1200, rules=rules(), out=BASE + GIB, out_stride=1200, tokens=BASE + 2 * GIB,
+    a = dict(logits=BASE, type=2, stride=9000, rows=5, vocab=9000, rules=rules(), out=BASE + GIB, out_stride=9000, tokens=BASE + 2 * GIB,
              workspace=BASE + 3 * GIB, bytes=GIB)
     a.update(over)
     st = lib.q4_logits_argmax(a["logits"], a["type"], a["stride"], a["rows"], a["vocab"], ref(a["rules"]), a["out"], a["out_stride"], a["tokens"],
