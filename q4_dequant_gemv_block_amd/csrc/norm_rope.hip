@@ -13,7 +13,12 @@
 // four tokens, whose heads are requested together.  Values (kv append) are copied by
 // the same groups.
 //
-// Bound by memory for prompts and by latency for single tokens, as the rotation alone.
+// Bound by memory for prompts and by latency for single tokens, as the rotation alone: a
+// token of 32/8 heads of 128 from binary32 into an f16 cache 4.4 us (an empty launch 3.8),
+// 5 ragged prompts of 6709 tokens, 32/8 heads, bf16, 34.4 us (165 MB read and written, 4.8
+// TB/s; a large copy reaches 4.7).  The heads of four tokens are held as they were read,
+// 16-bit ones packed, and one token's results are made at a time: held as binary32, with
+// all tokens' results under way, they took twice the registers (41.5 us).
 #include "kv_device.h"
 #include "q4gemv.h"
 
@@ -36,12 +41,38 @@ struct NormUnits {
     float inv_dim;
 };
 
+// V elements as they lie in memory.
+template <typename T, int V>
+struct Piece {
+    typedef typename Vec<T, V>::type raw;
+    raw v;
+    __device__ __forceinline__ void clear() { v = raw(0); }
+    __device__ __forceinline__ void load(const char* p) { v = *reinterpret_cast<const raw*>(p); }
+    __device__ __forceinline__ float at(int i) const { return (float)v[i]; }
+};
+template <typename T>
+struct Piece<T, 1> {
+    typename T::elem v;
+    __device__ __forceinline__ void clear() { v = (typename T::elem)0.0f; }
+    __device__ __forceinline__ void load(const char* p) { v = *reinterpret_cast<const typename T::elem*>(p); }
+    __device__ __forceinline__ float at(int) const { return (float)v; }
+};
+template <typename T, int V, int W>
+__device__ __forceinline__ void store_pair(char* p, const float (&x)[W]) {
+    if constexpr (V > 1) {
+        store_elems<T, W>(p, x);
+    } else {
+        reinterpret_cast<typename T::elem*>(p)[0] = (typename T::elem)x[0];
+        reinterpret_cast<typename T::elem*>(p)[1] = (typename T::elem)x[1];
+    }
+}
+
 // Units as in k_rope: half layout: V elements from the first half and V from the second
 // (or V that do not turn); interleaved: W consecutive ones.  NU units a lane.
 template <typename IN, typename OUT, bool HALF, int V, int NU>
 __global__ void __launch_bounds__(kThreads) k_norm_rope(const NormRopeArgs a, const NormUnits n) {
     constexpr int W = HALF ? V : (V < 2 ? 2 : V);
-    constexpr int E = HALF ? 2 * V : W;
+    constexpr int NP = HALF || V == 1 ? 2 : 1;  // pieces of a unit
     __shared__ f2 turn[kTokens][kMaxPairs];
     __shared__ float gain[2][2 * kMaxPairs];
     __shared__ int64_t place_k[kTokens], place_v[kTokens];
@@ -119,8 +150,9 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope(const NormRopeArgs a, co
         }
         const int list = item >= r.heads[0], h = item - (list ? r.heads[0] : 0);
         const HeadsArg in = list ? r.in[1] : r.in[0];
-        // all tokens' elements are read before any is written: out may be x itself
-        float x[kTokens][NU][E];
+        // All tokens' elements are read before any is written: out may be x itself.  They are
+        // held as they are read (16-bit ones packed) and converted twice.
+        Piece<IN, V> x[kTokens][NU][NP];
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
             const int64_t t = t0 + k < r.tokens ? t0 + k : r.tokens - 1;
@@ -129,26 +161,12 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope(const NormRopeArgs a, co
             for (int j = 0; j < NU; ++j) {
                 const int i = lane + (j << n.lanes_log2);
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[k][j][e] = 0.0f;
+                for (int e = 0; e < NP; ++e) x[k][j][e].clear();
                 if (i >= n.units) continue;
                 const bool turns = i < n.rotating;
                 const int e0 = turns ? i * (HALF ? V : W) : r.rot_dim + (i - n.rotating) * V;
-                if (!HALF && turns) {
-                    float v[W];
-                    load_elems<IN, W>(src + e0 * IN::bytes, v);
-#pragma unroll
-                    for (int e = 0; e < W; ++e) x[k][j][e] = v[e];
-                } else {
-                    float v[V];
-                    load_elems<IN, V>(src + e0 * IN::bytes, v);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) x[k][j][e] = v[e];
-                    if (HALF && turns) {
-                        load_elems<IN, V>(src + (e0 + half) * IN::bytes, v);
-#pragma unroll
-                        for (int e = 0; e < V; ++e) x[k][j][(HALF ? V : 0) + e] = v[e];
-                    }
-                }
+                x[k][j][0].load(src + e0 * IN::bytes);
+                if (NP == 2 && turns) x[k][j][NP - 1].load(src + (e0 + (HALF ? half : 1)) * IN::bytes);
             }
         }
         float scale[kTokens];
@@ -158,7 +176,10 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope(const NormRopeArgs a, co
 #pragma unroll
             for (int j = 0; j < NU; ++j)
 #pragma unroll
-                for (int e = 0; e < E; ++e) sum = __builtin_fmaf(x[k][j][e], x[k][j][e], sum);
+                for (int e = 0; e < NP * V; ++e) {
+                    const float v = x[k][j][e / V].at(e % V);
+                    sum = __builtin_fmaf(v, v, sum);
+                }
             scale[k] = sum;
         }
         for (int o = 1; o < 1 << n.lanes_log2; o <<= 1)
@@ -168,6 +189,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope(const NormRopeArgs a, co
         for (int k = 0; k < kTokens; ++k) scale[k] = 1.0f / __builtin_sqrtf(scale[k] * n.inv_dim + a.eps);
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
+            __builtin_amdgcn_sched_barrier(0);  // registers: one token's results at a time
             const int st = state[k];
             if (!(list == 0 ? st & 1 : st & 2)) continue;
             char* dst = list == 0 ? r.out.data + ((t0 + k) * r.out.token_stride + h * r.out.head_stride) * OUT::bytes
@@ -179,13 +201,14 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope(const NormRopeArgs a, co
                 const bool turns = i < n.rotating;
                 const int e0 = turns ? i * (HALF ? V : W) : r.rot_dim + (i - n.rotating) * V;
                 const float* g = &gain[list][e0];
+                const Piece<IN, V>*y = x[k][j];
                 if (turns) {
                     const f2* cs = &turn[k][HALF ? e0 : e0 / 2];
                     if (HALF) {
                         float lo[V], hi[V];
 #pragma unroll
                         for (int e = 0; e < V; ++e) {
-                            const float p = x[k][j][e] * scale[k] * g[e], q = x[k][j][(HALF ? V : 0) + e] * scale[k] * g[half + e];
+                            const float p = y[0].at(e) * scale[k] * g[e], q = y[NP - 1].at(e) * scale[k] * g[half + e];
                             lo[e] = p * cs[e].x - q * cs[e].y;
                             hi[e] = p * cs[e].y + q * cs[e].x;
                         }
@@ -195,16 +218,17 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope(const NormRopeArgs a, co
                         float o[W];
 #pragma unroll
                         for (int e = 0; e < W / 2; ++e) {
-                            const float p = x[k][j][2 * e] * scale[k] * g[2 * e], q = x[k][j][2 * e + (W > 1)] * scale[k] * g[2 * e + (W > 1)];
+                            const float p = (V > 1 ? y[0].at(V > 1 ? 2 * e : 0) : y[0].at(0)) * scale[k] * g[2 * e];
+                            const float q = (V > 1 ? y[0].at(V > 1 ? 2 * e + 1 : 0) : y[NP - 1].at(0)) * scale[k] * g[2 * e + 1];
                             o[2 * e] = p * cs[e].x - q * cs[e].y;
-                            o[2 * e + (W > 1)] = p * cs[e].y + q * cs[e].x;
+                            o[2 * e + 1] = p * cs[e].y + q * cs[e].x;
                         }
-                        store_elems<OUT, W>(dst + e0 * OUT::bytes, o);
+                        store_pair<OUT, V>(dst + e0 * OUT::bytes, o);
                     }
                 } else {
                     float o[V];
 #pragma unroll
-                    for (int e = 0; e < V; ++e) o[e] = x[k][j][e] * scale[k] * g[e];
+                    for (int e = 0; e < V; ++e) o[e] = y[0].at(e) * scale[k] * g[e];
                     store_elems<OUT, V>(dst + e0 * OUT::bytes, o);
                 }
             }
