@@ -685,8 +685,9 @@ typedef struct q4_kv_step {
  * not hold.  Pages are taken from the end of the free list, in the order of the
  * sequences and of their places.  A sequence whose pages do not fit into what is
  * left gets none of them (and so does every later one that needs any): missing says
- * how many it lacks, its held and entries stay as they were.  Entries behind the
- * pages a sequence holds are copied as they are.
+ * how many it lacks, held stays as it was, and the columns that lack a page are -1, so
+ * that nothing is read or written through what stood there.  Entries behind the pages
+ * a sequence needs are copied as they are.
  *   slots     : of new token i, place past_len + i in the cache
  *   positions : past_len + i; with parents past_len + the number of its ancestors
  *   mask      : bit j of a row (bit j % 64 of word j / 64): j is the token itself or
@@ -815,7 +816,7 @@ Q4_API q4_status q4_logits_argmax(const void* logits, int type, int64_t row_stri
  * The path through each sequence's drafted tree that the trunk agrees with: from the
  * sequence's first new token on, the lowest child whose draft is what was chosen
  * behind the node.  Rows are those of query_start and context_len as in q4_kv_batch;
- * a sequence whose rows are not all among the call's has none.
+ * a sequence whose rows are not all among the call's has none (accepted 0, next -1).
  *   choice  : tokens int32, the trunk's token behind each node (one below 0 ends the path)
  *   draft   : tokens int32, each node's own token
  *   parents : as in q4_kv_step, NULL: each node is the child of the one before

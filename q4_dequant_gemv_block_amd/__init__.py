@@ -1214,6 +1214,8 @@ class LogitRules:
                                              (bias_start, 1)) if t is not None]
         b = seqs if seqs is not None else sizes[0] if sizes else 0
         self.seqs = b
+        if b < 1 and (sizes or seqs is not None):
+            raise ValueError("no sequences")
 
         def vector(t, dtype, name, n):
             return None if t is None else _vector(t, dtype, name, n, dev)
@@ -1337,7 +1339,7 @@ def q4_tree_accept(batch: KVBatch, choice: torch.Tensor, draft: torch.Tensor, pa
     q4_kv_assign; None: a chain) drafted as what was chosen, and so on.  accepted counts the path's tokens, the first
     included; next_tokens is the choice behind its last; path has their indices in the sequence's first rows, then -1;
     lens the context with them alone.  history (int32 [B, L]) receives the path's tokens at the places they have.
-    out: the four tensors to write.  Rows of no sequence are left as they are (in a new path: -1)."""
+    T is at least 1.  out: the four tensors to write.  Rows of no sequence are left as they are (in a path made here: undefined)."""
     on = _on(batch.gpu, stream)
     if on is not None:
         with on:
@@ -1354,17 +1356,21 @@ def q4_tree_accept(batch: KVBatch, choice: torch.Tensor, draft: torch.Tensor, pa
         if history.dim() != 2 or history.shape[0] != b or history.get_device() != dev or (history.stride(1) != 1 and history.shape[1] != 1):
             raise ValueError("history must be [%d, entries] on GPU %d with consecutive entries" % (b, dev))
         hp, hs, hn = history.data_ptr(), history.stride(0), history.shape[1]
-    if out is None:
-        rest = torch.empty((3, b), dtype=i32, device=batch.device)
-        out = rest[0], rest[1], torch.full((t,), -1, dtype=i32, device=batch.device), rest[2]
-    accepted, following, path, lens = out
-    ap, np_, lp = _vector(accepted, i32, "accepted", b, dev), _vector(following, i32, "next_tokens", b, dev), _vector(lens, i32, "lens", b, dev)
-    rp = _vector(path, i32, "path", t, dev)
     if t == 0:
         raise ValueError("no tokens")
-    query_start, context_lens = batch._keep[1:]
+    if out is None:
+        accepted, following, lens = torch.empty((3, b), dtype=i32, device=batch.device).unbind()
+        path = choice.new_empty((t,))
+        out = accepted, following, path, lens
+        ap = accepted.data_ptr()
+        np_, lp, rp = ap + 4 * b, ap + 8 * b, path.data_ptr()
+    else:
+        accepted, following, path, lens = out
+        ap, np_, lp = _vector(accepted, i32, "accepted", b, dev), _vector(following, i32, "next_tokens", b, dev), _vector(lens, i32, "lens", b, dev)
+        rp = _vector(path, i32, "path", t, dev)
+    d = batch.desc
     status = (_lib or load_library()).q4_tree_accept(
-        query_start.data_ptr(), context_lens.data_ptr(), b, cp, dp, pp, t, ap, np_, rp, lp, hp, hs, hn, _current_stream(dev))
+        d.query_start, d.context_len, b, cp, dp, pp, t, ap, np_, rp, lp, hp, hs, hn, _current_stream(dev))
     if status:
         _check(status)
     return out

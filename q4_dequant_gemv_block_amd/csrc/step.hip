@@ -75,9 +75,11 @@ __global__ void __launch_bounds__(kThreads) k_assign(const AssignArgs a) {
         const bool served = x.lack == 0 || upto <= free_count;
         const int taken = served ? x.lack : 0;
         const int32_t* row_in = a.table_in + b * a.table_in_stride;
-        // the page behind column c
+        // the page behind column c: one taken, none for a column that lacks one (whatever
+        // stands there: it may be another sequence's by now), or the row's
         auto entry = [&](int c) {
-            return c >= x.held && c < x.held + taken ? a.free_pages[free_count - 1 - before - (c - x.held)] : row_in[c];
+            if (c < x.held || c >= x.held + x.lack) return row_in[c];
+            return served ? a.free_pages[free_count - 1 - before - (c - x.held)] : -1;
         };
         if (from == 0) {
             constexpr int64_t most = 0x7fffffff;
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) k_assign(const AssignArgs a) {
         // (a table in its own place keeps the other columns)
         const bool in_place = a.table_in == a.table;
         int32_t* row = a.table + b * a.table_stride;
-        for (int c = (in_place ? x.held : 0) + from; c < (in_place ? x.held + taken : a.table_pages); c += step) row[c] = entry(c);
+        for (int c = (in_place ? x.held : 0) + from; c < (in_place ? x.held + x.lack : a.table_pages); c += step) row[c] = entry(c);
         if (start < a.tokens) {
             const int n = (int)min((int64_t)x.fresh, a.tokens - start);
             for (int i = from; i < n; i += step) {
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) k_accept(const AcceptArgs a) {
     if (b >= a.seqs) return;
     const int first = a.query_start[b], last = a.query_start[b + 1], context = a.context_len[b];
     const int n = first < 0 || last > a.tokens || last < first ? 0 : last - first;
-    const int past = context - n;
+    const int past = context - max(last - first, 0);
     const int32_t *choice = a.choice + first, *draft = a.draft + first, *parents = a.parents ? a.parents + first : nullptr;
     int cur = 0, count = 0;
     int mine[kHold], token[kHold];  // nodes of the path at 64 k + lane, and their tokens

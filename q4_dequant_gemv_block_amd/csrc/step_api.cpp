@@ -253,6 +253,7 @@ q4_status q4_kv_move(const q4_kv_cache* caches, int layers, const q4_kv_batch* b
         Span at;
         const void* data;
         bool values;
+        int64_t rest;  // where in a period of the outermost axis it starts
     };
     Block blocks[2 * kMostLayers];
     int count = 0;
@@ -270,16 +271,41 @@ q4_status q4_kv_move(const q4_kv_cache* caches, int layers, const q4_kv_batch* b
             const Span at = cache_span(&c, values);
             if (overlap(at, p.at) || overlap(at, acc.at) || overlaps_batch(at, batch))
                 return fail(Q4_ERR_INVALID_ARG, "%s: the cache overlaps an input", fn);
-            blocks[count++] = Block{at, values ? c.v : c.k, values};
+            blocks[count++] = Block{at, values ? c.v : c.k, values, 0};
         }
     }
-    // blocks whose spans overlap may still lie beside each other (layers or sides of one tensor)
+    // Blocks whose spans overlap may still lie beside each other (layers or sides of one
+    // tensor).  Those with the same outermost axis only meet if what is inside it does,
+    // one period or another apart: then neighbours in the period are compared, not all
+    // pairs (1024 blocks side by side in one tensor 12 ms with all pairs, 0.03 with neighbours).
+    auto meet = [&](const Block& x, const Block& y) {
+        return overlap(x.at, y.at) && blocks_meet(x.values ? av : ak, x.values ? nv : nk, y.values ? av : ak, y.values ? nv : nk,
+                                                  caches->head_dim, (int64_t)((intptr_t)y.data - (intptr_t)x.data) / 2);
+    };
     std::sort(blocks, blocks + count, [](const Block& x, const Block& y) { return x.at.lo < y.at.lo; });
-    for (int i = 0; i < count; ++i)
-        for (int j = i + 1; j < count && blocks[j].at.lo < blocks[i].at.hi; ++j)
-            if (blocks_meet(blocks[i].values ? av : ak, blocks[i].values ? nv : nk, blocks[j].values ? av : ak, blocks[j].values ? nv : nk,
-                            caches->head_dim, (int64_t)((intptr_t)blocks[j].data - (intptr_t)blocks[i].data) / 2))
-                return fail(Q4_ERR_INVALID_ARG, "%s: keys and values of two layers are the same memory, or parts of them", fn);
+    bool apart = true;
+    for (int i = 1; i < count && apart; ++i) apart = blocks[i].at.lo >= blocks[i - 1].at.hi;
+    bool met = false;
+    if (!apart && nk && nv && ak->stride == av->stride && ak->count == av->count) {
+        int64_t inner = 0;
+        for (const bool values : {false, true}) {
+            int64_t r = caches->head_dim;
+            for (int i = 1; i < (values ? nv : nk); ++i) r = reach(r, (values ? av : ak)[i].count, (values ? av : ak)[i].stride);
+            inner = std::max(inner, r);
+        }
+        for (int i = 0; i < count; ++i) blocks[i].rest = (int64_t)((uint64_t)(uintptr_t)blocks[i].data / 2 % (uint64_t)ak->stride);
+        std::sort(blocks, blocks + count, [](const Block& x, const Block& y) { return x.rest < y.rest; });
+        for (int i = 0; i < count && !met; ++i)
+            for (int k = 1; k < count && !met; ++k) {
+                const int j = i + k < count ? i + k : i + k - count;
+                if (blocks[j].rest - blocks[i].rest + (j < i ? ak->stride : 0) >= inner) break;
+                met = meet(blocks[i], blocks[j]);
+            }
+    } else if (!apart) {
+        for (int i = 0; i < count && !met; ++i)
+            for (int j = i + 1; j < count && blocks[j].at.lo < blocks[i].at.hi && !met; ++j) met = meet(blocks[i], blocks[j]);
+    }
+    if (met) return fail(Q4_ERR_INVALID_ARG, "%s: keys and values of two layers are the same memory, or parts of them", fn);
     st = check_tensors(fn, {p, acc});
     if (st) return st;
     q4::MoveArgs a = {};

@@ -85,6 +85,7 @@ def assign(table, held, past, new, free, count, page, tokens, parents=None, word
         if lack and (full or lack > left):
             full = True
             out["missing"][b] = lack
+            out["table"][b, held[b] : held[b] + lack] = -1
         else:
             for c in range(lack):
                 left -= 1
@@ -222,7 +223,7 @@ def accept(start, ctx, choice, draft, parents, tokens, history=None):
     for b in range(len(ctx)):
         first, last = int(start[b]), int(start[b + 1])
         n = 0 if first < 0 or last > tokens or last < first else last - first
-        past = int(ctx[b]) - n
+        past = int(ctx[b]) - max(last - first, 0)
         got = [0] if n else []
         while got:
             cur = got[-1]

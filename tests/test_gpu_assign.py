@@ -11,12 +11,13 @@ pytestmark = pytest.mark.gpu
 
 
 def inputs(past, new, page, columns, seed, spare=3, held=None):
-    """A table in which each sequence holds the pages of what it has, -1 behind them, and the free pages."""
+    """A table in which each sequence holds the pages of what it has, others' pages and -1 behind them, and the free
+    pages."""
     rng = np.random.default_rng(seed)
     seqs = len(past)
     held = np.array([min(-(-max(p, 0) // page), columns) for p in past] if held is None else held, dtype=np.int32)
     ids = rng.permutation(seqs * columns + spare).astype(np.int32)
-    table = np.full((seqs, columns), -1, dtype=np.int32)
+    table = rng.integers(-1, seqs * columns, (seqs, columns)).astype(np.int32)
     at = 0
     for b in range(seqs):
         n = min(max(int(held[b]), 0), columns)

@@ -215,3 +215,75 @@ def test_two_streams_and_a_workspace():
     for i, job in enumerate(jobs):
         for out in got[i]:
             assert torch.equal(out, job[4])
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_captured_with_new_trees(dtype):
+    """A graph of a call cut into parts and of one taken whole, replayed with other lengths, trees and tables in the same
+    tensors, eager calls in between; both graphs use one workspace, one after the other."""
+    q4 = lib()
+    page, hq, hk, dim, tokens = 32, 8, 2, 128, 40
+    steps = [setup(lens, page, hq, hk, dim, dtype, 1, seed, tokens - sum(n for n, _ in lens), 300)
+             for seed, lens in enumerate(([(16, 9000), (20, 300)], [(1, 1), (0, 4000)], [(40, 40), (0, 0)], [(3, 6001), (33, 8999)]))]
+    pages = max(s[0].pages for s in steps)
+    k, v = (torch.zeros(pages, hk, page, dim, dtype=dtype, device="cuda") for _ in range(2))
+    cache, q = q4.KVCache(k, v), torch.zeros(tokens, hq, dim, dtype=dtype, device="cuda")
+    mask = torch.zeros(tokens, 1, dtype=torch.int64, device="cuda")
+    table, start, ctx = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in ((2, 300), (3,), (2,)))
+    out = torch.zeros(tokens, hq, dim, dtype=dtype, device="cuda")
+    batches = [q4.KVBatch(table, start, ctx, max_query_len=40, max_context_len=n) for n in (9600, 40)]
+    need = [q4.attention_tree_workspace_bytes(cache, b, hq, tokens) for b in batches]
+    assert need[0] > 0
+    ws = torch.empty(max(need), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for b in batches:
+        q4.q4_attention_tree(cache, b, q, mask, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            q4.q4_attention_tree(cache, b, q, mask, out=out, workspace=ws)
+    for batch, hq_, hk_, hv_, hm in steps * 2:
+        k[: batch.pages].copy_(hk_)
+        v[: batch.pages].copy_(hv_)
+        q.copy_(hq_)
+        mask.copy_(hm)
+        table.copy_(torch.from_numpy(batch.table))
+        start.copy_(torch.from_numpy(batch.start))
+        ctx.copy_(torch.tensor(batch.ctx, dtype=torch.int32))
+        n = int(batch.start[-1])
+        exact = step_ref.TreeExact(hq_, hk_, hv_, batch, hm, dim ** -0.5, 0)
+        for graph, b in zip(graphs, batches):
+            out.fill_(5.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            first = out.clone()
+            err = (first[:n].double().cpu() - exact.out[:n]).abs()
+            assert bool((err <= exact.bound[:n]).all()) and bool((first[n:] == 5.0).all())
+            assert torch.equal(q4.q4_attention_tree(cache, b, q, mask, workspace=ws)[:n], first[:n])
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("heads", [(8, 8), (40, 8)])
+def test_far_pages(heads):
+    """A cache of which some pages lie behind 2^32 bytes, read by items of few rows and by tiles, and written by an append
+    with norms: the same as in a small cache."""
+    q4 = lib()
+    hq, hk = heads
+    page, dim, pages = 64, 128, 36000
+    batch, q, k, v, mask = setup([(16, 700), (30, 1500)], page, hq, hk, dim, torch.bfloat16, 1, 4)
+    far = pages - batch.pages
+    caches = []
+    for count, first in ((batch.pages, 0), (pages, far)):
+        ck, cv = (torch.zeros(count, hk, page, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        ck[first:].copy_(k)
+        cv[first:].copy_(v)
+        table = torch.from_numpy(batch.table).cuda() + first
+        dev = q4.KVBatch(table, torch.from_numpy(batch.start).cuda(), torch.tensor(batch.ctx, dtype=torch.int32, device="cuda"))
+        x = q[:, :hk].cuda()
+        q4.q4_kv_append_norm(q4.KVCache(ck, cv), dev, x, 2 * x, inv_freq=q4.rope_frequencies(dim)[0])
+        caches.append((ck[first:], cv[first:], q4.q4_attention_tree(q4.KVCache(ck, cv), dev, q.cuda(), mask.cuda())))
+    assert not torch.equal(caches[0][0].cpu(), k)
+    for a, b in zip(*caches):
+        assert torch.equal(a, b)

@@ -206,3 +206,69 @@ def test_captured_with_new_lists():
             want = r.apply(l.numpy(), t)
             assert np.array_equal(out[t].cpu().numpy(), want) and int(tokens[t]) == r.pick(want)
         check(q4, l, r)
+
+
+def test_many_rows():
+    """More rows than a launch has along an axis, some of them without anything allowed."""
+    q4 = lib()
+    rows, vocab = 70001, 40
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(rows, vocab, device="cuda", generator=g)
+    allowed = torch.randint(-2 ** 31, 2 ** 31, (rows, 2), device="cuda", generator=g).to(torch.int32)
+    allowed[::1000] = 0
+    open_ = (allowed.repeat_interleave(32, 1)[:, :vocab] >> (torch.arange(vocab, device="cuda") % 32)) & 1
+    want = torch.where(open_.bool(), x, -math.inf)
+    out = torch.zeros_like(x)
+    tokens = q4.q4_logits_argmax(x, q4.LogitRules(allowed=allowed), out=out)
+    assert torch.equal(out, want)
+    assert torch.equal(tokens, torch.where(want.amax(1) > -math.inf, want.argmax(1), -1).int())
+    y = torch.randn(66000, 2100, device="cuda", generator=g)  # and of two slices
+    assert torch.equal(q4.q4_logits_argmax(y), y.argmax(1).int())
+
+
+def test_far_rows():
+    """Rows whose offsets pass 2^32 bytes, read and written."""
+    q4 = lib()
+    stride, vocab = (1 << 30) + 32, 9001
+    flat = torch.zeros(2 * stride + vocab, dtype=torch.float16, device="cuda")
+    x = flat.as_strided((3, vocab), (stride, 1))
+    y = torch.randn(3, vocab, generator=torch.Generator().manual_seed(1)).half().cuda()
+    x.copy_(y)
+    far = torch.zeros(2 * stride + vocab, device="cuda")
+    out = far.as_strided((3, vocab), (stride, 1))
+    presence = torch.ones(3, device="cuda")
+    history = y.argmax(1, keepdim=True).int()
+    tokens = q4.q4_logits_argmax(x, q4.LogitRules(history=history, history_lens=torch.ones(3, dtype=torch.int32, device="cuda"), presence=presence), out=out)
+    want = y.float().scatter_add(1, history.long(), -presence[:, None])
+    assert torch.equal(out, want) and torch.equal(tokens, want.argmax(1).int())
+
+
+def test_two_streams():
+    """Two calls at once, each with its own workspace and rules."""
+    q4 = lib()
+    jobs = []
+    for seed in range(2):
+        r = make(6, [1] * 6, 50021, seed, length=300, biases=20)
+        x = torch.randn(6, 50021, generator=torch.Generator().manual_seed(seed))
+        out, tokens = check(q4, x, r)
+        jobs.append((x.cuda(), r.device(q4), out, tokens, torch.cuda.Stream(),
+                     torch.empty(q4.logits_argmax_workspace_bytes(6, 50021), dtype=torch.uint8, device="cuda")))
+    torch.cuda.synchronize()
+    got = [[torch.empty_like(j[2]) for _ in range(10)] for j in jobs]
+    picks = [[], []]
+    torch.cuda.synchronize()
+    for n in range(10):
+        for i, (x, r, _, _, stream, ws) in enumerate(jobs):
+            picks[i].append(q4.q4_logits_argmax(x, r, out=got[i][n], workspace=ws, stream=stream))
+    torch.cuda.synchronize()
+    for i, j in enumerate(jobs):
+        assert all(torch.equal(o.view(torch.int32), j[2].view(torch.int32)) for o in got[i]) and all(torch.equal(p, j[3]) for p in picks[i])
+
+
+def test_no_sequences_are_refused():
+    q4 = lib()
+    zero, none = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(0, device="cuda")
+    for over in (dict(query_start=zero), dict(repetition=none), dict(bias_start=zero, bias_tokens=zero, bias_values=torch.zeros(1, device="cuda")),
+                 dict(allowed=torch.zeros(2, 2, dtype=torch.int32, device="cuda"), seqs=0)):
+        with pytest.raises(ValueError):
+            q4.LogitRules(**over)

@@ -45,7 +45,11 @@ def run(q4, new, ctx, parents, choice, draft, tokens, seqs_start=None, history=N
     torch.cuda.synchronize()
     accepted, following, path, lens = (x.tolist() for x in got)
     assert accepted == want[0] and following == want[1] and lens == want[3]
-    assert path == [-1 if x is None else x for x in want[2]]
+    assert [p for p, x in zip(path, want[2]) if x is not None] == [x for x in want[2] if x is not None]
+    out = tuple(torch.full_like(x, -77) for x in got)
+    assert q4.q4_tree_accept(batch, fill(choice), fill(draft), parents=None if parents is None else fill(parents), out=out) is out
+    assert out[2].tolist() == [-77 if x is None else x for x in want[2]]
+    assert all(torch.equal(out[i], got[i]) for i in (0, 1, 3))
     if history is not None:
         assert np.array_equal(h.cpu().numpy(), host)
     return got

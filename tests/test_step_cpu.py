@@ -2,6 +2,7 @@
 enqueued, with made-up addresses."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -202,6 +203,28 @@ def test_layers_of_one_tensor_are_apart(lib):
     q4.last_error()
     close = layers(*(cache(k=at + 4 * i * one - 16 * i, v=at + 4 * i * one + 2 * one, **wide) for i in range(2)))
     refused(lib, lib.q4_kv_move(close, 2, ref(batch()), BASE, BASE + GIB, 5, None), -1, "same memory")
+
+
+def test_many_layers_of_one_tensor(lib):
+    """Keys and values of 40 layers side by side in each page, in any order and over two tensors: none meet, and any
+    block moved into a neighbour (the last one's is the first one's next page) does."""
+    hk, page, dim = 2, 16, 128
+    one = 2 * hk * page * dim  # bytes
+    wide = dict(k_page_stride=40 * one // 2, v_page_stride=40 * one // 2)
+    tensors = (BASE + 16 * GIB + 2, BASE + 17 * GIB)  # 20 layers each
+    for seed in range(8):
+        rng = random.Random(seed)
+        places = [t + i * one for t in tensors for i in range(40)]
+        rng.shuffle(places)
+        at = rng.randrange(80)
+        for shift in (0, 2, -2, one - 2, 2 - one):
+            moved = list(places)
+            moved[at] += shift
+            caches = layers(*(cache(k=moved[2 * i], v=moved[2 * i + 1], **wide) for i in range(40)))
+            if shift:
+                refused(lib, lib.q4_kv_move(caches, 40, ref(batch()), BASE, BASE + GIB, 5, None), -1, "same memory")
+            else:
+                refused(lib, lib.q4_kv_move(caches, 40, ref(batch()), None, BASE, 5, None), -1, "null path")
 
 
 def test_python_checks():
