@@ -114,7 +114,7 @@ q4_status q4_kv_assign(const q4_kv_step* x, void* stream) {
 size_t q4_logits_argmax_workspace_bytes(int64_t n, int64_t vocab) {
     if (n < 1 || n > kMaxRows || vocab < 1 || vocab > kMaxRows) return 0;
     const int64_t slice = q4::logit_slice(n, vocab), slices = (vocab + slice - 1) / slice;
-    return slices > 1 ? (size_t)n * slices * 8 : 0;
+    return slices > 1 ? (size_t)n * slices * q4::kLogitKeys * 8 : 0;
 }
 
 q4_status q4_logits_argmax(const void* logits, int type, int64_t row_stride, int64_t n, int64_t vocab, const q4_logit_rules* r,

@@ -63,13 +63,14 @@ struct MoveArgs {
 };
 hipError_t launch_move(MoveArgs& a, bool wide, hipStream_t s);
 
+constexpr int kLogitKeys = 8;  // waves of a slice's workgroup
 struct LogitArgs {
     const char* logits;
     int64_t row_stride, rows, vocab;
     float* out;                // null: none
     int64_t out_stride;
     int32_t* tokens;
-    uint64_t* keys;            // [rows][slices], unless a slice is a row
+    uint64_t* keys;            // [rows][slices][kLogitKeys], unless a slice is a row
     int64_t slices;
     int seqs;
     const int32_t* query_start;

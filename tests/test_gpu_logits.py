@@ -272,3 +272,35 @@ def test_no_sequences_are_refused():
                  dict(allowed=torch.zeros(2, 2, dtype=torch.int32, device="cuda"), seqs=0)):
         with pytest.raises(ValueError):
             q4.LogitRules(**over)
+
+
+def test_quotients():
+    """Logits and repetitions of every size, results that overflow or have few bits among them: each quotient and product
+    is rounded once."""
+    q4 = lib()
+    rng = np.random.default_rng(5)
+    seqs, vocab = 40, 5003
+    x = torch.from_numpy(rng.integers(0, 2 ** 32, (seqs, vocab), dtype=np.uint64).astype(np.uint32).view(np.float32))
+    repetition = np.abs(rng.integers(1, 0x7F800000, seqs).astype(np.uint32).view(np.float32))
+    repetition[:8] = np.array([1.0, 1.1, 3.0, 2.0 ** -140, 1.17549435e-38, 3.4e38, 1 - 2.0 ** -24, 0.75], np.float32)
+    x[8:16] = torch.from_numpy((np.float32(2.0 ** -126) * rng.uniform(0.25, 4.0, (8, vocab))).astype(np.float32))  # around the normal ones' end
+    repetition[8:16] = np.array([2.0, 4.0, 1.5, 0.5, 1.0, 1.0 + 2.0 ** -23, 3.0, 8.0], np.float32)
+    with np.errstate(all="ignore"):
+        check(q4, x, step_ref.Rules(seqs, history=np.tile(np.arange(vocab, dtype=np.int32), (seqs, 1)), history_lens=np.full(seqs, vocab, np.int32),
+                                    repetition=repetition))
+
+
+def test_many_biases():
+    """More biases in a row than a workgroup has threads, most tokens several times; some rows with just as many, and
+    biases of zero."""
+    q4 = lib()
+    rng = np.random.default_rng(6)
+    for vocab in (700, 20011):
+        counts = [2000, 512, 513, 0, 511, 5000]
+        start = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        values = rng.normal(0, 5, start[-1]).astype(np.float32)
+        values[::3] = 0.0
+        values[1::7] = rng.integers(0, 9, len(values[1::7])).astype(np.uint32).view(np.float32)  # bits like small places
+        check(q4, torch.randn(6, vocab), step_ref.Rules(6, bias_start=start, bias_tokens=rng.integers(-2, vocab + 2, start[-1]).astype(np.int32),
+                                                        bias_values=values, history=rng.integers(0, vocab, (6, 30)).astype(np.int32),
+                                                        history_lens=np.full(6, 30, np.int32), presence=np.ones(6, np.float32)))
