@@ -687,7 +687,8 @@ typedef struct q4_kv_step {
  * left gets none of them (and so does every later one that needs any): missing says
  * how many it lacks, held stays as it was, and the columns that lack a page are -1, so
  * that nothing is read or written through what stood there.  Entries behind the pages
- * a sequence needs are copied as they are.
+ * a sequence needs are copied as they are; places behind the table's last column have
+ * no page and do not count as missing.
  *   slots     : of new token i, place past_len + i in the cache
  *   positions : past_len + i; with parents past_len + the number of its ancestors
  *   mask      : bit j of a row (bit j % 64 of word j / 64): j is the token itself or

@@ -114,7 +114,7 @@ def test_against_the_formula():
         # no step has more than |x| repetition + frequency count + presence + bias
         size = 2 * np.abs(logits[t].numpy()) + 2 * 400 + 2 + 25
         assert np.array_equal(np.isfinite(out[t].cpu().numpy()), on)
-        assert bool((np.abs(out[t].cpu().numpy() - exact)[on] <= 5 * 2.0 ** -24 * size[on]).all())
+        assert bool((np.abs(out[t].cpu().numpy()[on] - exact[on]) <= 5 * 2.0 ** -24 * size[on]).all())
 
 
 def test_ties_and_nothing_left():
