@@ -181,7 +181,10 @@ template <bool TREE>
 struct PlacesOf {
     // The kernel's loop over items is left after the first one and holds nothing for
     // others: no scalar registers are spilled for them (50 to 110 are for ranges).
-    static constexpr bool once = true;
+    static constexpr bool once = true, pair = false;
+    static __device__ __forceinline__ uint32_t ranges() { return gridDim.x; }
+    static __device__ __forceinline__ uint32_t range() { return blockIdx.x; }
+    static __device__ __forceinline__ int half() { return 0; }
     Seq seq;
 
     // Picks the sequence of a place; false if the place is empty.
@@ -249,9 +252,11 @@ struct PlacesOf {
 // 64 sequences (read once where there are no more), a wave's scan finds the
 // sequence of a unit.  A workgroup walks through the sequences twice, but there
 // are never more workgroups than the machine holds.
-template <bool TREE>
+// PAIR: two workgroups have a range, each half of an item's rows: 8 apart, so that they
+// run at once on one XCD, whose L2 then has the second one's keys.
+template <bool TREE, bool PAIR = false>
 struct WorkOf {
-    static constexpr bool once = false;
+    static constexpr bool once = false, pair = PAIR;
     uint32_t total;  // units of all sequences
     uint32_t begin;  // first unit of seq
     Seq seq;
@@ -314,13 +319,24 @@ struct WorkOf {
         return false;
     }
 
+    static __device__ __forceinline__ uint32_t ranges() { return PAIR ? gridDim.x / 2 : gridDim.x; }
+    static __device__ __forceinline__ uint32_t range() {
+        if constexpr (!PAIR) return blockIdx.x;
+        const uint32_t b = blockIdx.x, even = ranges() & ~7u;
+        return b < 2 * even ? (b >> 4) * 8 + (b & 7) : even + ((b - 2 * even) >> 1);
+    }
+    static __device__ __forceinline__ int half() {
+        if constexpr (!PAIR) return 0;
+        const uint32_t b = blockIdx.x, even = ranges() & ~7u;
+        return (int)((b < 2 * even ? b >> 3 : b) & 1);
+    }
     // This workgroup's range; next() goes through its items.
     __device__ __forceinline__ bool start(const Cut& c, const BatchArg& batch, Item*) {
         sum(c, batch);
-        const uint32_t grid = min((uint32_t)gridDim.x, total);  // no range is empty
-        if (blockIdx.x >= grid) return false;
-        lo = range_begin(total, blockIdx.x, grid);
-        hi = range_begin(total, blockIdx.x + 1, grid);
+        const uint32_t grid = min(ranges(), total), w = range();  // no range is empty
+        if (w >= grid) return false;
+        lo = range_begin(total, w, grid);
+        hi = range_begin(total, w + 1, grid);
         return find(c, batch, lo);
     }
     __device__ __forceinline__ bool next(const Cut& c, const BatchArg& batch, Item* x) {

@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) k_attn_tile(const A
     Item it;
     if (!work.start(cut, a.batch, &it)) return;
     const Seq& seq = work.seq;
-    const Parts<D> parts(a.workspace, (int)gridDim.x, ROWS);
+    constexpr int PART = WORK::pair ? 2 * ROWS : ROWS;  // rows of an item, and of its parts
+    const Parts<D> parts(a.workspace, (int)WORK::ranges(), PART);
 
     // where this lane reads in a tile: chunks 2 s + h of K's rows, 64-byte block d of V's
     int at_k0 = (first + n) * L::row + ((h ^ L::swz_k(n)) * 16), at_v0;
@@ -76,6 +77,11 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) k_attn_tile(const A
     }
 
     while (work.next(cut, a.batch, &it)) {
+        if constexpr (WORK::pair) {  // this workgroup's half
+            it.row0 += ROWS * WORK::half();
+            it.rows = min(ROWS, it.rows - ROWS * WORK::half());
+            if (it.rows <= 0) continue;
+        }
         const int32_t* table = a.batch.table + seq.b * a.batch.table_stride;
         const char* kbase = a.cache.k + (int64_t)it.head * a.cache.k_head * 2;
         const char* vbase = a.cache.v + (int64_t)it.head * a.cache.v_head * 2;
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) k_attn_tile(const A
                 }
             if (a.lse && h == 0) a.lse[(int64_t)(seq.row0 + qi) * a.q_heads + qh] = row_lse(m, l);
         } else {
-            const int64_t slot = ((int64_t)2 * blockIdx.x + (it.u0 == 0)) * ROWS + 32 * rows32 + n;
+            const int64_t slot = ((int64_t)2 * WORK::range() + (it.u0 == 0)) * PART + ROWS * WORK::half() + 32 * rows32 + n;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -494,7 +500,7 @@ hipError_t launch_work(const ARGS& a, const Cut& cut, const AttnShape& shape, hi
     const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, U, WORK, ARGS, NW>), lds);
     if (e != hipSuccess) return e;
     return launch_shape(shape, cut, [&](unsigned grid, const Cut& c) {
-        hipLaunchKernelGGL((k_attn_tile<T, D, U, WORK, ARGS, NW>), dim3(grid), dim3(64 * NW), lds, s, a, c);
+        hipLaunchKernelGGL((k_attn_tile<T, D, U, WORK, ARGS, NW>), dim3(WORK::pair ? 2 * grid : grid), dim3(64 * NW), lds, s, a, c);
     });
 }
 
