@@ -24,26 +24,24 @@ inline int64_t item_bound(const CacheArg& c, const BatchArg& b, int q_heads, int
 // their parts are joined by item, so they have numbers of their own, and more ways:
 // up to 128 rows in items of 32 (many workgroups of little each: 16 tokens of 4 heads
 // a kv head over 515 keys 11.7 us, in one item of 64 rows 14.9), more than 128 of heads
-// of 96 or 128 in items of 256 (8 waves that share the keys' tiles) where the keys and
-// values are more than the last-level cache keeps, so that items of 128 rows would read
-// them twice from HBM (3 sequences of 64 tokens over 32768 keys, 32/8 heads of 128, 141
-// us, with items of 128 161).
-// Fitted to 320 calls; of 648 (2 to 200 tokens of 1 to 96 sequences over up to 40000
-// keys, heads of 64 to 256, with and without windows), each run in every way, what is
-// taken is within 5 % of the best in 587, 1.5 % behind in the mean and 35 % at most (by
-// the numbers for prompts and decode steps 4.6 % in the mean).
+// of 96 or 128 in items of 256, whose halves two workgroups of one XCD have at a time:
+// the keys come from HBM once (3 sequences of 64 tokens over 32768 keys, 32/8 heads of
+// 128, f16, 139 us, with items of 128 161; of 40 tokens over 6000 keys 43 and 52).
+// The numbers for heads up to 128 are fitted to 378 calls.  Of 1044 (2 to 200 tokens of 1
+// to 96 sequences over up to 40000 keys, heads of 64 to 256, with and without windows),
+// each run in every way, what is taken is 1.3 % behind the best in the mean, within 5 %
+// of it in 959 and 28 % behind at most.
 struct TreeCost {
     double start, each;     // us of an item, of 256 keys (items of 16 and 32 rows) or a tile
-    double late;            // of what the last round lacks
+    double alone, late;     // a whole item on a CU of its own; of what the last round lacks
     double parts, range, traffic;  // the join's launch, units in ranges, the parts' way to memory and back
 };
 inline TreeCost tree_cost(int rows, int head_dim) {
     const double dim = head_dim / 128.0;
-    if (rows <= 32) return {1.4, (0.213 + 2.18 * dim) * (rows == 32 ? 1.05 : 1.0), 1.24, 10.4, 1.0, 0.71};
-    const double tile = head_dim > 128 ? (rows == 64 ? 1.82 : 2.14)
-                        : rows == 64   ? 0.47 + 0.75 * dim
-                                       : (0.515 + 0.77 * dim) * (rows == 256 ? 0.95 : 1.0);
-    return {0.38, tile, 0.16, 10.1, 1.17, 0.87};
+    if (rows <= 32) return {1.4, (0.213 + 2.18 * dim) * (rows == 32 ? 1.05 : 1.0), 1.0, 1.24, 10.4, 1.0, 0.71};
+    if (head_dim > 128) return {0.38, rows == 64 ? 1.82 : 2.14, 0.95, 0.16, 10.1, 1.17, 0.87};
+    const double tile = rows == 64 ? 0.431 + 0.617 * dim : (0.422 + 0.738 * dim) * (rows == 256 ? 0.711 : 1.0);
+    return {0.533, tile, 0.906, 0.166, 9.65, 1.302, 0.921};
 }
 
 // How a call is cut: the rows of an item, and whether items are taken whole or
@@ -96,7 +94,7 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
             const TreeCost cost = tree_cost(rows, c.head_dim);
             const double us = cost.each * (rows <= 32 ? keys / 256.0 : (double)((keys + 63) / 64));
             whole = rows <= 32 ? cost.start + us * (rounds > 1 ? rounds + cost.late * std::min(1.0, std::ceil(rounds) - rounds) : 1.0)
-                    : items <= cus ? 0.95 * (cost.start + us)  // each on its CU
+                    : items <= cus ? cost.alone * (cost.start + us)
                                    : cost.start + us * std::max(1.0, rounds + cost.late * std::min(1.0, std::ceil(rounds) - rounds));
             cut = cost.parts + cost.range * us * rounds + cost.traffic * traffic;
         } else if (rows <= 32) {
@@ -133,8 +131,7 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
         if (tree && most <= 128) consider(32);
         consider(64);
         consider(128);
-        const double bytes = 4.0 * c.kv_heads * c.head_dim * seqs * (window ? std::min<int64_t>(context, (int64_t)window + longest) : context);
-        if (tree && most > 128 && (c.head_dim == 96 || c.head_dim == 128) && bytes > 128e6) consider(256);
+        if (tree && most > 128 && (c.head_dim == 96 || c.head_dim == 128)) consider(256);
     }
     return best;
 }

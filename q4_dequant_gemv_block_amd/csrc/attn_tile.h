@@ -32,7 +32,7 @@ struct Mma32<BF16> {
 
 constexpr int kTile = 64;  // keys of a tile
 constexpr int kPageTiles = 32;  // tiles whose pages are looked up at once (trees)
-constexpr int kWaves = 4;  // of a workgroup, two of which share a CU; for trees also one of 8 that has it alone
+constexpr int kWaves = 4, kThreads = 64 * kWaves;  // of a workgroup, two of which share a CU
 
 // Places in LDS (rows and their swizzles as described above).
 template <int D>
@@ -42,11 +42,11 @@ struct Layout : LdsRow<D> {
     static __device__ __forceinline__ int swz_v(int r) { return R::chunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; }
 };
 
-template <typename T, int D, int U, typename WORK, typename ARGS, int NW>
-__global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) k_attn_tile(const ARGS a, const Cut cut) {
+template <typename T, int D, int U, typename WORK, typename ARGS>
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) k_attn_tile(const ARGS a, const Cut cut) {
     constexpr bool TREE = std::is_same<ARGS, TreeArgs>::value;
     typedef Layout<D> L;
-    constexpr int ROWS = 16 * NW * U, kThreads = 64 * NW;
+    constexpr int NW = kWaves, ROWS = 64 * U;
     constexpr int PAIRS = 8 * U;                       // pairs of scores of a tile a lane has
     constexpr int KS = D / 16;                         // k-steps of the first product
     constexpr int DT = D / 32;                         // 32-element tiles of the output
@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) k_attn_tile(const A
         int ahead_at = it.k_lo;
         auto look_ahead = [&](int t) {
             ahead_at = t;
-            const int u = threadIdx.x & (8 * kPageTiles - 1);  // (8 waves: each of them twice)
-            ahead[u] = page_of(a.cache, a.batch, table, t + 8 * u);
+            static_assert(8 * kPageTiles == kThreads, "a page a thread");
+            ahead[threadIdx.x] = page_of(a.cache, a.batch, table, t + 8 * (int)threadIdx.x);
         };
         auto pages = [&](int t) {
             if constexpr (TREE)
@@ -493,24 +493,21 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) k_attn_tile(const A
     }
 }
 
-template <typename T, int D, int U, typename WORK, typename ARGS, int NW>
+template <typename T, int D, int U, typename WORK, typename ARGS>
 hipError_t launch_work(const ARGS& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
-    constexpr size_t lds = (size_t)4 * Layout<D>::bytes + (NW + (std::is_same<ARGS, TreeArgs>::value ? 16 * NW * U + 8 * kPageTiles : 0)) * sizeof(int);
+    constexpr size_t lds = (size_t)4 * Layout<D>::bytes + (kWaves + (std::is_same<ARGS, TreeArgs>::value ? 64 * U + 8 * kPageTiles : 0)) * sizeof(int);
     static LdsLimit limit;
-    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, U, WORK, ARGS, NW>), lds);
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_attn_tile<T, D, U, WORK, ARGS>), lds);
     if (e != hipSuccess) return e;
     return launch_shape(shape, cut, [&](unsigned grid, const Cut& c) {
-        hipLaunchKernelGGL((k_attn_tile<T, D, U, WORK, ARGS, NW>), dim3(WORK::pair ? 2 * grid : grid), dim3(64 * NW), lds, s, a, c);
+        hipLaunchKernelGGL((k_attn_tile<T, D, U, WORK, ARGS>), dim3(WORK::pair ? 2 * grid : grid), dim3(kThreads), lds, s, a, c);
     });
 }
 
-template <typename T, int D, int U, typename ARGS, int NW = kWaves>
+template <typename T, int D, int U, typename ARGS>
 hipError_t launch(const ARGS& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
     constexpr bool TREE = std::is_same<ARGS, TreeArgs>::value;
-    if constexpr (NW == 8)  // (items of 256 rows are never taken whole)
-        return launch_work<T, D, U, WorkOf<TREE>, ARGS, NW>(a, cut, shape, s);
-    else
-        return shape.places ? launch_work<T, D, U, PlacesOf<TREE>, ARGS, NW>(a, cut, shape, s) : launch_work<T, D, U, WorkOf<TREE>, ARGS, NW>(a, cut, shape, s);
+    return shape.places ? launch_work<T, D, U, PlacesOf<TREE>>(a, cut, shape, s) : launch_work<T, D, U, WorkOf<TREE>>(a, cut, shape, s);
 }
 
 }  // namespace

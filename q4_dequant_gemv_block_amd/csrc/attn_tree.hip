@@ -15,14 +15,21 @@
 // row a group of lanes (34 -> 11 us for 3 sequences of 64 tokens), and waves without
 // rows do their loads alone.
 //
+// Items of 256 rows (trees of more than 128 rows of a kv head, heads of 96 and 128) are
+// taken by two workgroups, half of the rows each, that run at once on one XCD: the keys
+// come from HBM once and to the second one from the L2, and a CU's two workgroups hide
+// each other's waits (a workgroup of 8 waves that share the tiles in LDS took 6 % longer,
+// items of 128 rows by themselves 16 %, over 3 sequences of 64 tokens over 32768 keys).
+//
 // Measured, 32 query heads over 8 of 128, a call: 16 ragged sequences of up to 33 tokens
 // over up to 6001 keys 74 us (3.1 TB/s of keys and values; the matrix products of rows
 // that are there take 20, HBM 32 at 7.2 TB/s; a workgroup has about 1.5 items of 27
-// tiles, whose start and end, some 8 us, nothing hides), 3 of 64 over 32768 keys 144
-// (715 TFLOP/s; 94 at the rate of a large product), one of 16 tokens over 515 keys of 40
+// tiles, whose start and end, some 8 us, nothing hides), 3 of 64 over 32768 keys 139
+// (741 TFLOP/s; 88 at the rate of a large product), one of 16 tokens over 515 keys of 40
 // heads 10.5 (latency).
-// Tried: four tiles of K and of V in LDS for items of 256 rows instead of two (71 and 141
-// us, as before: not the loads are what is waited for).
+// Tried: four tiles of K and of V in LDS for 8 waves instead of two (71 and 141 us, as
+// before: not the loads are what is waited for); weights summed a step after they are
+// packed (no change).
 #include "attn_rows.h"
 
 namespace q4 {

@@ -7,7 +7,7 @@ namespace q4 {
 template <typename T, int D>
 hipError_t launch_attn_tile(const TreeArgs& a, const Cut& cut, const AttnShape& shape, hipStream_t s) {
     if constexpr (D == 96 || D == 128)
-        if (shape.rows == 256) return launch_work<T, D, 2, WorkOf<true, true>, TreeArgs, kWaves>(a, cut, shape, s);
+        if (shape.rows == 256) return launch_work<T, D, 2, WorkOf<true, true>>(a, cut, shape, s);  // (never taken whole)
     return shape.rows == 128 ? launch<T, D, 2>(a, cut, shape, s) : launch<T, D, 1>(a, cut, shape, s);
 }
 

@@ -14,23 +14,28 @@ SOME = [(20, 700), (9, 64), (0, 9), (31, 40), (7, 1000)]        # 62 or 124
 MANY = [(70, 700), (1, 65), (0, 17), (150, 260), (40, 38)]      # 300
 WIDE = [(50, 700), (1, 65), (0, 17), (64, 260), (40, 38)]       # 192
 FAR = [(50, 6500), (1, 65), (64, 2700), (40, 38)]
+NEAR = [(30, 700), (1, 65), (0, 17), (32, 260), (20, 38)]       # 128 of 8 heads
+NEARFAR = [(32, 6500), (1, 65), (30, 2700), (20, 38)]
 FARTHER = [(50, 17000), (64, 2700), (40, 38)] + [(0, 9)] * 9
 # rows of an item, whole -> sequences, query heads, window, rows behind the last sequence, the longest context that the
 # call names, right or not, without and with a window: they decide how it is cut
 CHOICE = {
     (16, True): ((ONE, 6, 0, 3, 300), (ONE, 6, 100, 3, 300)), (16, False): ((ONE, 6, 0, 3, 60000), (ONE, 6, 30000, 3, 60000)),
-    (32, True): ((TWO, 10, 0, 3, 300), (SOME, 4, 100, 3, 100)), (32, False): ((TWO, 10, 0, 3, 60000), (TWO, 10, 6000, 6000, 60000)),
+    (32, True): ((TWO, 10, 0, 3, 300), (SOME, 4, 100, 3, 300)), (32, False): ((TWO, 10, 0, 3, 60000), (TWO, 10, 6000, 6000, 60000)),
     (64, True): ((MANY, 4, 0, 3, 300), (MANY, 4, 100, 3, 300)), (64, False): ((MANY, 4, 0, 3, 3000), (FAR, 8, 2500, 3, 60000)),
     (128, True): ((MANY, 4, 0, 90000, 700), (MANY, 4, 100, 90000, 700)), (128, False): ((MANY, 4, 0, 3, 60000), (FAR, 8, 2500, 1200, 6500)),
     (256, False): ((WIDE, 6, 0, 300, 60000), (FARTHER, 6, 16000, 3000, 32000)),
 }
+# heads that items of 256 rows are for: those of 128 have parts where no sequence has more rows
+NARROW = ((NEAR, 8, 0, 300, 60000), (NEARFAR, 8, 4000, 2000, 6500))
 
 
 class Case:
     """rows of an item, head_dim, whole or cut, and what makes it so; pages of several sizes."""
 
     def __init__(self, rows, dim, whole, windowed, page):
-        self.lens, self.hq, self.window, self.pad, self.max_context = CHOICE[rows, whole][windowed]
+        choice = NARROW if (rows, whole) == (128, False) and dim in (96, 128) else CHOICE[rows, whole]
+        self.lens, self.hq, self.window, self.pad, self.max_context = choice[windowed]
         self.rows, self.dim, self.whole, self.page, self.hk = rows, dim, whole, page, 2
         self.max_query = max(n for n, _ in self.lens)
         self.columns = -(-max(self.max_context, max(c for _, c in self.lens)) // page)
