@@ -686,7 +686,8 @@ typedef struct q4_kv_step {
  * sequences and of their places.  A sequence whose pages do not fit into what is
  * left gets none of them (and so does every later one that needs any): missing says
  * how many it lacks, held stays as it was, and the columns that lack a page are -1, so
- * that nothing is read or written through what stood there.  Entries behind the pages
+ * that nothing is read or written through what stood there; what the step makes of its
+ * rows does not count, they are to be repeated when there are pages.  Entries behind the pages
  * a sequence needs are copied as they are; places behind the table's last column have
  * no page and do not count as missing.
  *   slots     : of new token i, place past_len + i in the cache

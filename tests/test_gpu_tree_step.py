@@ -178,3 +178,115 @@ def test_trees_give_the_plain_text(captured):
             assert int(server.past[b]) == at + n
             taken += n
     assert taken > 36  # more than one token a sequence and step
+
+
+def test_a_sequence_without_pages_touches_no_other():
+    """A sequence whose pages do not fit, with others' pages behind its own in the row: keys, values, outputs and moves of
+    the others are as without it, its own tokens are not stored."""
+    q4 = lib()
+    page, hq, hk, dim = 16, 8, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    k, v = (torch.randn(9, hk, page, dim, device="cuda", generator=g).half() for _ in range(2))
+    x = torch.randn(12, hq + 2 * hk, dim, device="cuda", generator=g)
+    parents = [-1, 0, 0, 1, -1, 0, 0, 1, -1, 0, 1, 1]
+    draft, choice = i32([7, 1, 2, 3] * 3), i32([2, 9, 5, 9, 2, 9, 5, 9, 1, 2, 9, 9])
+    freq, _ = q4.rope_frequencies(dim)
+    got = []
+    for news in ([4, 4, 4], [4, 0, 4]):
+        caches = k.clone(), v.clone()
+        cache = q4.KVCache(*caches)
+        step = q4.KVStep(3, 4, page, 12, 1)
+        # the second needs another page, none is left; behind its own stand the first's and the third's
+        table = i32([[0, 1, 8, 8], [2, 0, 1, 5], [4, 5, 0, 0]])
+        rows = [0, 1, 2, 3] + ([4, 5, 6, 7] if news[1] else []) + [8, 9, 10, 11]
+        pad = 12 - len(rows)
+        pick = torch.tensor(rows + [0] * pad, device="cuda")
+        own = torch.tensor([parents[r] for r in rows] + [-1] * pad, dtype=torch.int32, device="cuda")
+        q4.q4_kv_assign(step, table, i32([2, 1, 2]), i32([20, 14, 17]), i32(news), i32([7]), i32([0]), parents=own)
+        q, kk, vv = x[pick].split([hq, hk, hk], 1)
+        turned = q4.q4_kv_append_norm(cache, step.batch, kk, vv, q=q, inv_freq=freq, positions=step.positions)
+        out = q4.q4_attention_tree(cache, step.batch, turned, step.mask)
+        accepted, following, path, lens = q4.q4_tree_accept(step.batch, choice[pick].contiguous(), draft[pick].contiguous(), parents=own)
+        q4.q4_kv_move(cache, step.batch, path, accepted)
+        torch.cuda.synchronize()
+        at = [i for i, r in enumerate(rows) if r < 4 or r >= 8]
+        got.append((step, accepted, caches, out[at].clone()))
+    full, without = got
+    assert full[0].missing.tolist() == [0, 1, 0] and full[0].block_table.tolist()[1] == [2, -1, 1, 5]
+    assert full[0].slots[4:8].tolist() == [2 * page + 14, 2 * page + 15, -1, -1]
+    assert [full[1].tolist()[b] for b in (0, 2)] == [without[1].tolist()[b] for b in (0, 2)]
+    assert torch.equal(full[3], without[3])
+    for a, b, was in zip(full[2], without[2], (k, v)):
+        others = [p for p in range(9) if p != 2]
+        assert torch.equal(a[others], b[others])
+        assert torch.equal(a[2, :, :14], was[2, :, :14])  # its own page: the two tokens that have a place
+
+
+def test_each_on_a_stream_of_its_own():
+    """Every operator on a stream that is not the current one, behind work there that makes its inputs."""
+    q4 = lib()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    freq, _ = q4.rope_frequencies(128)
+    table, start, ctx = i32([[3, 1, 0], [2, 5, 4]]), i32([0, 5, 9]), i32([40, 44])
+    batch = q4.KVBatch(table, start, ctx)
+    x = torch.randn(9, 12, 128, device="cuda", generator=g).half()
+    base = [torch.randn(6, 2, 16, 128, device="cuda", generator=g).half() for _ in range(2)]
+    mask = torch.tensor([1, 3, 7, 11, 19, 1, 3, 7, 15], device="cuda").view(9, 1)
+    logits = torch.randn(9, 30000, device="cuda", generator=g)
+    history = torch.randint(0, 30000, (2, 50), device="cuda", generator=g, dtype=torch.int32)
+    pos = i32(range(9))
+
+    def norm(x, stream=None):
+        return [q4.q4_norm_rope(x, None, 1e-6, pos, freq, stream=stream)]
+
+    def append(x, stream=None):
+        kv = [t.clone() for t in base]
+        torch.cuda.synchronize()
+        q, k, v = x.split([8, 2, 2], 1)
+        return [q4.q4_kv_append_norm(q4.KVCache(*kv), batch, k, v, q=q, inv_freq=freq, stream=stream)] + kv
+
+    def tree(x, stream=None):
+        return [q4.q4_attention_tree(q4.KVCache(*base), batch, x, mask, stream=stream)]
+
+    def pick(x, stream=None):
+        rules = q4.LogitRules(query_start=start, history=history, history_lens=i32([50, 20]), presence=torch.ones(2, device="cuda"))
+        torch.cuda.synchronize()
+        return [q4.q4_logits_argmax(x, rules, stream=stream)]
+
+    def assign(x, stream=None):
+        step = q4.KVStep(2, 3, 16, 9, 1)
+        left, count = i32([9, 8, 7, 6]), i32([4])
+        torch.cuda.synchronize()
+        q4.q4_kv_assign(step, table, x[0], x[1], x[2], left, count, stream=stream)
+        return [step.block_table, step.held, step.missing, step.slots, step.mask]
+
+    def accept(x, stream=None):
+        return list(q4.q4_tree_accept(batch, x[0], x[1], parents=x[2], stream=stream))
+
+    def move(x, stream=None):
+        kv = [t.clone() for t in base]
+        torch.cuda.synchronize()
+        q4.q4_kv_move(q4.KVCache(*kv), batch, x[:9], x[9:], stream=stream)
+        return kv
+
+    cases = ((norm, x), (append, x), (tree, x[:, :8].contiguous()), (pick, logits), (assign, i32([[1, 2], [16, 30], [5, 4]])),
+             (accept, i32([[4, 9, 1, 1, 3, 5, 5, 5, 5], [0, 4, 7, 9, 8, 0, 5, 5, 5], [-1, 0, 0, 1, 1, -1, 0, 1, 2]])),
+             (move, i32([0, 2, 4, -1, -1, 0, 3, -1, -1, 3, 2])))
+    side, slow = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda").half()
+    for fn, real in cases:
+        say("stream", fn.__name__)
+        want = fn(real)
+        given = torch.zeros_like(real)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                slow @ slow
+            given.copy_(real)
+        got = fn(given, stream=side)
+        side.synchronize()
+        if fn is append or fn is move or fn is assign or fn is pick:
+            torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), fn.__name__
