@@ -191,7 +191,19 @@ struct PlacesOf {
     __device__ __forceinline__ bool find(const Cut& c, const BatchArg& batch, uint32_t place, uint32_t* item) {
         const uint32_t x = c.kv_heads.div(place);
         uint32_t up;  // item of the kv head
-        if (batch.seqs <= 64) {
+        bool one = false;
+        if constexpr (TREE) one = batch.seqs == 1;
+        if (one) {  // (scalar loads, and no sums over lanes)
+            typedef const __attribute__((address_space(4))) int32_t c_i32;
+            c_i32 *starts = (c_i32*)(uintptr_t)batch.query_start, *lens = (c_i32*)(uintptr_t)batch.context_len;
+            const int first = starts[0], last = starts[1];
+            seq.b = 0;
+            seq.ctx = lens[0];
+            seq.row0 = first;
+            seq.n = first < 0 || last > c.tokens || last < first ? 0 : last - first;
+            cut_sequence<TREE>(c, &seq);
+            up = x;
+        } else if (batch.seqs <= 64) {
             const int lane = threadIdx.x & 63;
             Seq s = {};
             if (lane < batch.seqs) read_sequence(c, batch, lane, &s);
