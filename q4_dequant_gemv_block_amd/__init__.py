@@ -1359,11 +1359,10 @@ def q4_tree_accept(batch: KVBatch, choice: torch.Tensor, draft: torch.Tensor, pa
     if t == 0:
         raise ValueError("no tokens")
     if out is None:
-        accepted, following, lens = torch.empty((3, b), dtype=i32, device=batch.device).unbind()
-        path = choice.new_empty((t,))
-        out = accepted, following, path, lens
-        ap = accepted.data_ptr()
-        np_, lp, rp = ap + 4 * b, ap + 8 * b, path.data_ptr()
+        made = choice.new_empty((3 * b + t,))
+        out = made.split_with_sizes((b, b, t, b))
+        ap = made.data_ptr()
+        np_, rp, lp = ap + 4 * b, ap + 8 * b, ap + 8 * b + 4 * t
     else:
         accepted, following, path, lens = out
         ap, np_, lp = _vector(accepted, i32, "accepted", b, dev), _vector(following, i32, "next_tokens", b, dev), _vector(lens, i32, "lens", b, dev)
