@@ -640,7 +640,8 @@ Q4_API q4_status q4_attention_paged(const q4_kv_cache* cache, const q4_kv_batch*
  *   q4_kv_append_norm  (q4_kv_append with norms of queries and keys) into the cache
  *   q4_attention_tree  each new token over the cached ones and its ancestors
  *   q4_logits_argmax   the pick behind each node under penalties and grammars
- *   q4_tree_accept     the path that the drafts share with the picks
+ *   q4_tree_accept     the path that the drafts share with the picks (q4_tree_accept_stored:
+ *                      of the nodes that have a place in the cache)
  *   q4_kv_move         the path's keys and values side by side in the cache
  *
  * Lengths, tables and paths stay in device memory, so the step can be one captured
@@ -686,10 +687,11 @@ typedef struct q4_kv_step {
  * sequences and of their places.  A sequence whose pages do not fit into what is
  * left gets none of them (and so does every later one that needs any): missing says
  * how many it lacks, held stays as it was, and the columns that lack a page are -1, so
- * that nothing is read or written through what stood there; what the step makes of its
- * rows does not count, they are to be repeated when there are pages.  Entries behind the pages
+ * that nothing is read or written through what stood there.  Entries behind the pages
  * a sequence needs are copied as they are; places behind the table's last column have
- * no page and do not count as missing.
+ * no page and do not count as missing.  What the step makes of a row whose slot is -1
+ * does not count, it is to be repeated when there is a page: q4_tree_accept_stored sees
+ * to that (rows in front, whose ancestors all have slots, are as they should be).
  *   slots     : of new token i, place past_len + i in the cache
  *   positions : past_len + i; with parents past_len + the number of its ancestors
  *   mask      : bit j of a row (bit j % 64 of word j / 64): j is the token itself or
@@ -837,6 +839,22 @@ Q4_API q4_status q4_tree_accept(const int32_t* query_start, const int32_t* conte
                                 const int32_t* choice, const int32_t* draft, const int32_t* parents, int64_t tokens,
                                 int32_t* accepted, int32_t* next, int32_t* path, int32_t* lens, int32_t* history,
                                 int64_t history_stride, int history_tokens, void* stream);
+
+/*
+ * q4_tree_accept for steps in which a sequence may lack pages, or have reached the end
+ * of its block table: a node whose slot is below 0 is not on the path, nor is anything
+ * behind it.
+ *   slots : NULL (every node is stored), or tokens int64, 8-byte aligned, as
+ *           q4_kv_assign writes them
+ * A sequence whose first new token has no slot takes nothing: accepted 0, lens without
+ * any new token, nothing in history, and next that token's own draft, so that the step
+ * after begins with it again.
+ */
+Q4_API q4_status q4_tree_accept_stored(const int32_t* query_start, const int32_t* context_len, int seqs,
+                                       const int32_t* choice, const int32_t* draft, const int32_t* parents,
+                                       const int64_t* slots, int64_t tokens, int32_t* accepted, int32_t* next,
+                                       int32_t* path, int32_t* lens, int32_t* history, int64_t history_stride,
+                                       int history_tokens, void* stream);
 
 /*
  * The keys and values of a path's nodes to the places behind each other that the path

@@ -47,7 +47,7 @@ EXPORTS = (
     "q4_0_gemv_batch", "q4_0_gemv_batch_handoff",
     "q4_rope", "q4_kv_append", "q4_attention_paged_workspace_bytes", "q4_attention_paged",
     "q4_kv_assign", "q4_norm_rope", "q4_kv_append_norm", "q4_attention_tree_workspace_bytes", "q4_attention_tree",
-    "q4_logits_argmax_workspace_bytes", "q4_logits_argmax", "q4_tree_accept", "q4_kv_move",
+    "q4_logits_argmax_workspace_bytes", "q4_logits_argmax", "q4_tree_accept", "q4_tree_accept_stored", "q4_kv_move",
 )
 
 Q4_TYPE_F16 = 0
@@ -214,6 +214,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.q4_logits_argmax.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, size, vp]
     lib.q4_tree_accept.restype = st
     lib.q4_tree_accept.argtypes = [vp, vp, i32, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i32, vp]
+    lib.q4_tree_accept_stored.restype = st
+    lib.q4_tree_accept_stored.argtypes = [vp, vp, i32, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i32, vp]
     lib.q4_kv_move.restype = st
     lib.q4_kv_move.argtypes = [vp, i32, vp, vp, vp, i64, vp]
     if path == LIB_PATH:
@@ -811,6 +813,7 @@ class KVBatch:
         self.device, self.gpu = block_table.device, block_table.get_device()
         self._keep = (block_table, query_start, context_lens)
         self.seqs = b
+        self.slots = None
         self.desc = BatchDesc(block_table.data_ptr(), block_table.stride(0), block_table.shape[1], b,
                               _vector(query_start, torch.int32, "query_start", b + 1, self.gpu),
                               _vector(context_lens, torch.int32, "context_lens", b, self.gpu),
@@ -960,6 +963,7 @@ class KVStep:
         self.mask = longs[tokens:].view(tokens, mask_words) if mask_words else None
         self.seqs, self.table_pages, self.page_size, self.tokens, self.mask_words = seqs, table_pages, page_size, tokens, mask_words
         self.batch = KVBatch(self.block_table, self.query_start, self.context_lens, max_query_len, max_context_len)
+        self.batch.slots = self.slots  # of this step's tokens: q4_tree_accept counts none without one
         self.device, self.gpu = self.batch.device, self.batch.gpu
         d = StepDesc()
         d.table, d.table_stride = self.block_table.data_ptr(), self.block_table.stride(0)
@@ -1333,17 +1337,20 @@ def q4_logits_argmax(logits: torch.Tensor, rules: LogitRules | None = None, out:
 
 
 def q4_tree_accept(batch: KVBatch, choice: torch.Tensor, draft: torch.Tensor, parents: torch.Tensor | None = None,
-                   history: torch.Tensor | None = None, out=None, stream=None):
+                   history: torch.Tensor | None = None, out=None, stream=None, slots: torch.Tensor | None = None):
     """(accepted [B], next_tokens [B], path [T], lens [B]), int32, of the trunk's choice behind each drafted token and
     the tokens themselves (int32 [T]): from each sequence's first new token the lowest child (parents as in
     q4_kv_assign; None: a chain) drafted as what was chosen, and so on.  accepted counts the path's tokens, the first
     included; next_tokens is the choice behind its last; path has their indices in the sequence's first rows, then -1;
     lens the context with them alone.  history (int32 [B, L]) receives the path's tokens at the places they have.
+    slots (int64 [T]; left out: those of the KVStep whose batch this is): tokens whose slot is below 0, for want of a page
+    or behind the table's end, are on no path; a sequence whose first one has none takes nothing (accepted 0), and its
+    next_tokens is that token again.
     T is at least 1.  out: the four tensors to write.  Rows of no sequence are left as they are (in a path made here: undefined)."""
     on = _on(batch.gpu, stream)
     if on is not None:
         with on:
-            return q4_tree_accept(batch, choice, draft, parents, history, out)
+            return q4_tree_accept(batch, choice, draft, parents, history, out, None, slots)
     dev, b, i32 = batch.gpu, batch.seqs, torch.int32
     cp = _vector(choice, i32, "choice", None, dev)
     t = choice.shape[0]
@@ -1367,9 +1374,14 @@ def q4_tree_accept(batch: KVBatch, choice: torch.Tensor, draft: torch.Tensor, pa
         accepted, following, path, lens = out
         ap, np_, lp = _vector(accepted, i32, "accepted", b, dev), _vector(following, i32, "next_tokens", b, dev), _vector(lens, i32, "lens", b, dev)
         rp = _vector(path, i32, "path", t, dev)
+    sp, rows = None, t
+    if slots is not None:
+        sp = _vector(slots, torch.int64, "slots", t, dev)
+    elif batch.slots is not None:  # (rows behind the step's are of no sequence)
+        sp, rows = batch.slots.data_ptr(), min(t, batch.slots.shape[0])
     d = batch.desc
-    status = (_lib or load_library()).q4_tree_accept(
-        d.query_start, d.context_len, b, cp, dp, pp, t, ap, np_, rp, lp, hp, hs, hn, _current_stream(dev))
+    status = (_lib or load_library()).q4_tree_accept_stored(
+        d.query_start, d.context_len, b, cp, dp, pp, sp, rows, ap, np_, rp, lp, hp, hs, hn, _current_stream(dev))
     if status:
         _check(status)
     return out

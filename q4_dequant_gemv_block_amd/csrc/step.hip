@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kThreads) k_assign(const AssignArgs a) {
 
 // A wave walks through one sequence's tree from its first new token: the child that
 // was drafted as what the trunk chose is the next, found with a ballot over the
-// nodes, 64 a register.
+// nodes, 64 a register.  Nodes without a slot are nobody's children: their keys and
+// values were not stored, so neither they nor what was chosen behind them may count.
 constexpr int kHold = 4;  // registers of nodes; longer trees are read again for every step
 
 __global__ void __launch_bounds__(kThreads) k_accept(const AcceptArgs a) {
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(kThreads) k_accept(const AcceptArgs a) {
     const int n = first < 0 || last > a.tokens || last < first ? 0 : last - first;
     const int past = context - max(last - first, 0);
     const int32_t *choice = a.choice + first, *draft = a.draft + first, *parents = a.parents ? a.parents + first : nullptr;
+    const int64_t* slots = a.slots ? a.slots + first : nullptr;
     int cur = 0, count = 0;
     int mine[kHold], token[kHold];  // nodes of the path at 64 k + lane, and their tokens
     int p[kHold], d[kHold], c[kHold];
@@ -169,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) k_accept(const AcceptArgs a) {
             p[k] = parents ? parents[i] : i - 1;
             d[k] = draft[i];
             c[k] = choice[i];
+            if (slots && slots[i] < 0) p[k] = -1;
         }
     }
     auto write = [&](int j, int node, int tok) {
@@ -179,7 +182,9 @@ __global__ void __launch_bounds__(kThreads) k_accept(const AcceptArgs a) {
     int chosen = -1;
     if (n) {
         int tok = held ? __builtin_amdgcn_readlane(d[0], 0) : draft[0];
-        for (;;) {
+        const bool stored = !slots || slots[0] >= 0;
+        if (!stored) chosen = tok;  // the step again, from the same token
+        while (stored) {
             // node `cur` is the path's next
             if (held) {
 #pragma unroll
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) k_accept(const AcceptArgs a) {
                 chosen = choice[cur];
                 for (int at = (cur + 1) & ~63; at < n && next < 0; at += 64) {
                     const int i = at + lane;
-                    const bool in = i > cur && i < n;
+                    const bool in = i > cur && i < n && (!slots || slots[i] >= 0);
                     const int parent = in ? (parents ? parents[i] : i - 1) : -1;
                     const uint64_t is = __ballot(in && parent == cur && draft[in ? i : cur] == chosen && chosen >= 0);
                     if (is) next = at + (int)__builtin_ctzll(is);

@@ -44,6 +44,27 @@ q4_status check_apart(const char* fn, std::initializer_list<Named> written, std:
 constexpr int kMaxWords = 16;
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 
+q4_status accept(const char* fn, const char* what, const int32_t* query_start, const int32_t* context_len, int seqs, const int32_t* choice,
+                 const int32_t* draft, const int32_t* parents, const int64_t* slots, int64_t tokens, int32_t* accepted, int32_t* next,
+                 int32_t* path, int32_t* lens, int32_t* history, int64_t history_stride, int history_tokens, void* stream) {
+    if (seqs < 1 || seqs > kMaxRows) return fail(Q4_ERR_INVALID_ARG, "%s: seqs = %d outside [1, 2^24]", fn, seqs);
+    if (tokens < 1 || tokens > kMaxTokens) return fail(Q4_ERR_INVALID_ARG, "%s: tokens = %lld outside [1, %lld]", fn, (long long)tokens, (long long)kMaxTokens);
+    if (history && (history_tokens < 1 || history_stride < 0 || history_stride > kMaxStride || (seqs > 1 && history_stride < history_tokens)))
+        return fail(Q4_ERR_INVALID_ARG, "%s: history_tokens = %d must be at least 1 and history_stride no smaller", fn, history_tokens);
+    const Named start = {"query_start", ints(query_start, (int64_t)seqs + 1), 4, false}, context = {"context_len", ints(context_len, seqs), 4, false};
+    const Named c = {"choice", ints(choice, tokens), 4, false}, d = {"draft", ints(draft, tokens), 4, false}, p = {"parents", ints(parents, tokens), 4, true};
+    const Named sl = {"slots", span(slots, slots ? 8 * (uint64_t)tokens : 0), 8, true};
+    const Named acc = {"accepted", ints(accepted, seqs), 4, false}, nx = {"next", ints(next, seqs), 4, false};
+    const Named pa = {"path", ints(path, tokens), 4, false}, le = {"lens", ints(lens, seqs), 4, false};
+    const Named hi = {"history", rows(history, seqs, history_stride, history_tokens, 4), 4, true};
+    q4_status st = check_tensors(fn, {start, context, c, d, p, sl, acc, nx, pa, le, hi});
+    if (!st) st = check_apart(fn, {acc, nx, pa, le, hi}, {start, context, c, d, p, sl});
+    if (st) return st;
+    const q4::AcceptArgs a = {query_start, context_len, choice, draft, parents, slots, accepted, next, path, lens,
+                              history, seqs > 1 ? history_stride : 0, history_tokens, seqs, tokens};
+    return hip_status(q4::launch_accept(a, static_cast<hipStream_t>(stream)), what);
+}
+
 }  // namespace
 
 extern "C" {
@@ -214,22 +235,16 @@ q4_status q4_logits_argmax(const void* logits, int type, int64_t row_stride, int
 q4_status q4_tree_accept(const int32_t* query_start, const int32_t* context_len, int seqs, const int32_t* choice, const int32_t* draft,
                          const int32_t* parents, int64_t tokens, int32_t* accepted, int32_t* next, int32_t* path, int32_t* lens,
                          int32_t* history, int64_t history_stride, int history_tokens, void* stream) {
-    const char* fn = "q4_tree_accept";
-    if (seqs < 1 || seqs > kMaxRows) return fail(Q4_ERR_INVALID_ARG, "%s: seqs = %d outside [1, 2^24]", fn, seqs);
-    if (tokens < 1 || tokens > kMaxTokens) return fail(Q4_ERR_INVALID_ARG, "%s: tokens = %lld outside [1, %lld]", fn, (long long)tokens, (long long)kMaxTokens);
-    if (history && (history_tokens < 1 || history_stride < 0 || history_stride > kMaxStride || (seqs > 1 && history_stride < history_tokens)))
-        return fail(Q4_ERR_INVALID_ARG, "%s: history_tokens = %d must be at least 1 and history_stride no smaller", fn, history_tokens);
-    const Named start = {"query_start", ints(query_start, (int64_t)seqs + 1), 4, false}, context = {"context_len", ints(context_len, seqs), 4, false};
-    const Named c = {"choice", ints(choice, tokens), 4, false}, d = {"draft", ints(draft, tokens), 4, false}, p = {"parents", ints(parents, tokens), 4, true};
-    const Named acc = {"accepted", ints(accepted, seqs), 4, false}, nx = {"next", ints(next, seqs), 4, false};
-    const Named pa = {"path", ints(path, tokens), 4, false}, le = {"lens", ints(lens, seqs), 4, false};
-    const Named hi = {"history", rows(history, seqs, history_stride, history_tokens, 4), 4, true};
-    q4_status st = check_tensors(fn, {start, context, c, d, p, acc, nx, pa, le, hi});
-    if (!st) st = check_apart(fn, {acc, nx, pa, le, hi}, {start, context, c, d, p});
-    if (st) return st;
-    const q4::AcceptArgs a = {query_start, context_len, choice, draft, parents, accepted, next, path, lens,
-                              history, seqs > 1 ? history_stride : 0, history_tokens, seqs, tokens};
-    return hip_status(q4::launch_accept(a, static_cast<hipStream_t>(stream)), "q4_tree_accept launch");
+    return accept("q4_tree_accept", "q4_tree_accept launch", query_start, context_len, seqs, choice, draft, parents, nullptr, tokens, accepted,
+                  next, path, lens, history, history_stride, history_tokens, stream);
+}
+
+q4_status q4_tree_accept_stored(const int32_t* query_start, const int32_t* context_len, int seqs, const int32_t* choice,
+                                const int32_t* draft, const int32_t* parents, const int64_t* slots, int64_t tokens, int32_t* accepted,
+                                int32_t* next, int32_t* path, int32_t* lens, int32_t* history, int64_t history_stride,
+                                int history_tokens, void* stream) {
+    return accept("q4_tree_accept_stored", "q4_tree_accept_stored launch", query_start, context_len, seqs, choice, draft, parents, slots,
+                  tokens, accepted, next, path, lens, history, history_stride, history_tokens, stream);
 }
 
 q4_status q4_kv_move(const q4_kv_cache* caches, int layers, const q4_kv_batch* batch, const int32_t* path, const int32_t* accepted,

@@ -39,6 +39,7 @@ struct AcceptArgs {
     const int32_t* choice;
     const int32_t* draft;
     const int32_t* parents;    // null: a chain
+    const int64_t* slots;      // null: every node has one
     int32_t* accepted;
     int32_t* next;
     int32_t* path;
