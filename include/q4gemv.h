@@ -698,8 +698,8 @@ typedef struct q4_kv_step {
  *               an ancestor of it; without parents each token follows the one before.
  *               With parents, new tokens from the 64 mask_words-th on (the 1024th
  *               without mask) have no bits and no ancestors.
- * Rows behind the last sequence's are left as they are, rows behind `tokens` are not
- * written.  Lengths below 0 count as 0, those above 2^30 as 2^30, held_in is taken
+ * Rows behind the last sequence's are left as they are (what walks over slots by itself
+ * ends at query_start[seqs], or clears them first), rows behind `tokens` are not written.  Lengths below 0 count as 0, those above 2^30 as 2^30, held_in is taken
  * as at most table_pages.  Nothing that is written overlaps anything else here,
  * except the table in place.  Deterministic.
  */

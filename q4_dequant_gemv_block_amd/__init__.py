@@ -936,7 +936,8 @@ class KVStep:
     context_lens [B], missing [B], free_count [1] and positions [T], int32, slots [T] and, with mask_words > 0, mask
     [T, mask_words], int64; and `batch`, the KVBatch of them.  The last step's tables (block_table, held, free_count)
     are the next one's inputs, so a program keeps two of these and takes them in turn.  table: a tensor [B, P] to
-    write the block table to instead of one of its own (say the one it is read from)."""
+    write the block table to instead of one of its own (say the one it is read from).  Rows of slots, positions and mask
+    behind a step's last token (query_start[B]) keep what an earlier step left there; at first they are -1, 0 and 0."""
 
     def __init__(self, seqs: int, table_pages: int, page_size: int, tokens: int, mask_words: int = 0,
                  max_query_len: int | None = None, max_context_len: int | None = None,
@@ -959,7 +960,7 @@ class KVStep:
             whole[at : at + n] for at, n in zip(starts, sizes))
         self.block_table = table if table is not None else torch.zeros((seqs, table_pages), dtype=torch.int32, device=device)
         longs = torch.zeros((tokens, 1 + mask_words), dtype=torch.int64, device=device).view(-1)
-        self.slots = longs[:tokens]
+        self.slots = longs[:tokens].fill_(-1)  # no row has a place yet
         self.mask = longs[tokens:].view(tokens, mask_words) if mask_words else None
         self.seqs, self.table_pages, self.page_size, self.tokens, self.mask_words = seqs, table_pages, page_size, tokens, mask_words
         self.batch = KVBatch(self.block_table, self.query_start, self.context_lens, max_query_len, max_context_len)

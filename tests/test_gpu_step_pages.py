@@ -232,3 +232,15 @@ def test_slots_of_a_step():
         q4.q4_tree_accept(step.batch, choice, draft, slots=step.slots)  # fewer slots than rows
     with pytest.raises(TypeError):
         q4.q4_tree_accept(step.batch, choice[:8], draft[:8], slots=i32([0] * 8))
+
+
+def test_a_new_step_has_no_slots():
+    """Rows that no step wrote yet name no place of the cache (0 is one), also where the first steps are shorter."""
+    q4 = lib()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for words in (0, 1, 3):
+        step = q4.KVStep(2, 2, 16, 9, words)
+        assert step.slots.tolist() == [-1] * 9 and step.positions.tolist() == [0] * 9
+        assert words == 0 or not step.mask.any()
+        q4.q4_kv_assign(step, i32([[0, 5], [1, 6]]), i32([1, 1]), i32([3, 0]), i32([2, 1]), i32([9]), i32([1]))
+        assert step.slots.tolist() == [3, 4, 16] + [-1] * 6
