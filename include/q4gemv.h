@@ -789,7 +789,9 @@ typedef struct q4_logit_rules {
                                    allowed; NULL: its own number */
 } q4_logit_rules;
 
-/* Bytes of device workspace q4_logits_argmax needs (0: none, or sizes that are not valid). */
+/* Bytes of device workspace for q4_logits_argmax (0: none, or sizes that are not valid):
+ * enough for every call of up to so many rows and entries, so one that is made for the
+ * largest batch serves all. */
 Q4_API size_t q4_logits_argmax_workspace_bytes(int64_t rows, int64_t vocab);
 
 /*

@@ -1271,7 +1271,7 @@ class LogitRules:
 
 
 def logits_argmax_workspace_bytes(rows: int, vocab: int) -> int:
-    """Bytes of the workspace q4_logits_argmax needs (0: none)."""
+    """Bytes of workspace for q4_logits_argmax (0: none), enough for every call of up to so many rows and entries."""
     return int(load_library().q4_logits_argmax_workspace_bytes(rows, vocab))
 
 

@@ -396,8 +396,8 @@ hipError_t launch_type(const LogitArgs& a, hipStream_t s) {
 // of 2048, 6.8 of 8192), many pay for each slice's scan of the history (37 rows of trees
 // 23 against 15 us, 192 rows of 4096 tokens 124 against 66).
 int64_t logit_slice(int64_t rows, int64_t vocab) {
-    int64_t slice = 2048;
-    while (slice < 8192 && rows * ((vocab + slice - 1) / slice) > 512) slice *= 2;
+    int64_t slice = kLogitShort;
+    while (slice < kLogitLong && rows * ((vocab + slice - 1) / slice) > kLogitFew) slice *= 2;
     return slice;
 }
 

@@ -4,6 +4,7 @@
 #include "kv_checks.h"
 #include "step_launch.h"
 
+#include <algorithm>
 #include <initializer_list>
 
 using namespace q4::check;
@@ -132,10 +133,16 @@ q4_status q4_kv_assign(const q4_kv_step* x, void* stream) {
     return hip_status(q4::launch_assign(a, static_cast<hipStream_t>(stream)), "q4_kv_assign launch");
 }
 
+// No fewer for more rows or entries, so that what was made for the largest call serves all:
+// slices shorter than the longest are taken where a call has no more than kLogitFew of
+// them, the longest ones' number grows with both sizes.
 size_t q4_logits_argmax_workspace_bytes(int64_t n, int64_t vocab) {
     if (n < 1 || n > kMaxRows || vocab < 1 || vocab > kMaxRows) return 0;
-    const int64_t slice = q4::logit_slice(n, vocab), slices = (vocab + slice - 1) / slice;
-    return slices > 1 ? (size_t)n * slices * q4::kLogitKeys * 8 : 0;
+    auto slices = [&](int64_t slice) { return (vocab + slice - 1) / slice; };
+    if (slices(q4::kLogitShort) == 1) return 0;
+    const int64_t few = std::min<int64_t>(n * slices(q4::kLogitShort), q4::kLogitFew);
+    const int64_t many = slices(q4::kLogitLong) > 1 ? n * slices(q4::kLogitLong) : 0;
+    return (size_t)std::max(few, many) * q4::kLogitKeys * 8;
 }
 
 q4_status q4_logits_argmax(const void* logits, int type, int64_t row_stride, int64_t n, int64_t vocab, const q4_logit_rules* r,
@@ -150,7 +157,8 @@ q4_status q4_logits_argmax(const void* logits, int type, int64_t row_stride, int
     if (out && n > 1 && out_stride < vocab) return fail(Q4_ERR_INVALID_ARG, "%s: the rows of out overlap each other", fn);
     const Named in = {"logits", rows(logits, n, row_stride, vocab, b), b, false};
     const Named res = {"out", rows(out, n, out_stride, vocab, 4), 4, true}, tok = {"tokens", ints(tokens, n), 4, false};
-    const size_t need = q4_logits_argmax_workspace_bytes(n, vocab);
+    const int64_t slice = q4::logit_slice(n, vocab), slices = (vocab + slice - 1) / slice;
+    const size_t need = slices > 1 ? (size_t)n * slices * q4::kLogitKeys * 8 : 0;
     const Named ws = {"workspace", span(workspace, workspace ? need : 0), 8, true};
     q4_status st = check_tensors(fn, {in, res, tok});
     if (st) return st;

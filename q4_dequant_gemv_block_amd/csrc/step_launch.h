@@ -94,6 +94,8 @@ struct LogitArgs {
     int64_t allowed_stride, allowed_rows;
     const int32_t* allowed_row;
 };
+constexpr int64_t kLogitShort = 2048, kLogitLong = 8192;  // logits of a slice
+constexpr int64_t kLogitFew = 512;                        // slices of a call for which one shorter than kLogitLong is taken
 // Logits of one slice of a row: a rule on sizes, the same for the workspace and the launch.
 int64_t logit_slice(int64_t rows, int64_t vocab);
 hipError_t launch_logits(LogitArgs a, int type, hipStream_t s);

@@ -1,8 +1,9 @@
-"""Refusals of q4_tree_accept_stored: every call here fails on the host before anything would be enqueued, with made-up
-addresses."""
+"""Refusals of q4_tree_accept_stored, and workspaces made for the largest call: every call here fails on the host before
+anything would be enqueued, with made-up addresses."""
 import pytest
 
-from test_kv_cpu import BASE, GIB, lib, refused  # noqa: F401
+import q4_dequant_gemv_block_amd as q4
+from test_kv_cpu import BASE, GIB, lib, ref, refused  # noqa: F401
 
 NAMES = dict(query_start=1, context_len=2, choice=3, draft=4, parents=5, accepted=6, next=7, path=8, lens=9, history=10, slots=11)
 OUTPUTS = ("accepted", "next", "path", "lens", "history")
@@ -22,3 +23,24 @@ def test_refusals(lib, over, want, text):
                                    a["tokens"], a["accepted"], a["next"], a["path"], a["lens"], a["history"], a["history_stride"],
                                    a["history_tokens"], None)
     refused(lib, st, want, text)
+
+
+def enough_for_logits(lib, rows, vocab, given):
+    """Whether a workspace of `given` bytes serves a call (which then fails on its rules)."""
+    st = lib.q4_logits_argmax(BASE, q4.Q4_TYPE_F32, vocab, rows, vocab, ref(q4.RulesDesc(seqs=0)), None, 0, BASE - GIB, BASE - 64 * GIB, given,
+                              None)
+    assert st == -3 or (st == -1 and "seqs" in q4.last_error()), q4.last_error()
+    return st == -1
+
+
+@pytest.mark.parametrize("vocab", [1, 2048, 2049, 8192, 8193, 32000, 50021, 151936, 1 << 24])
+def test_a_logits_workspace_serves_fewer_rows(lib, vocab):
+    """A workspace for so many rows and entries serves every call of fewer rows, or fewer entries."""
+    sizes = [*range(1, 70), 127, 128, 129, 255, 256, 257, 511, 512, 513, 1000, 4097, 70001]
+    for rows in sizes:
+        given = q4.logits_argmax_workspace_bytes(rows, vocab)
+        assert given >= q4.logits_argmax_workspace_bytes(max(rows - 1, 1), vocab)
+        for fewer in sizes:
+            if fewer <= rows:
+                for v in (vocab, vocab // 2, vocab // 3, 9000, 2049):
+                    assert not 1 <= v <= vocab or enough_for_logits(lib, fewer, v, given), (rows, fewer, v)
