@@ -598,7 +598,8 @@ Q4_API q4_status q4_kv_append(const q4_kv_cache* cache, const q4_kv_batch* batch
 
 /* Bytes of device workspace q4_attention_paged needs; 0 if none, or, with the
  * error text set, if the arguments are not valid.  It depends on these sizes, on
- * batch->max_query and max_context and on the current device, not on lengths. */
+ * batch->max_query and max_context and on the current device, not on lengths, and may
+ * be larger for smaller sizes (q4_attention_workspace_most). */
 Q4_API size_t q4_attention_paged_workspace_bytes(const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads,
                                                  int64_t tokens, int64_t window);
 
@@ -734,9 +735,17 @@ Q4_API q4_status q4_kv_append_norm(const q4_kv_cache* cache, const q4_kv_batch* 
                                    const int32_t* positions, const double* inv_freq, int rot_dim, int layout,
                                    float mscale, void* stream);
 
-/* As q4_attention_paged_workspace_bytes, for q4_attention_tree. */
+/* As q4_attention_paged_workspace_bytes, for q4_attention_tree (and as little a bound for
+ * smaller sizes). */
 Q4_API size_t q4_attention_tree_workspace_bytes(const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads,
                                                 int64_t tokens, int64_t window);
+
+/* Bytes of device workspace that serve every call of q4_attention_paged and
+ * q4_attention_tree with up to `tokens` new tokens over such a cache (its heads, their
+ * head_dim and q_heads), whatever its sequences, lengths, hints and window, on the
+ * current device: what a program that makes one workspace for all its steps needs (at
+ * most 68 MB on 256 CUs).  0, with the error text set, if the arguments are not valid. */
+Q4_API size_t q4_attention_workspace_most(const q4_kv_cache* cache, int q_heads, int64_t tokens);
 
 /*
  * q4_attention_paged where the new tokens of a sequence are a tree (q4_kv_batch's

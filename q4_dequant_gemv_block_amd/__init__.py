@@ -47,6 +47,7 @@ EXPORTS = (
     "q4_0_gemv_batch", "q4_0_gemv_batch_handoff",
     "q4_rope", "q4_kv_append", "q4_attention_paged_workspace_bytes", "q4_attention_paged",
     "q4_kv_assign", "q4_norm_rope", "q4_kv_append_norm", "q4_attention_tree_workspace_bytes", "q4_attention_tree",
+    "q4_attention_workspace_most",
     "q4_logits_argmax_workspace_bytes", "q4_logits_argmax", "q4_tree_accept", "q4_tree_accept_stored", "q4_kv_move",
 )
 
@@ -206,6 +207,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.q4_kv_append_norm.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, vp, vp, i32, f32, vp, vp, i32, i32, f32, vp]
     lib.q4_attention_tree_workspace_bytes.restype = size
     lib.q4_attention_tree_workspace_bytes.argtypes = [vp, vp, i32, i64, i64]
+    lib.q4_attention_workspace_most.restype = size
+    lib.q4_attention_workspace_most.argtypes = [vp, i32, i64]
     lib.q4_attention_tree.restype = st
     lib.q4_attention_tree.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i64, f32, i64, vp, size, vp]
     lib.q4_logits_argmax_workspace_bytes.restype = size
@@ -875,12 +878,25 @@ def q4_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
 
 
 def attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, tokens: int, window: int = 0) -> int:
-    """Bytes of the workspace q4_attention_paged needs for these sizes (0: none)."""
+    """Bytes of the workspace q4_attention_paged needs for these sizes (0: none); smaller sizes may need more
+    (attention_workspace_most)."""
     if tokens == 0:
         return 0
     with torch.cuda.device(cache.device):  # the work is cut for this device
         n = int(load_library().q4_attention_paged_workspace_bytes(cache._ref, batch._ref, q_heads, tokens, window))
     if n == 0 and last_error():
+        raise Q4Error(Q4_ERR_INVALID_ARG, last_error())
+    return n
+
+
+def attention_workspace_most(cache: KVCache, q_heads: int, tokens: int) -> int:
+    """Bytes of a workspace for every call of q4_attention_paged and q4_attention_tree with up to `tokens` new tokens over
+    such a cache, whatever its batch and window."""
+    if tokens == 0:
+        return 0
+    with torch.cuda.device(cache.device):
+        n = int(load_library().q4_attention_workspace_most(cache._ref, q_heads, tokens))
+    if n == 0:
         raise Q4Error(Q4_ERR_INVALID_ARG, last_error())
     return n
 
@@ -1123,7 +1139,8 @@ def _mask(mask: torch.Tensor, rows: int, gpu: int) -> int:
 
 
 def attention_tree_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, tokens: int, window: int = 0) -> int:
-    """Bytes of the workspace q4_attention_tree needs for these sizes (0: none)."""
+    """Bytes of the workspace q4_attention_tree needs for these sizes (0: none); smaller sizes may need more
+    (attention_workspace_most)."""
     if tokens == 0:
         return 0
     with torch.cuda.device(cache.device):  # the work is cut for this device

@@ -86,6 +86,8 @@ AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t 
     return attn_shape_on(compute_units(), c, b, q_heads, tokens, window, max_query, max_context, tree);
 }
 
+size_t attn_most_bytes(int head_dim, int64_t rows) { return attn_workspace_most(compute_units(), head_dim, rows); }
+
 hipError_t launch_attention(const AttnArgs& a, const AttnShape& shape, int type, hipStream_t s) {
     return type == Q4_TYPE_F16 ? launch_type<F16>(a, shape, s) : launch_type<BF16>(a, shape, s);
 }

@@ -44,6 +44,29 @@ inline TreeCost tree_cost(int rows, int head_dim) {
     return {0.533, tile, 0.906, 0.166, 9.65, 1.302, 0.921};
 }
 
+// Workgroups that the machine holds at a time, and the workspace of as many with parts.
+inline int attn_slots(int cus, int rows, int head_dim) { return rows <= 32 || rows == 256 || head_dim > 128 ? cus : 2 * cus; }
+inline size_t attn_parts_bytes(int grid, int rows, int head_dim) {
+    return (size_t)2 * grid * rows * (head_dim * sizeof(float) + 2 * sizeof(float));
+}
+inline bool attn_rows_256(int head_dim) { return head_dim == 96 || head_dim == 128; }  // items of 256 rows, of trees
+
+// The most that a call with up to `most` query rows of a kv head takes.  (One call's need
+// is not such a bound: fewer rows or keys may be cut where more are taken whole, and into
+// larger items.)
+inline size_t attn_workspace_most(int cus, int head_dim, int64_t most) {
+    size_t bytes = 0;
+    auto consider = [&](int rows, bool taken) {
+        if (taken) bytes = std::max(bytes, attn_parts_bytes(attn_slots(cus, rows, head_dim), rows, head_dim));
+    };
+    consider(16, true);
+    consider(32, most > 16);
+    consider(64, most > 32);
+    consider(128, most > 32);
+    consider(256, most > 128 && attn_rows_256(head_dim));
+    return bytes;
+}
+
 // How a call is cut: the rows of an item, and whether items are taken whole or
 // in parts.  Parts cost a launch that waits for the first one (measured 5 to 7
 // us), their way to memory and back at about 4 TB/s, and in tiles the L2: whole
@@ -78,7 +101,7 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
         s.step = rows <= 32 ? kAttnStep : 64;
         s.unit = 64;
         s.most_rows = (int)std::min<int64_t>(rows, most);
-        const int slots = rows <= 32 || rows == 256 || c.head_dim > 128 ? cus : 2 * cus;
+        const int slots = attn_slots(cus, rows, c.head_dim);
         // keys of an item, the part of them that its sequence's items see on average, and all items
         const int64_t keys = window ? std::min<int64_t>(context, (int64_t)window + (tree ? longest : (rows - 1) / group) + 2) : context;
         const int64_t past = std::max<int64_t>(context - longest, 0);
@@ -117,7 +140,7 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
             while (s.unit < (1 << 30) && bound * (capacity / s.unit + 1) >= (int64_t(1) << 31)) s.unit *= 2;
             s.grid = slots;
             s.few = items * 8 <= slots;
-            s.bytes = (size_t)2 * s.grid * s.rows * (c.head_dim * sizeof(float) + 2 * sizeof(float));
+            s.bytes = attn_parts_bytes(s.grid, s.rows, c.head_dim);
         }
         const double taken = rows <= 128 ? std::min(whole, cut) : cut;  // items of 256 are not taken whole
         if (!best.rows || taken < best_cost) {
@@ -131,7 +154,7 @@ inline AttnShape attn_shape_on(int cus, const CacheArg& c, const BatchArg& b, in
         if (tree && most <= 128) consider(32);
         consider(64);
         consider(128);
-        if (tree && most > 128 && (c.head_dim == 96 || c.head_dim == 128)) consider(256);
+        if (tree && most > 128 && attn_rows_256(c.head_dim)) consider(256);
     }
     return best;
 }

@@ -244,6 +244,13 @@ size_t q4_attention_tree_workspace_bytes(const q4_kv_cache* cache, const q4_kv_b
     return q4::attn_shape(cache_arg(*cache), batch_arg(*batch), q_heads, tokens, window_arg(window), batch->max_query, batch->max_context, true).bytes;
 }
 
+size_t q4_attention_workspace_most(const q4_kv_cache* cache, int q_heads, int64_t tokens) {
+    const char* fn = "q4_attention_workspace_most";
+    if (check_cache(fn, cache) || check_attention_sizes(fn, cache, q_heads, tokens)) return 0;
+    ok();
+    return q4::attn_most_bytes(cache->head_dim, tokens * (q_heads / cache->kv_heads));
+}
+
 q4_status q4_attention_paged(const q4_kv_cache* cache, const q4_kv_batch* batch, const q4_heads* q, const q4_heads* out,
                              float* lse, int q_heads, int64_t tokens, float scale, int64_t window, void* workspace,
                              size_t workspace_bytes, void* stream) {

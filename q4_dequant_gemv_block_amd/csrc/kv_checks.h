@@ -239,17 +239,24 @@ inline q4::BatchArg batch_arg(const q4_kv_batch& b) {
     return q4::BatchArg{b.block_table, b.table_stride, b.table_pages, b.seqs, b.query_start, b.context_len};
 }
 
+// Heads and tokens of attention over a cache that is checked.
+inline q4_status check_attention_sizes(const char* fn, const q4_kv_cache* cache, int q_heads, int64_t tokens) {
+    const q4_status st = check_sizes(fn, tokens, q_heads, cache->head_dim);
+    if (st) return st;
+    if (!q4::attn_head_dim_ok(cache->head_dim)) return fail(Q4_ERR_INVALID_ARG, "%s: head_dim = %d must be 64, 96, 128 or 256", fn, cache->head_dim);
+    if (q_heads % cache->kv_heads) return fail(Q4_ERR_INVALID_ARG, "%s: q_heads = %d must be a multiple of kv_heads = %d", fn, q_heads, cache->kv_heads);
+    if (tokens * q_heads > (int64_t(1) << 30)) return fail(Q4_ERR_INVALID_ARG, "%s: more than 2^30 query rows", fn);
+    return Q4_OK;
+}
+
 inline q4_status check_attention(const char* fn, const q4_kv_cache* cache, const q4_kv_batch* batch, int q_heads, int64_t tokens,
                           int64_t window) {
     q4_status st = check_cache(fn, cache);
     if (st) return st;
     st = check_batch(fn, batch, cache);
     if (st) return st;
-    st = check_sizes(fn, tokens, q_heads, cache->head_dim);
+    st = check_attention_sizes(fn, cache, q_heads, tokens);
     if (st) return st;
-    if (!q4::attn_head_dim_ok(cache->head_dim)) return fail(Q4_ERR_INVALID_ARG, "%s: head_dim = %d must be 64, 96, 128 or 256", fn, cache->head_dim);
-    if (q_heads % cache->kv_heads) return fail(Q4_ERR_INVALID_ARG, "%s: q_heads = %d must be a multiple of kv_heads = %d", fn, q_heads, cache->kv_heads);
-    if (tokens * q_heads > (int64_t(1) << 30)) return fail(Q4_ERR_INVALID_ARG, "%s: more than 2^30 query rows", fn);
     if (!aligned(cache->k, 16) || !aligned(cache->v, 16)) return fail(Q4_ERR_MISALIGNED, "%s: the cache must be 16-byte aligned", fn);
     const q4::CacheArg c = cache_arg(*cache);
     if ((c.k_page | c.k_head | c.k_slot | c.v_page | c.v_head | c.v_slot) % 8)
@@ -259,7 +266,6 @@ inline q4_status check_attention(const char* fn, const q4_kv_cache* cache, const
     if (window < 0) return fail(Q4_ERR_INVALID_ARG, "%s: window must not be negative", fn);
     return Q4_OK;
 }
-
 
 }  // namespace check
 }  // namespace q4

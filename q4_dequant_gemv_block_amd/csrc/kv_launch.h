@@ -123,6 +123,7 @@ struct AttnShape {
 };
 bool attn_head_dim_ok(int head_dim);
 AttnShape attn_shape(const CacheArg& c, const BatchArg& b, int q_heads, int64_t tokens, int window, int max_query, int max_context, bool tree = false);
+size_t attn_most_bytes(int head_dim, int64_t rows);  // that any call with up to so many rows of a kv head takes
 hipError_t launch_attention_tree(const TreeArgs& a, const AttnShape& shape, int type, hipStream_t s);
 hipError_t launch_attention(const AttnArgs& a, const AttnShape& shape, int type, hipStream_t s);
 

@@ -3,7 +3,7 @@ anything would be enqueued, with made-up addresses."""
 import pytest
 
 import q4_dequant_gemv_block_amd as q4
-from test_kv_cpu import BASE, GIB, lib, ref, refused  # noqa: F401
+from test_kv_cpu import BASE, GIB, batch, cache, lib, ref, refused  # noqa: F401
 
 NAMES = dict(query_start=1, context_len=2, choice=3, draft=4, parents=5, accepted=6, next=7, path=8, lens=9, history=10, slots=11)
 OUTPUTS = ("accepted", "next", "path", "lens", "history")
@@ -44,3 +44,31 @@ def test_a_logits_workspace_serves_fewer_rows(lib, vocab):
             if fewer <= rows:
                 for v in (vocab, vocab // 2, vocab // 3, 9000, 2049):
                     assert not 1 <= v <= vocab or enough_for_logits(lib, fewer, v, given), (rows, fewer, v)
+
+
+SIZES = [1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 24, 31, 32, 33, 40, 63, 64, 65, 100, 127, 128, 129, 200, 513, 2048, 9000]
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("q_heads", [2, 8, 14, 40])
+def test_an_attention_workspace_serves_fewer_tokens(lib, dim, q_heads):
+    """attention_workspace_most covers every batch of up to so many new tokens, whatever its sequences, lengths, hints and
+    window, of both kinds of attention, and is no more than the most that one of them takes."""
+    c = cache(head_dim=dim, pages=9000)
+    most = {n: lib.q4_attention_workspace_most(ref(c), q_heads, n) for n in SIZES}
+    needed = 0
+    for n in SIZES:
+        for pages in (1, 4, 40, 400, 4000):
+            for seqs in (1, 2, 3, 16, 64, 65, 300):
+                for query in (0, 1, n // 2, n):
+                    for context in (0, pages * 9):
+                        for window in (0, 100, 4000):
+                            b = batch(table_pages=pages, table_stride=pages, seqs=seqs, max_query=query, max_context=context)
+                            for fn in (lib.q4_attention_paged_workspace_bytes, lib.q4_attention_tree_workspace_bytes):
+                                needed = max(needed, fn(ref(c), ref(b), q_heads, n, window))
+        assert needed <= most[n], n  # of this many or fewer
+    assert needed == most[SIZES[-1]]
+    assert lib.q4_attention_workspace_most(ref(c), q_heads, 0) == 0 and "tokens" in q4.last_error()
+    assert lib.q4_attention_workspace_most(ref(c), 7, 4) == 0 and "multiple of kv_heads" in q4.last_error()
+    assert lib.q4_attention_workspace_most(ref(cache(head_dim=80)), q_heads, 4) == 0 and "head_dim" in q4.last_error()
+    assert lib.q4_attention_workspace_most(None, q_heads, 4) == 0 and "null cache" in q4.last_error()
