@@ -1133,7 +1133,7 @@ def _mask(mask: torch.Tensor, rows: int, gpu: int) -> int:
         raise TypeError("mask must be int64, got %s" % mask.dtype)
     if mask.get_device() != gpu:
         raise ValueError("mask must be on GPU %d, is on %s" % (gpu, mask.device))
-    if mask.dim() != 2 or mask.shape[0] != rows or not mask.is_contiguous():
+    if mask.dim() != 2 or mask.shape[0] != rows or mask.shape[1] < 1 or not mask.is_contiguous():
         raise ValueError("mask must be contiguous, [%d, words]" % rows)
     return mask.data_ptr()
 

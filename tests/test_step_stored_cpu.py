@@ -1,6 +1,7 @@
 """Refusals of q4_tree_accept_stored, and workspaces made for the largest call: every call here fails on the host before
 anything would be enqueued, with made-up addresses."""
 import pytest
+import torch
 
 import q4_dequant_gemv_block_amd as q4
 from test_kv_cpu import BASE, GIB, batch, cache, lib, ref, refused  # noqa: F401
@@ -72,3 +73,11 @@ def test_an_attention_workspace_serves_fewer_tokens(lib, dim, q_heads):
     assert lib.q4_attention_workspace_most(ref(c), 7, 4) == 0 and "multiple of kv_heads" in q4.last_error()
     assert lib.q4_attention_workspace_most(ref(cache(head_dim=80)), q_heads, 4) == 0 and "head_dim" in q4.last_error()
     assert lib.q4_attention_workspace_most(None, q_heads, 4) == 0 and "null cache" in q4.last_error()
+
+
+def test_masks_have_words():
+    """A mask of no words is refused; it would be as none at all, by which rows see every drafted token up to their own."""
+    for words in (1, 16):
+        q4._mask(torch.zeros(3, words, dtype=torch.int64), 3, -1)
+    with pytest.raises(ValueError, match="words"):
+        q4._mask(torch.zeros(3, 0, dtype=torch.int64), 3, -1)
