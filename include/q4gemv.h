@@ -761,7 +761,9 @@ Q4_API size_t q4_attention_workspace_most(const q4_kv_cache* cache, int q_heads,
  *            itself: the place a token of a path has.  The mask alone decides about
  *            new tokens.
  * Everything else, workspace and limits included, as in q4_attention_paged.  With the
- * mask of a chain the rows see what they see there.
+ * mask of a chain the rows see what they see there; where a window is shorter than the
+ * chain, with the mask that leaves out the new tokens in front of each row's last
+ * `window` ones (a row that sees so many has no cached key in its window).
  */
 Q4_API q4_status q4_attention_tree(const q4_kv_cache* cache, const q4_kv_batch* batch, const q4_heads* q,
                                    const q4_heads* out, const uint64_t* mask, int mask_words, float* lse, int q_heads,

@@ -1155,8 +1155,8 @@ def q4_attention_tree(cache: KVCache, batch: KVBatch, q: torch.Tensor, mask: tor
                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q4_attention_paged for drafted trees: each new token sees the cached keys before its sequence's new ones (with
     window > 0 those from past + depth - window + 1 on, depth: the new tokens it sees beside itself) and the new tokens
-    whose bits its mask has (int64 [T, words], bit j % 64 of word j / 64: the sequence's j-th; KVStep.mask).  Append
-    the new tokens first.  out, lse, workspace as there (attention_tree_workspace_bytes)."""
+    whose bits its mask has (int64 [T, words], bit j % 64 of word j / 64: the sequence's j-th; KVStep.mask), whatever the
+    window: paths longer than it need masks without the tokens outside of it.  Append the new tokens first.  out, lse, workspace as there (attention_tree_workspace_bytes)."""
     on = _on(cache.gpu, stream)
     if on is not None:
         with on:
