@@ -1,6 +1,6 @@
-// Attention of many new tokens a sequence: the kernel of items of 64 or 128 rows and
-// its launches (attn_tile.hip has what they compute, how, and what it measured;
-// attn_tree_tile.hip has them over trees of new tokens).
+// Attention of many new tokens a sequence: the kernel of items of 64, 128 or, of trees,
+// 256 rows (half of them a workgroup) and its launches (attn_tile.hip has what they
+// compute, how, and what it measured; attn_tree_tile.hip has them over trees of new tokens).
 #pragma once
 
 #include "attn_device.h"
