@@ -24,9 +24,9 @@
 // Measured, 32 query heads over 8 of 128, a call: 16 ragged sequences of up to 33 tokens
 // over up to 6001 keys 74 us (3.1 TB/s of keys and values; the matrix products of rows
 // that are there take 20, HBM 32 at 7.2 TB/s; a workgroup has about 1.5 items of 27
-// tiles, whose start and end, some 8 us, nothing hides), 3 of 64 over 32768 keys 139
-// to 142 (735 TFLOP/s; 88 at the rate of a large product), one of 16 tokens over 515 keys of
-// 40 heads 10.2 (latency).
+// tiles, whose start and end, some 8 us, nothing hides), 3 of 64 over 32768 keys 140
+// (738 TFLOP/s; 792 in the kernel; 88 us at the rate of a large product), one of 16 tokens
+// over 515 keys of 40 heads 10.1 (latency).
 // Tried: four tiles of K and of V in LDS for 8 waves instead of two (71 and 141 us, as
 // before: not the loads are what is waited for); weights summed a step after they are
 // packed (no change).

@@ -18,7 +18,7 @@
 // joining in the first one would need counters that are zero before every call.
 //
 // Bound by memory in large batches: 192 rows of 151936 binary32 logits, each with up to
-// 4096 tokens and 300 biases, read and written in 52 us of kernel time (4.5 TB/s; a
+// 4096 tokens and 300 biases, read and written in 51 us of kernel time (4.6 TB/s; a
 // copy of them takes 45, the bare pick with its copy 46).  Bound by latency in small
 // ones: the sequence, its lengths, the lists and the counts follow each other, 4.9 us for
 // one row, 13 for 37 rows of trees, and 2 to 4 for the second launch.  What made the

@@ -2,8 +2,8 @@
 // and the cache's slots closed up behind it (gfx950).  Whole numbers and copies:
 // bound by latency, so each is one launch whose workgroups need nothing from each
 // other.  Measured (an empty launch is 3.8 us): tables of 8 sequences of a token 3.8 us,
-// of 256 trees of up to 64 tokens over 16384 6.0; the path through a tree of 16 2.5, 48
-// through trees of up to 48 6.1; their slots in 36 layers' caches 6.5.
+// of 256 trees of up to 64 tokens over 16384 5.9; the path through a tree of 16 2.5, 48
+// through trees of up to 48 6.0; their slots in 36 layers' caches 6.5.
 #include "kv_device.h"
 #include "step_launch.h"
 
